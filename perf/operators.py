@@ -291,8 +291,8 @@ def _plain_beam(s):
     x = torch.where(x.isnan(), -math.inf, x).clamp(max=torch.finfo(s["logits"].dtype).max)
     top = x.amax(1, keepdim=True)
     top = torch.where(top.isinf(), 0.0, top)
-    lse = top + (x - top).exp().sum(1, keepdim=True).log()
-    logp = torch.where(x.isinf(), -math.inf, x - lse)
+    x = x - top
+    logp = torch.where(x.isinf(), -math.inf, x - x.exp().sum(1, keepdim=True).log())
     flat = (s["scores"].double()[..., None] + logp.view(b, w, v)).view(b, w * v)
     # the k largest, ties to the lowest index: what is above the k-th value, then its equals in order
     kth = flat.topk(k).values[:, -1:]
