@@ -13,6 +13,12 @@
  *                            mixes chunked-prefill requests (many query tokens on
  *                            a cached prefix, causal within the chunk) and decode
  *                            requests (one query token).
+ * Around it stand the operators that turn one step's results into the next step's
+ * inputs, all on the device, so that a whole decoding step can be one CUDA graph:
+ *   4. pa_rotary_and_cache   rotary positions of q and k, and the write of 1. in one pass;
+ *   5. pa_beam_select        the best continuations of every sequence's beams;
+ *   6. pa_fork_blocks, pa_append_blocks, pa_release_blocks   block tables, reference
+ *                            counts and slots of sequences that branch, grow and end.
  *
  * Sources, cited by key:
  *   [AGENTIC] "宣稱省下 106 倍成本：vLLM 怎麼把 Serving 系統校準給 Agentic Workload"
@@ -140,6 +146,9 @@ typedef enum pa_dtype {
  * entry differs from the group's first member on a block declared shared.  The
  * output is unaffected: that member read its own block. */
 #define PA_ERRFLAG_SHARED_MISMATCH 0x20u
+#define PA_ERRFLAG_PARENT 0x40u    /* pa_fork_blocks: a parent >= num_parents */
+#define PA_ERRFLAG_POOL 0x80u      /* pa_append_blocks: fewer free blocks than the call needs */
+#define PA_ERRFLAG_REF_COUNT 0x100u /* a block in use whose reference count is below 1 */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* pa_status_string(pa_status status);
@@ -206,6 +215,178 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_cache
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_mapping, int32_t num_pairs,
                          int32_t num_blocks, int32_t num_kv_heads, int32_t head_size, int32_t block_size,
                          pa_dtype cache_dtype, pa_stream_t stream);
+
+/*
+ * Rotary frequencies (HOST: writes host memory, needs no device).  [NOTES] "Prefill 与
+ * Decode": every new token's q and k carry its position; rotary positions turn pair i
+ * of a head by position x inv_freq[i].  With R = rotary_dim and f_i = base^(-2i/R):
+ *   PA_ROTARY_UNSCALED  inv_freq[i] = f_i
+ *   PA_ROTARY_LINEAR    f_i / factor (positions squeezed into the trained range)
+ *   PA_ROTARY_NTK       base replaced by base x factor^(R / (R - 2)) (R >= 4)
+ *   PA_ROTARY_BY_PARTS  by the turns r_i = original_max_position x f_i / 2 pi that a pair
+ *                       makes over the trained range: pairs with r_i >= high_turns keep
+ *                       f_i, those with r_i <= low_turns get f_i / factor, a linear ramp
+ *                       in r_i mixes the two between.  0 <= low_turns < high_turns.
+ *   inv_freq     host, [rotary_dim / 2], computed in fp64 and rounded once
+ *   attn_factor  host, one float or NULL: 0.1 ln(factor) + 1 for PA_ROTARY_BY_PARTS (pass
+ *                it to pa_rotary_and_cache, or 1 where the model wants none), else 1
+ *   rotary_dim   even, >= 2; factor >= 1 (unused, like the last three, where the kind of
+ *                scaling does not name it)
+ */
+typedef enum pa_rotary_scaling {
+  PA_ROTARY_UNSCALED = 0,
+  PA_ROTARY_LINEAR = 1,
+  PA_ROTARY_NTK = 2,
+  PA_ROTARY_BY_PARTS = 3
+} pa_rotary_scaling;
+
+pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rotary_dim, double base,
+                                pa_rotary_scaling scaling, double factor, double original_max_position,
+                                double low_turns, double high_turns);
+
+/*
+ * pa_rotary_and_cache -- rotate the new tokens' q and k by their positions and write
+ * k and v into the paged cache: pa_reshape_and_cache with the rotation fused into it.
+ *
+ *   With theta = positions[t] x inv_freq[i], c = attn_factor cos theta and
+ *   s = attn_factor sin theta, pair i < R/2 of every q and k head becomes
+ *   (x c - y s, y c + x s).  Pairs are elements (i, i + R/2), or (2i, 2i + 1) where
+ *   interleaved != 0; elements from R = rotary_dim on stay as they are, and so does v.
+ *   theta is formed exactly (64-bit fixed point turns), so every int32 position is
+ *   served, negative ones too; the rotation runs in fp32 and its result is rounded
+ *   once: q to q_out, k to the cache (FP8 and NVFP4: quantised from fp32 by the rules of
+ *   pa_reshape_and_cache, not from k rounded to src_dtype).
+ *
+ *   q_out        [num_tokens] rows of num_q_heads x head_size, src_dtype (written)
+ *   q, key, value  rows of num_q_heads (key, value: num_kv_heads) x head_size, src_dtype
+ *   *_stride     elements from one token's row to the next, >= the row (unused for one
+ *                token): slices of one [num_tokens][q + k + v] projection are served as
+ *                they are.  q_out may be q itself (same stride); otherwise nothing that is
+ *                written may overlap anything that is read
+ *   positions    int32 [num_tokens]
+ *   slot_mapping int64 [num_tokens], as pa_reshape_and_cache; a token with a negative
+ *                slot is padding and one with a slot out of range an error
+ *                (PA_ERRFLAG_SLOT): neither its q_out row nor the cache is written
+ *   inv_freq     device, float [rotary_dim / 2]
+ *   num_q_heads  0 leaves q out (q and q_out may be NULL)
+ *   rotary_dim   even, 2 .. head_size; attn_factor positive and finite
+ *   the rest as pa_reshape_and_cache; q, q_out, key and value need only their element's
+ *   alignment.  Where they are 16-byte aligned with strides to match, and the rotated
+ *   part is whole 16-byte pieces (16 elements for FP8 and NVFP4 caches; per half for
+ *   pairs (i, i + R/2)), rows move in 16-byte pieces, else element by element.
+ */
+pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                              void* v_cache, const int32_t* positions, const int64_t* slot_mapping,
+                              const float* inv_freq, int32_t num_tokens, int32_t num_blocks, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_size, int32_t rotary_dim, int32_t block_size,
+                              int32_t interleaved, float attn_factor, int64_t q_out_stride, int64_t q_stride,
+                              int64_t key_stride, int64_t value_stride, pa_dtype src_dtype, pa_dtype cache_dtype,
+                              const float* k_scale, const float* v_scale, pa_stream_t stream);
+
+/*
+ * pa_beam_select -- beam search's step over beams and vocabulary.
+ * A candidate is (beam w, token v) of a sequence; its score is
+ *   beam_scores[w] + logits[w][v] - log sum_u exp(logits[w][u]),
+ * and the num_candidates best of each sequence's num_beams x vocab_size come back, best
+ * first.  Scores are compared in fp64 (the sums of exponentials are held in fp32 and joined
+ * in fp64); equal ones go to the lower beam, within it to the larger logit, then to the
+ * lower token.
+ *
+ *   out_scores   float [num_seqs][num_candidates]
+ *   out_tokens   int32 [num_seqs][num_candidates]
+ *   out_parents  int32 [num_seqs][num_candidates], the beam's row: sequence x num_beams + w,
+ *                as pa_fork_blocks takes it where row r of the tables belongs to beam r
+ *   logits       [num_seqs x num_beams] rows of vocab_size, row_stride elements apart
+ *                (>= vocab_size; unused for one row), fp32, f16 or bf16
+ *   beam_scores  float [num_seqs][num_beams]
+ * Masked logits are -inf and are never selected.  A NaN logit counts as -inf and +inf as
+ * the type's largest finite value.  A beam whose score is -inf or NaN (one that has
+ * ended, or does not exist yet) gives no candidates.  Where a sequence has fewer
+ * candidates than num_candidates, the rest are score -inf, token -1, parent -1.
+ *   num_candidates 1 .. PA_MAX_BEAM_CANDIDATES (num_beams, or twice that where some may
+ *                end); num_beams <= PA_MAX_BEAMS; num_seqs x num_beams <= 65535
+ *   workspace    >= pa_beam_select_workspace_size(...) bytes, 256-byte aligned; contents
+ *                need no initialisation
+ * The outputs must not overlap the inputs.
+ */
+#define PA_MAX_BEAM_CANDIDATES 32
+#define PA_MAX_BEAMS 1024
+
+size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,
+                                     int32_t num_candidates);
+pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_parents, const void* logits,
+                         int64_t row_stride, const float* beam_scores, int32_t num_seqs, int32_t num_beams,
+                         int32_t vocab_size, int32_t num_candidates, pa_dtype logits_dtype, void* workspace,
+                         size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * Pages of sequences.  [AGENTIC] "統一分頁 + 共用池": sequences draw their blocks from one
+ * pool, share them by reference counts and copy a shared one before they write into it.
+ * The three calls below keep that state in device arrays of the caller:
+ *   ref_counts   int32 [num_blocks]: how many table rows hold the block; 0 = free
+ *   block_tables int32 [rows][max_blocks_per_seq], seq_lens int32 [rows] (0 = no sequence)
+ * A row holds its first ceil(seq_len / block_size) entries.  A negative entry is a block
+ * released before a sliding window: it is carried along and never counted.  An entry >=
+ * num_blocks sets PA_ERRFLAG_BLOCK_TABLE and is never counted.  A length below 0 or above
+ * max_blocks_per_seq x block_size sets PA_ERRFLAG_SEQ_LEN.  Entries behind a row's blocks
+ * are neither read nor written.  Block numbers handed out depend on the arrays alone.  Calls
+ * that share ref_counts must be ordered (one stream, or events between streams).
+ *
+ * pa_fork_blocks -- children take their parents' blocks and lengths: row i of
+ * block_tables_out and seq_lens_out becomes a copy of row parents[i], and every block of it
+ * counts one holder more.  Samples and subagents of one prompt, and the reordering of
+ * beams: fork the chosen parents into a second pair of arrays, then release the first.
+ *   parents      int32 [num_children]; a negative parent leaves child i empty (length 0), one
+ *                >= num_parents does too and sets PA_ERRFLAG_PARENT
+ *   block_tables_out, seq_lens_out must not overlap block_tables, seq_lens (they may be other
+ *   rows of the same arrays); overlapping ranges are PA_ERR_INVALID_ARG.  What a child row
+ *   held before is overwritten, not released.
+ */
+pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* parents, int32_t* ref_counts,
+                         int32_t num_children, int32_t num_parents, int32_t max_blocks_per_seq, int32_t num_blocks,
+                         int32_t block_size, pa_stream_t stream);
+
+/*
+ * pa_append_blocks -- make room for the next tokens of every sequence: blocks, slots, and
+ * the copies that shared tails need.  Row i gains query_start_loc[i+1] - query_start_loc[i]
+ * tokens (0 leaves it as it is).  Rows are served in order, each like this: where the row's
+ * last block is partly filled and has other holders, a free block takes its place (counts
+ * move along) and block_mapping[i] = (old, new); then blocks are added until the new tokens
+ * fit.  So of rows that share a tail, all copy but the last, and that one too where others
+ * than these rows hold it.  Free blocks are handed out by ascending number.
+ *
+ *   block_tables, seq_lens, ref_counts  updated; seq_lens[i] then counts the new tokens
+ *   query_start_loc int32 [num_seqs + 1], as pa_varlen_attn
+ *   slot_mapping    int64 [total_q_tokens] (written): the new tokens' slots
+ *   block_mapping   int64 [num_seqs][2] (written): the copies to be made by pa_copy_blocks,
+ *                   in every layer, before the new tokens are written; (0, 0), a no-op
+ *                   there, for rows without one
+ *   workspace       >= pa_append_workspace_size(...) bytes, 256-byte aligned; contents need
+ *                   no initialisation
+ * All or nothing: where the pool has fewer free blocks than the call needs (PA_ERRFLAG_POOL),
+ * or an input is out of range (PA_ERRFLAG_QUERY, _SEQ_LEN; _BLOCK_TABLE or _REF_COUNT for a
+ * partly filled last block), tables, lengths and counts stay as they were, every slot is -1
+ * and every pair (0, 0), so that the calls that follow write nothing.  [LINEAGE]: running
+ * out of memory is handled at admission, never while writing KV.
+ */
+size_t pa_append_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t block_size);
+pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32_t* query_start_loc,
+                           int64_t* slot_mapping, int64_t* block_mapping, int32_t* ref_counts, int32_t num_seqs,
+                           int32_t total_q_tokens, int32_t max_blocks_per_seq, int32_t num_blocks,
+                           int32_t block_size, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_release_blocks -- give up the ends of sequences, or all of them: row i keeps its first
+ * keep_lens[i] tokens (keep_lens NULL: none), the blocks behind them lose one holder, and
+ * seq_lens[i] becomes the kept length.  A row no longer than keep_lens[i] stays as it is, so
+ * releasing twice is harmless; a negative keep_lens[i] sets PA_ERRFLAG_SEQ_LEN and leaves the
+ * row as it is.  Table entries are not changed.  A block whose count is already 0 stays at 0
+ * and sets PA_ERRFLAG_REF_COUNT.
+ */
+pa_status pa_release_blocks(const int32_t* block_tables, int32_t* seq_lens, const int32_t* keep_lens,
+                            int32_t* ref_counts, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_blocks,
+                            int32_t block_size, pa_stream_t stream);
 
 /*
  * Context tokens per split-K partition that pa_decode / pa_varlen_attn use when
@@ -455,7 +636,9 @@ pa_status pa_get_error_flags(uint32_t* flags, int32_t clear, pa_stream_t stream)
  * run beside them), 5 = shared-prefix tiles, 6 = the span of the shared-prefix
  * and private-remainder kernels of pa_decode_shared_prefix, 7 = copy_blocks,
  * 8 = the span of the single-token-row and multi-token-row kernels of
- * pa_varlen_attn, which run concurrently on two streams),
+ * pa_varlen_attn, which run concurrently on two streams, 9 = rotary_and_cache,
+ * 10 = beam_select (its kernels together), 11 = fork_blocks, 12 = append_blocks,
+ * 13 = release_blocks),
  * returns the launch count and the summed device milliseconds since the last
  * reset (reset != 0 clears every kind).
  * Tracing is off by default and costs nothing when off.  Not thread-safe.

@@ -24,7 +24,7 @@ Sources cited by key in the docstrings of this package:
            (ai.youdonthavefriends.com, llm/ai/deep-analysis/2026/08/08/vllm-architecture).
 
 Parity status: every public function here is pinned by a ``-m "not gpu"`` test
-in ``tests/test_oracle_pins.py`` against values the pages print, closed forms,
+in ``tests/test_oracle_pins.py`` (``decoding_step.py``: ``tests/test_decoding_oracle.py``) against values the pages print, closed forms,
 invariants, an independent library routine or brute force.  No function is
 "parity unpinned".
 """
@@ -65,4 +65,12 @@ from .paged_attention import (  # noqa: F401
     softmax_partial,
     softmax_weights,
     query_positions,
+)
+from .decoding_step import (  # noqa: F401
+    append_blocks,
+    beam_select,
+    fork_blocks,
+    release_blocks,
+    rotary_frequencies,
+    rotate,
 )

@@ -39,19 +39,35 @@ PA_ERRFLAG_BLOCK_TABLE, PA_ERRFLAG_SLOT, PA_ERRFLAG_SEQ_LEN, PA_ERRFLAG_QUERY, P
     0x1, 0x2, 0x4, 0x8, 0x10
 # diagnostic only: a declared shared block differed for some member (the output is unaffected)
 PA_ERRFLAG_SHARED_MISMATCH = 0x20
+PA_ERRFLAG_PARENT, PA_ERRFLAG_POOL, PA_ERRFLAG_REF_COUNT = 0x40, 0x80, 0x100
+PA_MAX_BEAM_CANDIDATES, PA_MAX_BEAMS = 32, 1024
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 # Names of the kernel kinds reported by pa_trace_read.
 TRACE_KINDS = ("reshape_and_cache", "attention", "merge", "varlen_plan", "prefill_tiles", "shared_prefix",
-               "shared_span", "copy_blocks", "varlen_span")
+               "shared_span", "copy_blocks", "varlen_span", "rotary_and_cache", "beam_select", "fork_blocks",
+               "append_blocks", "release_blocks")
 
 # Every symbol include/pa.h declares, with its ctypes signature.
 _P, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_D = ctypes.c_double
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "pa_version": (_I32, []),
     "pa_reshape_and_cache": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                             ctypes.c_int, ctypes.c_int, _P, _P, _P]),
     "pa_copy_blocks": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, ctypes.c_int, _P]),
+    "pa_rotary_frequencies": (ctypes.c_int, [ctypes.POINTER(_F), ctypes.POINTER(_F), _I32, _D, ctypes.c_int, _D, _D,
+                                             _D, _D]),
+    "pa_rotary_and_cache": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                           _I32, _I32, _F, _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                           _P, _P, _P]),
+    "pa_beam_select_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "pa_beam_select": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, ctypes.c_int, _P, _SZ, _P]),
+    "pa_fork_blocks": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P]),
+    "pa_append_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "pa_append_blocks": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
+    "pa_release_blocks": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "pa_default_partition_size": (_I32, [_I32, _I32, _I32, _I32]),
     "pa_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
     "pa_decode": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
@@ -188,6 +204,183 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
     n = block_mapping.shape[0]
     _check(_lib.pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_mapping) if n else None, n, nb, hkv, d,
                                bs, kv_code(k_cache), _stream(stream)), "pa_copy_blocks")
+
+
+def _device_call(fn, where, tensors, args, stream):
+    """Call fn(*args, stream) on the tensors' device: the current stream of that device, or
+    the caller's, which has to belong to it."""
+    index = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{where}: expected CUDA tensors")
+        if index is None:
+            index = d
+        elif d != index:
+            raise ValueError(f"{where}: the tensors are on different devices")
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"{where}: the stream belongs to another device than the tensors")
+    s = stream if stream is not None else torch.cuda.current_stream(index)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, s.cuda_stream)
+    if st != PA_OK:
+        raise PAError(st, where)
+
+
+def _int32(t, shape, what):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, what):
+    """(pointer, elements between tokens) of a [tokens][heads][head_size] tensor whose heads
+    are contiguous; tokens may be any distance apart."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what} must be [num_tokens][heads][head_size] with contiguous heads")
+    return t.data_ptr(), t.stride(0)
+
+
+def pa_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_max_position=0.0,
+                          low_turns=1.0, high_turns=32.0, device=None):
+    """(inv_freq, attn_factor) for pa_rotary_and_cache: a float32 tensor [rotary_dim/2] on
+    ``device`` (default: the current CUDA device) and the factor on the rotated values.
+    scaling: "none", "linear", "ntk" or "by_parts" (see pa.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    host = (ctypes.c_float * max(1, int(rotary_dim) // 2))()
+    attn = ctypes.c_float(1.0)
+    _check(_lib.pa_rotary_frequencies(host, ctypes.byref(attn), int(rotary_dim), float(base),
+                                      ROTARY_SCALINGS[scaling], float(factor), float(original_max_position),
+                                      float(low_turns), float(high_turns)), "pa_rotary_frequencies")
+    return torch.tensor(list(host), dtype=torch.float32, device=device or "cuda"), float(attn.value)
+
+
+def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
+                        interleaved=False, attn_factor=1.0, k_scale=None, v_scale=None, stream=None) -> None:
+    """Rotate q [T][Hq][d] into q_out (which may be q) and key [T][Hkv][d] by positions (int32
+    [T]), and write key and value into the paged caches at slot_mapping (int64 [T]; a negative
+    slot skips the token).  inv_freq float32 [rotary_dim/2].  q, key and value may be slices of
+    one projection (any distance between tokens).  q and q_out None: keys only."""
+    nb, hkv, bs, d = cache_geometry(k_cache, v_cache, key.shape[-1])
+    t = key.shape[0]
+    k_ptr, k_stride = _rows(key, "key")
+    v_ptr, v_stride = _rows(value, "value")
+    if tuple(key.shape) != (t, hkv, d) or value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("key/value must be [num_tokens][num_kv_heads][head_size] of one dtype")
+    hq = 0
+    q_ptr = qo_ptr = None
+    q_stride = qo_stride = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or tuple(q.shape) != (t, q.shape[1], d) or q_out.shape != q.shape or \
+                q.dtype != key.dtype or q_out.dtype != q.dtype:
+            raise ValueError("q/q_out must be [num_tokens][num_q_heads][head_size] of key's dtype")
+        hq = q.shape[1]
+        q_ptr, q_stride = _rows(q, "q")
+        qo_ptr, qo_stride = _rows(q_out, "q_out")
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (t,) or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 tensor [num_tokens]")
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float32 tensor [rotary_dim/2]")
+    pos_ptr = _int32(positions, (t,), "positions")
+    code = kv_code(k_cache, k_scale)
+    for sc in (k_scale, v_scale):
+        if sc is not None and (sc.dtype != torch.float32 or sc.numel() not in (1, hkv)):
+            raise ValueError("scales: float32, one per tensor or one per KV head")
+    if code in (PA_FP8_E4M3_PER_HEAD, PA_FP8_E5M2_PER_HEAD, PA_NVFP4_PER_HEAD) and \
+            (v_scale is None or v_scale.numel() != k_scale.numel()):
+        raise ValueError("k_scale and v_scale must both hold one value per KV head")
+    _device_call(_lib.pa_rotary_and_cache, "pa_rotary_and_cache",
+                 (key, value, q, q_out, k_cache, v_cache, positions, slot_mapping, inv_freq, k_scale, v_scale),
+                 (qo_ptr, q_ptr, k_ptr, v_ptr, _ptr(k_cache), _ptr(v_cache), pos_ptr, slot_mapping.data_ptr(),
+                  inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.numel(), bs, 1 if interleaved else 0,
+                  float(attn_factor), qo_stride, q_stride, k_stride, v_stride, dtype_code(key), code, _ptr(k_scale),
+                  _ptr(v_scale)), stream)
+
+
+def pa_beam_select_workspace_size(num_seqs, num_beams, vocab_size, num_candidates) -> int:
+    return _lib.pa_beam_select_workspace_size(num_seqs, num_beams, vocab_size, num_candidates)
+
+
+def pa_beam_select(out_scores, out_tokens, out_parents, logits, beam_scores, workspace, stream=None) -> None:
+    """The best candidates of each sequence's beams: out_scores float32, out_tokens and
+    out_parents int32, all [num_seqs][num_candidates]; logits [num_seqs*num_beams][vocab]
+    (rows may be padded), beam_scores float32 [num_seqs][num_beams]."""
+    if beam_scores.dtype != torch.float32 or beam_scores.dim() != 2 or not beam_scores.is_contiguous():
+        raise ValueError("beam_scores must be a contiguous float32 tensor [num_seqs][num_beams]")
+    b, w = beam_scores.shape
+    if logits.dim() != 2 or logits.shape[0] != b * w or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [num_seqs*num_beams][vocab_size] with contiguous rows")
+    if out_scores.dim() != 2 or out_scores.shape[0] != b or out_scores.dtype != torch.float32 or \
+            not out_scores.is_contiguous():
+        raise ValueError("out_scores must be a contiguous float32 tensor [num_seqs][num_candidates]")
+    shape = tuple(out_scores.shape)
+    _device_call(_lib.pa_beam_select, "pa_beam_select",
+                 (logits, beam_scores, out_scores, out_tokens, out_parents, workspace),
+                 (out_scores.data_ptr(), _int32(out_tokens, shape, "out_tokens"),
+                  _int32(out_parents, shape, "out_parents"), logits.data_ptr(), logits.stride(0),
+                  beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits), _ptr(workspace),
+                  workspace.numel() * workspace.element_size()), stream)
+
+
+def pa_fork_blocks(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts, block_size,
+                   stream=None) -> None:
+    """Children rows take the blocks and lengths of rows ``parents`` (int32 [children];
+    negative: an empty row) of block_tables/seq_lens; ref_counts int32 [num_blocks] counts
+    the holders of every block.  See pa.h."""
+    if block_tables.dim() != 2 or parents.dim() != 1 or ref_counts.dim() != 1:
+        raise ValueError("block_tables [rows][max_blocks_per_seq], parents [children], ref_counts [num_blocks]")
+    m, width = block_tables.shape
+    n = parents.numel()
+    _device_call(_lib.pa_fork_blocks, "pa_fork_blocks",
+                 (block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts),
+                 (_int32(block_tables_out, (n, width), "block_tables_out"), _int32(seq_lens_out, (n,), "seq_lens_out"),
+                  _int32(block_tables, (m, width), "block_tables"), _int32(seq_lens, (m,), "seq_lens"),
+                  _int32(parents, (n,), "parents"), _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n, m,
+                  width, ref_counts.numel(), int(block_size)), stream)
+
+
+def pa_append_workspace_size(num_seqs, total_q_tokens, block_size) -> int:
+    return _lib.pa_append_workspace_size(num_seqs, total_q_tokens, block_size)
+
+
+def pa_append_blocks(block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping, ref_counts, block_size,
+                     workspace, stream=None) -> None:
+    """Room for the next tokens of every row (query_start_loc int32 [rows+1]): blocks from the
+    pool, slots (int64 [new tokens]) and copy-on-write pairs (block_mapping int64 [rows][2],
+    for pa_copy_blocks).  All or nothing; see pa.h."""
+    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+        raise ValueError("block_tables [rows][max_blocks_per_seq], ref_counts [num_blocks]")
+    n, width = block_tables.shape
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 tensor [total_q_tokens]")
+    if block_mapping.dtype != torch.int64 or tuple(block_mapping.shape) != (n, 2) or not block_mapping.is_contiguous():
+        raise ValueError("block_mapping must be a contiguous int64 tensor [rows][2]")
+    _device_call(_lib.pa_append_blocks, "pa_append_blocks",
+                 (block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping, ref_counts, workspace),
+                 (_int32(block_tables, (n, width), "block_tables"), _int32(seq_lens, (n,), "seq_lens"),
+                  _int32(query_start_loc, (n + 1,), "query_start_loc"), slot_mapping.data_ptr(),
+                  block_mapping.data_ptr(), _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n,
+                  slot_mapping.numel(), width, ref_counts.numel(), int(block_size), _ptr(workspace),
+                  workspace.numel() * workspace.element_size()), stream)
+
+
+def pa_release_blocks(block_tables, seq_lens, ref_counts, block_size, keep_lens=None, stream=None) -> None:
+    """Give up what lies behind the first keep_lens (int32 [rows]; None: 0) tokens of every row:
+    the blocks lose a holder and seq_lens is cut.  See pa.h."""
+    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+        raise ValueError("block_tables [rows][max_blocks_per_seq], ref_counts [num_blocks]")
+    n, width = block_tables.shape
+    _device_call(_lib.pa_release_blocks, "pa_release_blocks", (block_tables, seq_lens, ref_counts, keep_lens),
+                 (_int32(block_tables, (n, width), "block_tables"), _int32(seq_lens, (n,), "seq_lens"),
+                  None if keep_lens is None else _int32(keep_lens, (n,), "keep_lens"),
+                  _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n, width, ref_counts.numel(),
+                  int(block_size)), stream)
 
 
 def pa_default_partition_size(num_seqs, num_kv_heads, max_seq_len, block_size) -> int:

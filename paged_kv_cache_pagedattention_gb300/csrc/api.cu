@@ -289,7 +289,7 @@ bool cache_maps(CUtensorMap* tk, CUtensorMap* tv, const void* k_cache, const voi
 
 // ------------------------------------------------------------------ tracing
 
-constexpr int kTraceKinds = 9;
+constexpr int kTraceKinds = 14;
 bool g_trace_on = false;
 struct TraceSlot {
   int kind;
@@ -452,6 +452,61 @@ AttnParams base_params(void* out, const void* q, const void* k_cache, const void
   return p;  // part / part_pf / part_shared are set by the caller
 }
 
+struct BeamLayout {
+  int segment, segments;
+  size_t state_off, keys_off, total;
+};
+
+BeamLayout beam_layout(int num_seqs, int num_beams, int vocab_size, int num_candidates) {
+  BeamLayout L;
+  const long long rows = (long long)num_seqs * num_beams;
+  L.segment = pa::beam_segment(rows, vocab_size);
+  L.segments = static_cast<int>(ceil_div(vocab_size, L.segment));
+  const size_t parts = (size_t)rows * L.segments;
+  L.state_off = 0;
+  L.keys_off = align256(parts * sizeof(float2));
+  L.total = L.keys_off + align256(parts * num_candidates * sizeof(unsigned long long));
+  return L;
+}
+
+struct AppendLayout {
+  size_t tail_off, need_off, first_off, fresh_off, total;
+};
+
+// Per row its shared tail, its need and where that starts; then the blocks given out: at
+// most one copy and one part-filled block a row, and the full blocks of the new tokens.
+AppendLayout append_layout(int num_seqs, int total_q, int block_size) {
+  AppendLayout L;
+  const size_t rows = align256((size_t)num_seqs * sizeof(int32_t));
+  L.tail_off = 0;
+  L.need_off = rows;
+  L.first_off = 2 * rows;
+  L.fresh_off = 3 * rows;
+  L.total = L.fresh_off + align256((2 * (size_t)num_seqs + total_q / block_size) * sizeof(int32_t));
+  return L;
+}
+
+pa::SequenceParams sequence_params(int32_t* block_tables, int32_t* seq_lens, int32_t* ref_counts, int32_t num_rows,
+                                   int32_t max_blocks_per_seq, int32_t num_blocks, int32_t block_size) {
+  pa::SequenceParams p;
+  memset(&p, 0, sizeof(p));
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.ref_counts = ref_counts;
+  p.err = error_word();
+  p.num_rows = num_rows;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  return p;
+}
+
+// Whether two byte ranges share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
 }  // namespace
 
 namespace pa {
@@ -491,7 +546,7 @@ const char* pa_status_string(pa_status status) {
   }
 }
 
-int32_t pa_version(void) { return 100; }
+int32_t pa_version(void) { return 200; }
 
 pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_cache, void* v_cache,
                                const int64_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
@@ -560,6 +615,221 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_mapp
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   TraceScope t(7, s);
   return cuda_status(pa::launch_copy_blocks(p, s));
+}
+
+pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rotary_dim, double base,
+                                pa_rotary_scaling scaling, double factor, double original_max_position,
+                                double low_turns, double high_turns) {
+  if (!inv_freq || rotary_dim < 2 || rotary_dim % 2) return PA_ERR_INVALID_ARG;
+  if (!(base > 0.0) || !(base < INFINITY)) return PA_ERR_INVALID_ARG;
+  if (scaling != PA_ROTARY_UNSCALED && (!(factor >= 1.0) || !(factor < INFINITY))) return PA_ERR_INVALID_ARG;
+  double b = base;
+  switch (scaling) {
+    case PA_ROTARY_UNSCALED:
+    case PA_ROTARY_LINEAR: break;
+    case PA_ROTARY_NTK:
+      if (rotary_dim < 4) return PA_ERR_INVALID_ARG;  // the exponent R / (R - 2)
+      b = base * pow(factor, (double)rotary_dim / (rotary_dim - 2));
+      break;
+    case PA_ROTARY_BY_PARTS:
+      if (!(original_max_position > 0.0) || !(original_max_position < INFINITY) || !(low_turns < high_turns) ||
+          !(low_turns >= 0.0) || !(high_turns < INFINITY))
+        return PA_ERR_INVALID_ARG;
+      break;
+    default: return PA_ERR_UNSUPPORTED;
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = pow(b, -2.0 * i / rotary_dim);
+    if (scaling == PA_ROTARY_LINEAR) f /= factor;
+    if (scaling == PA_ROTARY_BY_PARTS) {
+      const double turns = original_max_position * f / 6.283185307179586476925;
+      const double keep = std::min(1.0, std::max(0.0, (turns - low_turns) / (high_turns - low_turns)));
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    inv_freq[i] = static_cast<float>(f);
+  }
+  if (attn_factor) *attn_factor = scaling == PA_ROTARY_BY_PARTS ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.f;
+  return PA_OK;
+}
+
+pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                              void* v_cache, const int32_t* positions, const int64_t* slot_mapping,
+                              const float* inv_freq, int32_t num_tokens, int32_t num_blocks, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_size, int32_t rotary_dim, int32_t block_size,
+                              int32_t interleaved, float attn_factor, int64_t q_out_stride, int64_t q_stride,
+                              int64_t key_stride, int64_t value_stride, pa_dtype src_dtype, pa_dtype cache_dtype,
+                              const float* k_scale, const float* v_scale, pa_stream_t stream) {
+  const int scale_stride = scale_stride_of(cache_dtype);
+  cache_dtype = base_dtype(cache_dtype);
+  if (num_tokens < 0 || num_blocks < 1 || num_q_heads < 0 || num_kv_heads < 1 || head_size < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_size) return PA_ERR_INVALID_ARG;
+  if (!(attn_factor > 0.f) || !(attn_factor < INFINITY)) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !positions || !slot_mapping || !inv_freq) return PA_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && (!q || !q_out)) return PA_ERR_INVALID_ARG;
+  if (src_dtype != PA_F32 && src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  const bool cache_scaled = scaled_dtype(cache_dtype);
+  if (cache_dtype != src_dtype && !cache_scaled) return PA_ERR_UNSUPPORTED;
+  if (cache_scaled && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  const long long eb = dtype_bytes(src_dtype);
+  if ((head_size * eb) % 16) return PA_ERR_UNSUPPORTED;
+  if (cache_dtype == PA_NVFP4 ? !nvfp4_shape_ok(head_size, block_size) : (head_size * dtype_bytes(cache_dtype)) % 16)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t q_width = (int64_t)num_q_heads * head_size, kv_width = (int64_t)num_kv_heads * head_size;
+  if (num_tokens > 1 && (key_stride < kv_width || value_stride < kv_width ||
+                         (num_q_heads > 0 && (q_stride < q_width || q_out_stride < q_width))))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && q == q_out && num_tokens > 1 && q_stride != q_out_stride) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key, eb) || !aligned(value, eb) ||
+      (num_q_heads > 0 && (!aligned(q, eb) || !aligned(q_out, eb))))
+    return PA_ERR_INVALID_ARG;
+  pa::RotaryParams p;
+  p.q_out = q_out;
+  p.q = q;
+  p.key = key;
+  p.value = value;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.inv_freq = inv_freq;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err = error_word();
+  p.q_out_stride = q_out_stride;
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.scale_stride = scale_stride;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.head_size = head_size;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.attn_factor = attn_factor;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(9, s);
+  return cuda_status(pa::launch_rotary(p, src_dtype, cache_dtype, s));
+}
+
+size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,
+                                     int32_t num_candidates) {
+  if (num_seqs < 1 || num_beams < 1 || vocab_size < 1 || num_candidates < 1) return 256;
+  return beam_layout(num_seqs, num_beams, vocab_size, num_candidates).total;
+}
+
+pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_parents, const void* logits,
+                         int64_t row_stride, const float* beam_scores, int32_t num_seqs, int32_t num_beams,
+                         int32_t vocab_size, int32_t num_candidates, pa_dtype logits_dtype, void* workspace,
+                         size_t workspace_bytes, pa_stream_t stream) {
+  if (num_seqs < 0 || num_beams < 1 || vocab_size < 1 || num_candidates < 1) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!out_scores || !out_tokens || !out_parents || !logits || !beam_scores || !workspace) return PA_ERR_INVALID_ARG;
+  if (logits_dtype != PA_F32 && logits_dtype != PA_F16 && logits_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (num_candidates > PA_MAX_BEAM_CANDIDATES) return PA_ERR_UNSUPPORTED;
+  const long long rows = (long long)num_seqs * num_beams;
+  if (rows > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_beams > PA_MAX_BEAMS) return PA_ERR_UNSUPPORTED;
+  if (rows > 1 && row_stride < vocab_size) return PA_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype_bytes(logits_dtype))) return PA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+  const BeamLayout L = beam_layout(num_seqs, num_beams, vocab_size, num_candidates);
+  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  pa::BeamParams p;
+  p.logits = logits;
+  p.beam_scores = beam_scores;
+  p.out_scores = out_scores;
+  p.out_tokens = out_tokens;
+  p.out_parents = out_parents;
+  p.state = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + L.state_off);
+  p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + L.keys_off);
+  p.row_stride = row_stride;
+  p.num_seqs = num_seqs;
+  p.num_beams = num_beams;
+  p.vocab_size = vocab_size;
+  p.num_candidates = num_candidates;
+  p.segment = L.segment;
+  p.num_segments = L.segments;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(10, s);
+  return cuda_status(pa::launch_beam_select(p, logits_dtype, s));
+}
+
+pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* parents, int32_t* ref_counts,
+                         int32_t num_children, int32_t num_parents, int32_t max_blocks_per_seq, int32_t num_blocks,
+                         int32_t block_size, pa_stream_t stream) {
+  if (num_children < 0 || num_parents < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (num_children == 0) return PA_OK;
+  if (!block_tables_out || !seq_lens_out || !parents || !ref_counts) return PA_ERR_INVALID_ARG;
+  if (num_parents > 0 && (!block_tables || !seq_lens)) return PA_ERR_INVALID_ARG;
+  const size_t row = (size_t)max_blocks_per_seq * sizeof(int32_t);
+  if (overlap(block_tables_out, num_children * row, block_tables, num_parents * row) ||
+      overlap(seq_lens_out, num_children * sizeof(int32_t), seq_lens, num_parents * sizeof(int32_t)))
+    return PA_ERR_INVALID_ARG;  // a child would overwrite a parent that another child still reads
+  pa::SequenceParams p = sequence_params(block_tables_out, seq_lens_out, ref_counts, num_children,
+                                         max_blocks_per_seq, num_blocks, block_size);
+  p.parent_tables = block_tables;
+  p.parent_lens = seq_lens;
+  p.parents = parents;
+  p.num_parents = num_parents;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(11, s);
+  return cuda_status(pa::launch_fork_blocks(p, s));
+}
+
+size_t pa_append_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t block_size) {
+  if (num_seqs < 1 || total_q_tokens < 0 || block_size < 1) return 256;
+  return append_layout(num_seqs, total_q_tokens, block_size).total;
+}
+
+pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32_t* query_start_loc,
+                           int64_t* slot_mapping, int64_t* block_mapping, int32_t* ref_counts, int32_t num_seqs,
+                           int32_t total_q_tokens, int32_t max_blocks_per_seq, int32_t num_blocks,
+                           int32_t block_size, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (num_seqs < 0 || total_q_tokens < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return total_q_tokens == 0 ? PA_OK : PA_ERR_INVALID_ARG;
+  if (!block_tables || !seq_lens || !query_start_loc || !block_mapping || !ref_counts || !workspace)
+    return PA_ERR_INVALID_ARG;
+  if (total_q_tokens > 0 && !slot_mapping) return PA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+  const AppendLayout L = append_layout(num_seqs, total_q_tokens, block_size);
+  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  pa::SequenceParams p =
+      sequence_params(block_tables, seq_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.query_start_loc = query_start_loc;
+  p.slot_mapping = slot_mapping;
+  p.block_mapping = block_mapping;
+  p.total_tokens = total_q_tokens;
+  p.ws_tail = reinterpret_cast<int32_t*>(ws + L.tail_off);
+  p.ws_need = reinterpret_cast<int32_t*>(ws + L.need_off);
+  p.ws_first = reinterpret_cast<int32_t*>(ws + L.first_off);
+  p.ws_fresh = reinterpret_cast<int32_t*>(ws + L.fresh_off);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(12, s);
+  return cuda_status(pa::launch_append_blocks(p, s));
+}
+
+pa_status pa_release_blocks(const int32_t* block_tables, int32_t* seq_lens, const int32_t* keep_lens,
+                            int32_t* ref_counts, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_blocks,
+                            int32_t block_size, pa_stream_t stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!block_tables || !seq_lens || !ref_counts) return PA_ERR_INVALID_ARG;
+  pa::SequenceParams p =
+      sequence_params(const_cast<int32_t*>(block_tables), seq_lens, ref_counts, num_seqs, max_blocks_per_seq,
+                      num_blocks, block_size);
+  p.keep_lens = keep_lens;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(13, s);
+  return cuda_status(pa::launch_release_blocks(p, s));
 }
 
 int32_t pa_default_partition_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len,

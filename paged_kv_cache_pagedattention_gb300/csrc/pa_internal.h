@@ -95,6 +95,84 @@ struct CopyParams {
 
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 
+// Rotary positions with the cache write.  Strides are in elements, between tokens.
+struct RotaryParams {
+  void* q_out;
+  const void* q;  // nullptr with num_q_heads == 0
+  const void* key;
+  const void* value;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* positions;
+  const int64_t* slot_mapping;
+  const float* inv_freq;  // [rotary_dim / 2]
+  const float* k_scale;   // FP8 / NVFP4: scale of KV head h at k_scale[h * scale_stride]
+  const float* v_scale;
+  unsigned* err;
+  long long q_out_stride, q_stride, key_stride, value_stride;
+  int scale_stride;
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_size;
+  int rotary_dim;
+  int interleaved;
+  int num_blocks;
+  int block_size;
+  float attn_factor;
+};
+
+cudaError_t launch_rotary(const RotaryParams& p, int src_dtype, int cache_dtype, cudaStream_t stream);
+
+struct BeamParams {
+  const void* logits;        // [num_seqs * num_beams][vocab_size], rows row_stride elements apart
+  const float* beam_scores;  // [num_seqs][num_beams]
+  float* out_scores;         // [num_seqs][num_candidates]
+  int32_t* out_tokens;
+  int32_t* out_parents;
+  float2* state;             // [rows][num_segments] (maximum, sum of exp against it)
+  unsigned long long* keys;  // [rows][num_segments][num_candidates] best logits, best first, 0 = none
+  long long row_stride;
+  int num_seqs;
+  int num_beams;
+  int vocab_size;
+  int num_candidates;
+  int segment;               // elements of a row that one block takes
+  int num_segments;
+};
+
+int beam_segment(long long rows, int vocab_size);
+cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream);
+
+// Pages of sequences.  Rows are the table rows a call changes; parents are pa_fork_blocks'.
+struct SequenceParams {
+  int32_t* block_tables;         // [num_rows][max_blocks_per_seq]
+  int32_t* seq_lens;             // [num_rows]
+  int32_t* ref_counts;           // [num_blocks]
+  const int32_t* parent_tables;  // fork: [num_parents][max_blocks_per_seq]
+  const int32_t* parent_lens;    // fork: [num_parents]
+  const int32_t* parents;        // fork: [num_rows]
+  const int32_t* keep_lens;      // release: [num_rows], or nullptr (keep nothing)
+  const int32_t* query_start_loc;  // append: [num_rows + 1]
+  int64_t* slot_mapping;         // append: [total_tokens]
+  int64_t* block_mapping;        // append: [num_rows][2]
+  int32_t* ws_tail;              // append scratch: [num_rows] each
+  int32_t* ws_need;
+  int32_t* ws_first;
+  int32_t* ws_fresh;             // append scratch: the blocks given out
+  unsigned* err;
+  int num_rows;
+  int num_parents;
+  int num_blocks;
+  int max_blocks_per_seq;
+  int block_size;
+  int total_tokens;
+};
+
+cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream);
+cudaError_t launch_append_blocks(const SequenceParams& p, cudaStream_t stream);
+cudaError_t launch_release_blocks(const SequenceParams& p, cudaStream_t stream);
+
 // pa_decode's argument checks on everything but the workspace (api.cu).
 pa_status check_decode_args(const void* out, const void* q, const void* k_cache, const void* v_cache,
                             int32_t num_blocks, const int32_t* block_tables, int32_t max_blocks_per_seq,

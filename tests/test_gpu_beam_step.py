@@ -1,0 +1,167 @@
+"""A whole beam search on the device with the library's calls together: append blocks, copy
+shared tails, rotate and write, attend, select, fork and release, as eager calls and as
+one captured graph replayed for the whole generation, against a dense fp64 beam search
+that knows no pages.  The model is one attention layer with random weights; the reference
+checks that no choice was closer than 1e-3, far above fp32's error, so tokens are equal."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+DEV = "cuda:0"
+VOCAB, E, HQ, HKV, D, ROT, BS = 97, 32, 4, 2, 64, 48, 16
+BEAMS, STEPS = 3, 20
+PROMPTS = [1, 2, 16, 17, 33, 48]
+LONGEST = max(PROMPTS) + STEPS
+
+
+def weights(seed=10):
+    rng = np.random.default_rng(seed)
+    f = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    return {"embed": f(VOCAB, E), "qkv": f(E, (HQ + 2 * HKV) * D) / 4, "out": f(HQ * D, VOCAB) / 3,
+            "skip": f(E, VOCAB) / 5, "freq": oracle.rotary_frequencies(ROT)[0].astype(np.float32),
+            "prompts": [rng.integers(0, VOCAB, n) for n in PROMPTS]}
+
+
+def dense_beam_search(w):
+    """Tokens [seq][beam][STEPS] and scores of the hypotheses, each attended from scratch."""
+    w64 = {k: v.astype(np.float64) for k, v in w.items() if k not in ("prompts", "freq")}
+    all_tokens, all_scores, gap = [], [], math.inf
+    for prompt in w["prompts"]:
+        beams = [(0.0, [int(t) for t in prompt])]
+        for _ in range(STEPS):
+            cands = []
+            for cum, toks in beams:
+                x = w64["embed"][toks]
+                q, k, v = np.split(x @ w64["qkv"], [HQ * D, (HQ + HKV) * D], axis=1)
+                pos = np.arange(len(toks))
+                q = oracle.rotate(q.reshape(-1, HQ, D), pos, w["freq"])[-1]
+                k = oracle.rotate(k.reshape(-1, HKV, D), pos, w["freq"])
+                v = v.reshape(-1, HKV, D)
+                heads = []
+                for h in range(HQ):
+                    s = k[:, h // (HQ // HKV)] @ q[h] / math.sqrt(D)
+                    p = np.exp(s - s.max())
+                    heads.append((p / p.sum()) @ v[:, h // (HQ // HKV)])
+                logits = np.concatenate(heads) @ w64["out"] + x[-1] @ w64["skip"]
+                logp = logits - logits.max()
+                logp -= math.log(np.exp(logp).sum())
+                cands += [(cum + lp, toks + [t]) for t, lp in enumerate(logp)]
+            cands.sort(key=lambda c: -c[0])
+            scores = [c[0] for c in cands[:BEAMS + 1]]
+            gap = min(gap, -max(np.diff(scores)))
+            beams = cands[:BEAMS]
+        all_tokens.append([b[1][len(prompt):] for b in beams])
+        all_scores.append([b[0] for b in beams])
+    return np.array(all_tokens), np.array(all_scores), gap
+
+
+@pytest.fixture(scope="module")
+def reference():
+    w = weights()
+    tokens, scores, gap = dense_beam_search(w)
+    assert gap > 1e-3
+    return w, tokens, scores
+
+
+def test_reference_has_clear_choices(reference):
+    """On the CPU: the dense search's choices are far apart, and beams cross."""
+    w, tokens, scores = reference
+    assert tokens.shape == (len(PROMPTS), BEAMS, STEPS) and np.all(np.diff(scores, axis=1) < 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_beam_search(reference, graph):
+    import paged_kv_cache_pagedattention_gb300 as pa
+
+    pa.pa_get_error_flags(clear=True)
+    w, want_tokens, want_scores = reference
+    seqs, rows = len(PROMPTS), len(PROMPTS) * BEAMS
+    width = -(-LONGEST // BS)
+    blocks = sum(-(-n // BS) for n in PROMPTS) + rows * 4
+    d = {k: torch.from_numpy(v).to(DEV) for k, v in w.items() if k != "prompts"}
+    kc = torch.full((blocks, HKV, BS, D), 100.0, device=DEV)   # stale contents that nothing may read
+    vc = torch.full_like(kc, 100.0)
+    refs = torch.zeros(blocks, dtype=torch.int32, device=DEV)
+    state = [(torch.full((rows, width), -1, dtype=torch.int32, device=DEV),
+              torch.zeros(rows, dtype=torch.int32, device=DEV)) for _ in range(2)]
+
+    def write(tokens, table, lens, qsl, slots, pairs, positions, ws):
+        """Room for the tokens, their k and v in the cache; their rotated q."""
+        pa.pa_append_blocks(table, lens, qsl, slots, pairs, refs, BS, ws)
+        pa.pa_copy_blocks(kc, vc, pairs)
+        x = d["embed"][tokens]
+        q, k, v = (t.unflatten(1, (-1, D)) for t in (x @ d["qkv"]).split([HQ * D, HKV * D, HKV * D], 1))
+        q_out = torch.empty(len(x), HQ, D, device=DEV)
+        pa.pa_rotary_and_cache(q_out, q, k, v, kc, vc, positions, slots, d["freq"])
+        return x, q_out
+
+    # prompts but for their last token, in the first row of each sequence
+    lens = np.zeros(rows, np.int32)
+    lens[::BEAMS] = np.array(PROMPTS) - 1
+    qsl = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(DEV)
+    total = int(lens.sum())
+    body = torch.from_numpy(np.concatenate([p[:-1] for p in w["prompts"]])).to(DEV)
+    at = torch.from_numpy(np.concatenate([np.arange(n - 1) for n in PROMPTS]).astype(np.int32)).to(DEV)
+    slots = torch.empty(total, dtype=torch.int64, device=DEV)
+    pairs = torch.empty(rows, 2, dtype=torch.int64, device=DEV)
+    write(body, *state[0], qsl, slots, pairs, at, pa.workspace_tensor(pa.pa_append_workspace_size(rows, total, BS)))
+    pa.pa_fork_blocks(*state[1], *state[0], torch.arange(rows, dtype=torch.int32, device=DEV) // BEAMS * BEAMS, refs, BS)
+    pa.pa_release_blocks(*state[0], refs, BS)
+    state.reverse()
+
+    cum = torch.full((seqs, BEAMS), -math.inf, device=DEV)
+    cum[:, 0] = 0.0
+    tokens = torch.tensor([int(p[-1]) for p in w["prompts"] for _ in range(BEAMS)], dtype=torch.int32, device=DEV)
+    one = torch.arange(rows + 1, dtype=torch.int32, device=DEV)
+    slots = torch.empty(rows, dtype=torch.int64, device=DEV)
+    picked = [torch.empty(seqs, BEAMS, dtype=torch.int32, device=DEV) for _ in range(4)]
+    ws_append = pa.workspace_tensor(pa.pa_append_workspace_size(rows, rows, BS))
+    ws_beam = pa.workspace_tensor(pa.pa_beam_select_workspace_size(seqs, BEAMS, VOCAB, BEAMS))
+    ws_decode = pa.workspace_tensor(pa.pa_decode_workspace_size(rows, HQ, HKV, D, LONGEST, BS))
+
+    def step(now, then, out_tokens, out_parents):
+        table, lens = now
+        x, q = write(tokens, table, lens, one, slots, pairs, lens.clone(), ws_append)
+        attn = torch.empty_like(q)
+        pa.pa_decode(attn, q, kc, vc, table, lens, LONGEST, 1 / math.sqrt(D), ws_decode)
+        logits = attn.flatten(1) @ d["out"] + x @ d["skip"]
+        scores = torch.empty_like(cum)
+        pa.pa_beam_select(scores, out_tokens, out_parents, logits, cum, ws_beam)
+        cum.copy_(scores)
+        tokens.copy_(out_tokens.flatten())
+        pa.pa_fork_blocks(*then, table, lens, out_parents.flatten(), refs, BS)
+        pa.pa_release_blocks(table, lens, refs, BS)
+
+    def two_steps():
+        step(state[0], state[1], picked[0], picked[1])
+        step(state[1], state[0], picked[2], picked[3])
+
+    replay = two_steps
+    if graph:
+        saved = [t.clone() for t in (kc, vc, refs, cum, tokens, *state[0], *state[1])]
+        two_steps()                             # warm-up outside the capture, then back to the start
+        for t, s in zip((kc, vc, refs, cum, tokens, *state[0], *state[1]), saved):
+            t.copy_(s)
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            two_steps()
+        replay = captured.replay
+    got = np.zeros((seqs, BEAMS, 0), np.int64)
+    for _ in range(STEPS // 2):
+        replay()
+        for tok, par in ((picked[0], picked[1]), (picked[2], picked[3])):
+            par = par.cpu().numpy() - np.arange(seqs)[:, None] * BEAMS
+            got = np.concatenate([got[np.arange(seqs)[:, None], par], tok.cpu().numpy()[..., None]], -1)
+    assert pa.pa_get_error_flags(clear=True) == 0
+    assert np.array_equal(got, want_tokens)
+    assert np.abs(cum.cpu().numpy() - want_scores).max() < 1e-3
+    assert state[0][1].tolist() == [n + STEPS - 1 for n in PROMPTS for _ in range(BEAMS)]
+    pa.pa_release_blocks(*state[0], refs, BS)
+    assert not bool(refs.any()) and pa.pa_get_error_flags(clear=True) == 0
