@@ -206,44 +206,45 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
                                bs, kv_code(k_cache), _stream(stream)), "pa_copy_blocks")
 
 
-def _device_call(fn, where, tensors, args, stream):
-    """Call fn(*args, stream) on the tensors' device: the current stream of that device, or
-    the caller's, which has to belong to it."""
-    index = None
+# The raw handle of a device's current stream; torch.cuda.current_stream builds an object
+# first (1.1 against 0.1 us on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(fn, where, tensors, stream, *args):
+    """Call fn(*args, stream) on the tensors' device: on the current stream of that device, or
+    on the caller's, which has to belong to it."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{where}: expected CUDA tensors")
-        if index is None:
-            index = d
-        elif d != index:
-            raise ValueError(f"{where}: the tensors are on different devices")
-    if stream is not None and stream.device.index != index:
+        if t.get_device() != index or index < 0:
+            raise ValueError(f"{where}: expected CUDA tensors on one device")
+    if stream is None:
+        raw = _raw_stream(index)
+    elif stream.device.index != index:
         raise ValueError(f"{where}: the stream belongs to another device than the tensors")
-    s = stream if stream is not None else torch.cuda.current_stream(index)
+    else:
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == index:
-        st = fn(*args, s.cuda_stream)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, s.cuda_stream)
+            st = fn(*args, raw)
     if st != PA_OK:
         raise PAError(st, where)
 
 
-def _int32(t, shape, what):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _check_int32(t, shape, what):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)}")
-    return t.data_ptr()
 
 
-def _rows(t, what):
-    """(pointer, elements between tokens) of a [tokens][heads][head_size] tensor whose heads
-    are contiguous; tokens may be any distance apart."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{what} must be [num_tokens][heads][head_size] with contiguous heads")
-    return t.data_ptr(), t.stride(0)
+def _row_stride(t, heads, d, what):
+    """Elements between the tokens of a [tokens][heads][d] tensor whose heads are contiguous."""
+    token, head, elem = t.stride()
+    if (elem != 1 and d > 1) or (head != d and heads > 1):
+        raise ValueError(f"{what}: every token's [heads][head_size] must be contiguous")
+    return token
 
 
 def pa_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_max_position=0.0,
@@ -267,40 +268,42 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
     [T]), and write key and value into the paged caches at slot_mapping (int64 [T]; a negative
     slot skips the token).  inv_freq float32 [rotary_dim/2].  q, key and value may be slices of
     one projection (any distance between tokens).  q and q_out None: keys only."""
-    nb, hkv, bs, d = cache_geometry(k_cache, v_cache, key.shape[-1])
-    t = key.shape[0]
-    k_ptr, k_stride = _rows(key, "key")
-    v_ptr, v_stride = _rows(value, "value")
-    if tuple(key.shape) != (t, hkv, d) or value.shape != key.shape or value.dtype != key.dtype:
+    shape, dtype = key.shape, key.dtype
+    if len(shape) != 3 or value.shape != shape or value.dtype is not dtype:
         raise ValueError("key/value must be [num_tokens][num_kv_heads][head_size] of one dtype")
-    hq = 0
-    q_ptr = qo_ptr = None
-    q_stride = qo_stride = 0
+    t, hkv, d = shape
+    nb, heads, bs, head = cache_geometry(k_cache, v_cache, d)
+    if heads != hkv or head != d or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous and match key's heads")
+    tensors = [key, value, k_cache, v_cache, positions, slot_mapping, inv_freq]
+    hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None or q_out is not None:
-        if q is None or q_out is None or tuple(q.shape) != (t, q.shape[1], d) or q_out.shape != q.shape or \
-                q.dtype != key.dtype or q_out.dtype != q.dtype:
+        if q is None or q_out is None or q.dim() != 3 or q_out.shape != q.shape or q.dtype is not dtype or \
+                q_out.dtype is not dtype or q.shape[0] != t or q.shape[2] != d:
             raise ValueError("q/q_out must be [num_tokens][num_q_heads][head_size] of key's dtype")
         hq = q.shape[1]
-        q_ptr, q_stride = _rows(q, "q")
-        qo_ptr, qo_stride = _rows(q_out, "q_out")
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (t,) or not slot_mapping.is_contiguous():
+        q_ptr, q_stride = q.data_ptr(), _row_stride(q, hq, d, "q")
+        q_out_ptr, q_out_stride = q_out.data_ptr(), _row_stride(q_out, hq, d, "q_out")
+        tensors += [q, q_out]
+    _check_int32(positions, (t,), "positions")
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (t,) or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [num_tokens]")
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float32 tensor [rotary_dim/2]")
-    pos_ptr = _int32(positions, (t,), "positions")
     code = kv_code(k_cache, k_scale)
-    for sc in (k_scale, v_scale):
-        if sc is not None and (sc.dtype != torch.float32 or sc.numel() not in (1, hkv)):
-            raise ValueError("scales: float32, one per tensor or one per KV head")
-    if code in (PA_FP8_E4M3_PER_HEAD, PA_FP8_E5M2_PER_HEAD, PA_NVFP4_PER_HEAD) and \
-            (v_scale is None or v_scale.numel() != k_scale.numel()):
-        raise ValueError("k_scale and v_scale must both hold one value per KV head")
-    _device_call(_lib.pa_rotary_and_cache, "pa_rotary_and_cache",
-                 (key, value, q, q_out, k_cache, v_cache, positions, slot_mapping, inv_freq, k_scale, v_scale),
-                 (qo_ptr, q_ptr, k_ptr, v_ptr, _ptr(k_cache), _ptr(v_cache), pos_ptr, slot_mapping.data_ptr(),
-                  inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.numel(), bs, 1 if interleaved else 0,
-                  float(attn_factor), qo_stride, q_stride, k_stride, v_stride, dtype_code(key), code, _ptr(k_scale),
-                  _ptr(v_scale)), stream)
+    k_scale_ptr = v_scale_ptr = None
+    if code >= PA_FP8_E4M3 and k_scale is not None and v_scale is not None:
+        for scale in (k_scale, v_scale):
+            if scale.dtype is not torch.float32 or not scale.is_contiguous() or scale.numel() != k_scale.numel() or \
+                    scale.numel() not in (1, hkv):
+                raise ValueError("scales: float32, both one per tensor or both one per KV head")
+        k_scale_ptr, v_scale_ptr = k_scale.data_ptr(), v_scale.data_ptr()
+        tensors += [k_scale, v_scale]
+    _launch(_lib.pa_rotary_and_cache, "pa_rotary_and_cache", tensors, stream, q_out_ptr, q_ptr, key.data_ptr(),
+            value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+            inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.shape[0], bs, 1 if interleaved else 0, attn_factor,
+            q_out_stride, q_stride, _row_stride(key, hkv, d, "key"), _row_stride(value, hkv, d, "value"),
+            dtype_code(key), code, k_scale_ptr, v_scale_ptr)
 
 
 def pa_beam_select_workspace_size(num_seqs, num_beams, vocab_size, num_candidates) -> int:
@@ -311,21 +314,34 @@ def pa_beam_select(out_scores, out_tokens, out_parents, logits, beam_scores, wor
     """The best candidates of each sequence's beams: out_scores float32, out_tokens and
     out_parents int32, all [num_seqs][num_candidates]; logits [num_seqs*num_beams][vocab]
     (rows may be padded), beam_scores float32 [num_seqs][num_beams]."""
-    if beam_scores.dtype != torch.float32 or beam_scores.dim() != 2 or not beam_scores.is_contiguous():
+    if beam_scores.dtype is not torch.float32 or beam_scores.dim() != 2 or not beam_scores.is_contiguous():
         raise ValueError("beam_scores must be a contiguous float32 tensor [num_seqs][num_beams]")
     b, w = beam_scores.shape
     if logits.dim() != 2 or logits.shape[0] != b * w or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be [num_seqs*num_beams][vocab_size] with contiguous rows")
-    if out_scores.dim() != 2 or out_scores.shape[0] != b or out_scores.dtype != torch.float32 or \
+    if out_scores.dim() != 2 or out_scores.shape[0] != b or out_scores.dtype is not torch.float32 or \
             not out_scores.is_contiguous():
         raise ValueError("out_scores must be a contiguous float32 tensor [num_seqs][num_candidates]")
-    shape = tuple(out_scores.shape)
-    _device_call(_lib.pa_beam_select, "pa_beam_select",
-                 (logits, beam_scores, out_scores, out_tokens, out_parents, workspace),
-                 (out_scores.data_ptr(), _int32(out_tokens, shape, "out_tokens"),
-                  _int32(out_parents, shape, "out_parents"), logits.data_ptr(), logits.stride(0),
-                  beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits), _ptr(workspace),
-                  workspace.numel() * workspace.element_size()), stream)
+    shape = out_scores.shape
+    _check_int32(out_tokens, shape, "out_tokens")
+    _check_int32(out_parents, shape, "out_parents")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _launch(_lib.pa_beam_select, "pa_beam_select", (logits, beam_scores, out_scores, out_tokens, out_parents, workspace),
+            stream, out_scores.data_ptr(), out_tokens.data_ptr(), out_parents.data_ptr(), logits.data_ptr(),
+            logits.stride(0), beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits),
+            workspace.data_ptr(), workspace.nbytes)
+
+
+def _pages(block_tables, seq_lens, ref_counts):
+    """(rows, max_blocks_per_seq, num_blocks) of a pool's arrays."""
+    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+        raise ValueError("block_tables must be [rows][max_blocks_per_seq] and ref_counts [num_blocks]")
+    n, width = shape = block_tables.shape
+    _check_int32(block_tables, shape, "block_tables")
+    _check_int32(seq_lens, (n,), "seq_lens")
+    _check_int32(ref_counts, ref_counts.shape, "ref_counts")
+    return n, width, ref_counts.shape[0]
 
 
 def pa_fork_blocks(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts, block_size,
@@ -333,16 +349,17 @@ def pa_fork_blocks(block_tables_out, seq_lens_out, block_tables, seq_lens, paren
     """Children rows take the blocks and lengths of rows ``parents`` (int32 [children];
     negative: an empty row) of block_tables/seq_lens; ref_counts int32 [num_blocks] counts
     the holders of every block.  See pa.h."""
-    if block_tables.dim() != 2 or parents.dim() != 1 or ref_counts.dim() != 1:
-        raise ValueError("block_tables [rows][max_blocks_per_seq], parents [children], ref_counts [num_blocks]")
-    m, width = block_tables.shape
-    n = parents.numel()
-    _device_call(_lib.pa_fork_blocks, "pa_fork_blocks",
-                 (block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts),
-                 (_int32(block_tables_out, (n, width), "block_tables_out"), _int32(seq_lens_out, (n,), "seq_lens_out"),
-                  _int32(block_tables, (m, width), "block_tables"), _int32(seq_lens, (m,), "seq_lens"),
-                  _int32(parents, (n,), "parents"), _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n, m,
-                  width, ref_counts.numel(), int(block_size)), stream)
+    m, width, blocks = _pages(block_tables, seq_lens, ref_counts)
+    if parents.dim() != 1:
+        raise ValueError("parents must be int32 [children]")
+    n = parents.shape[0]
+    _check_int32(parents, (n,), "parents")
+    _check_int32(block_tables_out, (n, width), "block_tables_out")
+    _check_int32(seq_lens_out, (n,), "seq_lens_out")
+    _launch(_lib.pa_fork_blocks, "pa_fork_blocks",
+            (block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts), stream,
+            block_tables_out.data_ptr(), seq_lens_out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            parents.data_ptr(), ref_counts.data_ptr(), n, m, width, blocks, block_size)
 
 
 def pa_append_workspace_size(num_seqs, total_q_tokens, block_size) -> int:
@@ -354,33 +371,31 @@ def pa_append_blocks(block_tables, seq_lens, query_start_loc, slot_mapping, bloc
     """Room for the next tokens of every row (query_start_loc int32 [rows+1]): blocks from the
     pool, slots (int64 [new tokens]) and copy-on-write pairs (block_mapping int64 [rows][2],
     for pa_copy_blocks).  All or nothing; see pa.h."""
-    if block_tables.dim() != 2 or ref_counts.dim() != 1:
-        raise ValueError("block_tables [rows][max_blocks_per_seq], ref_counts [num_blocks]")
-    n, width = block_tables.shape
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+    n, width, blocks = _pages(block_tables, seq_lens, ref_counts)
+    _check_int32(query_start_loc, (n + 1,), "query_start_loc")
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [total_q_tokens]")
-    if block_mapping.dtype != torch.int64 or tuple(block_mapping.shape) != (n, 2) or not block_mapping.is_contiguous():
+    if block_mapping.dtype is not torch.int64 or block_mapping.shape != (n, 2) or not block_mapping.is_contiguous():
         raise ValueError("block_mapping must be a contiguous int64 tensor [rows][2]")
-    _device_call(_lib.pa_append_blocks, "pa_append_blocks",
-                 (block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping, ref_counts, workspace),
-                 (_int32(block_tables, (n, width), "block_tables"), _int32(seq_lens, (n,), "seq_lens"),
-                  _int32(query_start_loc, (n + 1,), "query_start_loc"), slot_mapping.data_ptr(),
-                  block_mapping.data_ptr(), _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n,
-                  slot_mapping.numel(), width, ref_counts.numel(), int(block_size), _ptr(workspace),
-                  workspace.numel() * workspace.element_size()), stream)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _launch(_lib.pa_append_blocks, "pa_append_blocks",
+            (block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping, ref_counts, workspace), stream,
+            block_tables.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
+            block_mapping.data_ptr(), ref_counts.data_ptr(), n, slot_mapping.shape[0], width, blocks, block_size,
+            workspace.data_ptr(), workspace.nbytes)
 
 
 def pa_release_blocks(block_tables, seq_lens, ref_counts, block_size, keep_lens=None, stream=None) -> None:
     """Give up what lies behind the first keep_lens (int32 [rows]; None: 0) tokens of every row:
     the blocks lose a holder and seq_lens is cut.  See pa.h."""
-    if block_tables.dim() != 2 or ref_counts.dim() != 1:
-        raise ValueError("block_tables [rows][max_blocks_per_seq], ref_counts [num_blocks]")
-    n, width = block_tables.shape
-    _device_call(_lib.pa_release_blocks, "pa_release_blocks", (block_tables, seq_lens, ref_counts, keep_lens),
-                 (_int32(block_tables, (n, width), "block_tables"), _int32(seq_lens, (n,), "seq_lens"),
-                  None if keep_lens is None else _int32(keep_lens, (n,), "keep_lens"),
-                  _int32(ref_counts, (ref_counts.numel(),), "ref_counts"), n, width, ref_counts.numel(),
-                  int(block_size)), stream)
+    n, width, blocks = _pages(block_tables, seq_lens, ref_counts)
+    tensors, keep_ptr = (block_tables, seq_lens, ref_counts), None
+    if keep_lens is not None:
+        _check_int32(keep_lens, (n,), "keep_lens")
+        tensors, keep_ptr = (*tensors, keep_lens), keep_lens.data_ptr()
+    _launch(_lib.pa_release_blocks, "pa_release_blocks", tensors, stream, block_tables.data_ptr(),
+            seq_lens.data_ptr(), keep_ptr, ref_counts.data_ptr(), n, width, blocks, block_size)
 
 
 def pa_default_partition_size(num_seqs, num_kv_heads, max_seq_len, block_size) -> int:
