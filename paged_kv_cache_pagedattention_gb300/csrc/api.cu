@@ -453,15 +453,14 @@ AttnParams base_params(void* out, const void* q, const void* k_cache, const void
 }
 
 struct BeamLayout {
-  int segment, segments;
+  int segments;
   size_t state_off, keys_off, total;
 };
 
 BeamLayout beam_layout(int num_seqs, int num_beams, int vocab_size, int num_candidates) {
   BeamLayout L;
   const long long rows = (long long)num_seqs * num_beams;
-  L.segment = pa::beam_segment(rows, vocab_size);
-  L.segments = static_cast<int>(ceil_div(vocab_size, L.segment));
+  L.segments = pa::beam_segments(rows, vocab_size);
   const size_t parts = (size_t)rows * L.segments;
   L.state_off = 0;
   L.keys_off = align256(parts * sizeof(float2));
@@ -752,7 +751,6 @@ pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_pa
   p.num_beams = num_beams;
   p.vocab_size = vocab_size;
   p.num_candidates = num_candidates;
-  p.segment = L.segment;
   p.num_segments = L.segments;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   TraceScope t(10, s);

@@ -13,87 +13,273 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPerThread = 16;                   // elements of a tile that one thread holds
+constexpr int kTile = kThreads * kPerThread;
+constexpr int kSpare = 256;                      // kept candidates that do not force a merge
+constexpr int kJoinThreads = 256;
+constexpr int kMaxKeep = PA_MAX_BEAM_CANDIDATES;
 constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kMaxKeep <= 32, "the threshold is one of 32 group maxima");
 
-// A logit as fp32: NaN counts as -inf, +inf as the type's largest finite value, and -0 as 0.
 template <int DT>
-__device__ __forceinline__ float clean_logit(typename Elem<DT>::T raw) {
-  constexpr float top = DT == PA_F16 ? 65504.f : DT == PA_BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f;
-  const float x = Elem<DT>::load(&raw);
-  return x != x ? kNegInf : fminf(x, top) + 0.f;
+constexpr float largest() {
+  return DT == PA_F16 ? 65504.f : DT == PA_BF16 ? 3.3895313892515355e38f : 3.4028234663852886e38f;
 }
 
-// Keys order logits by value, then by the lower index; 0 is below every key.
-__device__ __forceinline__ unsigned long long make_key(float x, unsigned index) {
-  const unsigned b = __float_as_uint(x);
+// Keys order logits by value (-0 as 0), then by the lower index; 0 is below every key.
+using Key = unsigned long long;
+__device__ __forceinline__ Key make_key(float x, unsigned index) {
+  const unsigned b = __float_as_uint(x + 0.f);
   const unsigned ordered = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (static_cast<unsigned long long>(ordered) << 32) | (0xffffffffu - index);
+  return (static_cast<Key>(ordered) << 32) | (0xffffffffu - index);
 }
-__device__ __forceinline__ float key_value(unsigned long long key) {
+__device__ __forceinline__ float key_value(Key key) {
   const unsigned o = static_cast<unsigned>(key >> 32);
   return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
-__device__ __forceinline__ unsigned key_index(unsigned long long key) {
-  return 0xffffffffu - static_cast<unsigned>(key);
-}
+__device__ __forceinline__ unsigned key_index(Key key) { return 0xffffffffu - static_cast<unsigned>(key); }
 
 // m, s <- the softmax state of both: s is sum exp(x - m); (-inf, 0) is empty.
 __device__ __forceinline__ void join_state(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   if (top == kNegInf) return;
-  s = s * expf(m - top) + s2 * expf(m2 - top);
+  s = s * ex2_approx((m - top) * kLog2e) + s2 * ex2_approx((m2 - top) * kLog2e);
   m = top;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams p) {
-  using T = typename Elem<DT>::T;
-  __shared__ float sm[kThreads / 32], ss[kThreads / 32];
-  __shared__ unsigned long long sk[kThreads / 32];
-  const int seg = blockIdx.x;
-  const long long row = blockIdx.y;
-  const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
-  const int lo = seg * p.segment, hi = min(p.vocab_size, lo + p.segment);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float m = kNegInf, s = 0.f;
-  for (int i = lo + threadIdx.x; i < hi; i += kThreads) join_state(m, s, clean_logit<DT>(x[i]), 1.f);
-  for (int o = 16; o; o >>= 1) join_state(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
-  if (lane == 0) {
-    sm[warp] = m;
-    ss[warp] = s;
+// The k-th largest of the block's 32 groups of neighbouring threads, by each group's largest
+// v.  The values of k groups are at or above it, so the k largest of all are too.
+template <int kSize, class V>
+__device__ __forceinline__ V group_threshold(V v, int k, V* groups) {
+  constexpr int kGroup = kSize / 32;
+#pragma unroll
+  for (int o = 1; o < kGroup; o <<= 1) v = max(v, __shfl_xor_sync(~0u, v, o));
+  if (threadIdx.x % kGroup == 0) groups[threadIdx.x / kGroup] = v;
+  __syncthreads();
+  const int lane = threadIdx.x % 32;
+  const V mine = groups[lane];
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const V other = groups[i];
+    rank += other > mine || (other == mine && i < lane);
+  }
+  const unsigned at = __ballot_sync(~0u, rank == k - 1);
+  const V result = __shfl_sync(~0u, mine, __ffs(at) - 1);
+  __syncthreads();
+  return result;
+}
+
+struct SegmentShared {
+  Key buffer[kTile + kSpare];  // candidates of this segment so far
+  unsigned short picked[kTile + kSpare];  // merge: places of the ones above the threshold
+  Key groups[32];
+  float float_groups[32];
+  Key best[kMaxKeep];
+  float m[kWarps], s[kWarps];
+  int count, picked_count;
+};
+
+// Reduce the block's candidates to the k best, in order, at the buffer's start; the keys
+// behind them become 0 in `best`.  Returns the k-th best key, or 0 where there are fewer.
+__device__ Key merge_candidates(SegmentShared& sh, int k) {
+  const int n = sh.count;
+  Key top = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, sh.buffer[i]);
+  if (threadIdx.x < kMaxKeep) sh.best[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.picked_count = 0;
+  const Key threshold = group_threshold<kThreads>(top, k, sh.groups);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    if (sh.buffer[i] >= threshold) sh.picked[atomicAdd(&sh.picked_count, 1)] = i;
   }
   __syncthreads();
+  const int m = sh.picked_count;
+  for (int i = threadIdx.x; i < m; i += kThreads) {
+    const Key key = sh.buffer[sh.picked[i]];
+    int rank = 0;
+    for (int j = 0; j < m; ++j) rank += sh.buffer[sh.picked[j]] > key;  // keys are distinct
+    if (rank < k) sh.best[rank] = key;
+  }
+  __syncthreads();
+  if (threadIdx.x < k) sh.buffer[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) sh.count = min(n, k);
+  const Key last = sh.best[k - 1];
+  __syncthreads();
+  return last;
+}
+
+// 16 bytes from byte `shift` (0 .. 15) of the 32 in lo and hi.
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, unsigned shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const unsigned bits = 8 * (shift & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// One block a segment of a row, in one pass: tiles of kTile elements in registers, the next
+// tile's loads in flight.  Per thread a running maximum and the sum of exp against it,
+// rescaled once a tile; a tile's elements are looked at one by one only in threads whose
+// maximum reaches the block's threshold.  The first threshold comes from the tile's group
+// maxima, later ones from the merges.
+//
+// A thread's elements are given by their index in the row alone, so equal rows have equal
+// sums wherever they lie in memory.  Rows off the 16-byte grid (an odd vocabulary, kShifted)
+// are read as the two pieces that cover 16 bytes; pieces that reach over the row's ends are
+// read element by element.
+template <int DT, bool kShifted>
+__global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr int kVec = 16 / Elem<DT>::bytes;      // elements of a 16-byte piece
+  constexpr int kLoads = kPerThread / kVec;
+  extern __shared__ __align__(16) unsigned char raw[];
+  SegmentShared& sh = *reinterpret_cast<SegmentShared*>(raw);
+  const int seg = blockIdx.x, k = p.num_candidates;
+  const long long row = blockIdx.y;
+  const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
+  // the row's whole pieces, cut evenly; the elements behind the last go to the last segment
+  const int pieces = p.vocab_size / kVec;
+  const int first = static_cast<int>((long long)pieces * seg / p.num_segments);
+  const int end = static_cast<int>((long long)pieces * (seg + 1) / p.num_segments);
+  const unsigned shift = kShifted ? reinterpret_cast<uintptr_t>(x) % 16 : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - shift);
+  // pieces [inner, inner_end) lie in the row with the 32 bytes that are read for them
+  const int inner = shift ? 1 : 0;
+  const int inner_end = (p.vocab_size - kVec + static_cast<int>(shift / sizeof(T))) / kVec;
+  if (threadIdx.x == 0) sh.count = 0;
+
+  float m = kNegInf, s = 0.f;
+  Key threshold = 0;
+  bool fresh = true;  // no threshold yet
+  // index_of(i): the row's element that v[i] is
+  auto take = [&](float (&v)[kPerThread], auto index_of) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < kPerThread; ++i) top = fmaxf(top, v[i]);  // NaN is passed over
+    float sum = 0.f;
+    float m2 = fmaxf(m, top);
+    if (m2 != kNegInf) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) sum += ex2_approx((v[i] - m2) * kLog2e);
+    }
+    if (top == INFINITY || sum != sum) {  // NaN and +inf: once more, as -inf and the largest finite value
+      top = kNegInf;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        v[i] = fminf(fmaxf(v[i], kNegInf), largest<DT>());
+        top = fmaxf(top, v[i]);
+      }
+      m2 = fmaxf(m, top);
+      sum = 0.f;
+      if (m2 != kNegInf) {
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) sum += ex2_approx((v[i] - m2) * kLog2e);
+      }
+    }
+    if (m2 != kNegInf) {
+      s = s * ex2_approx((m - m2) * kLog2e) + sum;
+      m = m2;
+    }
+    if (fresh) {
+      const float t = group_threshold<kThreads>(top, k, sh.float_groups);
+      threshold = t == kNegInf ? 0 : make_key(t, 0xffffffffu);
+      fresh = false;
+    }
+    bool full = false;
+    if (top != kNegInf && (threshold == 0 || top >= key_value(threshold))) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        const Key key = make_key(v[i], static_cast<unsigned>(index_of(i)));
+        if (v[i] > kNegInf && key >= threshold) {
+          const int at = atomicAdd(&sh.count, 1);
+          sh.buffer[at] = key;
+          full |= at >= kSpare;
+        }
+      }
+    }
+    if (__syncthreads_or(full)) threshold = max(threshold, merge_candidates(sh, k));
+  };
+
+  uint4 next[kLoads], over[kShifted ? kLoads : 1];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = base + i * kThreads + threadIdx.x;
+      if (at >= end) continue;
+      if (!kShifted || (at >= inner && at < inner_end)) {
+        next[i] = src[at];
+        if constexpr (kShifted) over[i] = src[at + 1];
+      } else {
+        T each[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) each[j] = x[(long long)at * kVec + j];
+        memcpy(&next[i], each, 16);
+      }
+    }
+  };
+  load(first);
+  for (int base = first; base < end; base += kLoads * kThreads) {
+    float v[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = base + i * kThreads + threadIdx.x;
+      uint4 piece = next[i];
+      if constexpr (kShifted) piece = shifted(piece, over[i], at >= inner && at < inner_end ? shift : 0);
+      const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == PA_F32) {
+          v[i * kVec + j] = at < end ? __uint_as_float(w[j]) : kNegInf;
+        } else {
+          const float2 f = unpack2<DT>(w[j]);
+          v[i * kVec + 2 * j] = at < end ? f.x : kNegInf;
+          v[i * kVec + 2 * j + 1] = at < end ? f.y : kNegInf;
+        }
+      }
+    }
+    load(base + kLoads * kThreads);
+    take(v, [&](int i) { return (base + i / kVec * kThreads + threadIdx.x) * kVec + i % kVec; });
+  }
+  const int tail = pieces * kVec;
+  if (seg == p.num_segments - 1 && tail < p.vocab_size) {
+    float v[kPerThread];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) v[j] = kNegInf;
+    if (static_cast<int>(threadIdx.x) < p.vocab_size - tail) v[0] = Elem<DT>::load(x + tail + threadIdx.x);
+    take(v, [&](int) { return tail + threadIdx.x; });
+  }
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int o = 16; o; o >>= 1) join_state(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+  if (lane == 0) {
+    sh.m[warp] = m;
+    sh.s[warp] = s;
+  }
+  __syncthreads();
+  merge_candidates(sh, k);
   const long long part = row * p.num_segments + seg;
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) join_state(m, s, sm[w], ss[w]);
+    for (int w = 1; w < kWarps; ++w) join_state(m, s, sh.m[w], sh.s[w]);
     p.state[part] = make_float2(m, s);
   }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < p.num_candidates; ++k) {
-    unsigned long long best = 0;
-    for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-      const float v = clean_logit<DT>(x[i]);
-      if (v == kNegInf) continue;
-      const unsigned long long key = make_key(v, i);
-      if (key < last && key > best) best = key;
-    }
-    for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
-    if (lane == 0) sk[warp] = best;
-    __syncthreads();
-    best = 0;
-    for (int w = 0; w < kThreads / 32; ++w) best = max(best, sk[w]);
-    __syncthreads();
-    if (threadIdx.x == 0) p.keys[part * p.num_candidates + k] = best;
-    last = best;  // 0 once the segment is used up: nothing is below it
-  }
+  if (threadIdx.x < k) p.keys[part * k + threadIdx.x] = sh.best[threadIdx.x];
 }
 
 // A candidate of a sequence, and the order of candidates: by score, then the lower beam,
 // then the key (larger logit, lower token).  Key 0 is none and comes last.
 struct Candidate {
   double score;
-  unsigned long long key;
+  Key key;
   int beam;
 };
 __device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
@@ -103,34 +289,103 @@ __device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
   return a.key > b.key;
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
-  extern __shared__ double2 norm[];  // [num_beams] (maximum, log of the sum against it)
-  __shared__ Candidate found[kThreads / 32];
+// A beam of a sequence: its score, its row's maximum and the log of the sum against it.
+struct Beam {
+  double log_sum;
+  float score, m;
+};
+
+__device__ __forceinline__ Candidate candidate_of(const Beam* beams, Key key, int beam) {
+  const Beam b = beams[beam];
+  return {b.score + ((key_value(key) - static_cast<double>(b.m)) - b.log_sum), b.score == kNegInf ? 0 : key, beam};
+}
+
+__device__ __forceinline__ void write_out(const BeamParams& p, long long seq, int k, const Candidate& c) {
+  const long long at = seq * p.num_candidates + k;
+  const bool none = c.key == 0;
+  p.out_scores[at] = none ? kNegInf : static_cast<float>(c.score);
+  p.out_tokens[at] = none ? -1 : static_cast<int>(key_index(c.key));
+  p.out_parents[at] = none ? -1 : static_cast<int>(seq * p.num_beams + c.beam);
+}
+
+constexpr int kJoin = 1024;  // candidates that are ranked at once
+
+// One block a sequence: the rows' states are joined, then the segments' candidates.  Most
+// fall to a threshold on their fp32 scores, held with the scores' error bounds so that
+// none of the best can be lost; the rest are ranked by their fp64 scores.
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParams p) {
+  extern __shared__ Beam beams[];  // [num_beams]
+  __shared__ Candidate kept[kJoin];
+  __shared__ float groups[32];
+  __shared__ Candidate found[kJoinThreads / 32];
+  __shared__ int count;
   const long long seq = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int w = threadIdx.x; w < p.num_beams; w += kThreads) {
+  if (threadIdx.x == 0) count = 0;
+  for (int w = warp; w < p.num_beams; w += kJoinThreads / 32) {
     const float2* st = p.state + (seq * p.num_beams + w) * p.num_segments;
     float m = kNegInf;
-    for (int i = 0; i < p.num_segments; ++i) m = fmaxf(m, st[i].x);
+    for (int i = lane; i < p.num_segments; i += 32) m = fmaxf(m, st[i].x);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     double sum = 0.0;
     if (m != kNegInf)
-      for (int i = 0; i < p.num_segments; ++i) sum += static_cast<double>(st[i].y * expf(st[i].x - m));
-    norm[w] = make_double2(m, log(sum));
+      for (int i = lane; i < p.num_segments; i += 32) sum += static_cast<double>(st[i].y * expf(st[i].x - m));
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) {
+      const float cum = p.beam_scores[seq * p.num_beams + w];
+      beams[w] = {log(sum), fminf(fmaxf(cum, kNegInf), largest<PA_F32>()), m};
+    }
   }
   __syncthreads();
   const int per_beam = p.num_segments * p.num_candidates, n = p.num_beams * per_beam;
-  const unsigned long long* keys = p.keys + seq * n;
+  const Key* keys = p.keys + seq * n;
+  // fp32: each of the three terms and sums is rounded once, so a score is off by less than
+  // 2^-22 of the terms' magnitudes
+  auto bounds = [&](int c, Key key, float& lo, float& hi) {
+    const Beam b = beams[c / per_beam];
+    const float rel = key_value(key) - b.m, log_sum = static_cast<float>(b.log_sum);
+    const float score = b.score + (rel - log_sum);
+    const float error = 0x1p-21f * (fabsf(b.score) + fabsf(rel) + fabsf(log_sum));
+    const bool none = key == 0 || b.score == kNegInf;
+    lo = none ? kNegInf : score - error;
+    hi = none ? kNegInf : score + error;
+  };
+  float top = kNegInf;
+  for (int c = threadIdx.x; c < n; c += kJoinThreads) {
+    float lo, hi;
+    bounds(c, keys[c], lo, hi);
+    top = fmaxf(top, lo);
+  }
+  const float threshold = group_threshold<kJoinThreads>(top, p.num_candidates, groups);
+  for (int c = threadIdx.x; c < n; c += kJoinThreads) {
+    const Key key = keys[c];
+    float lo, hi;
+    bounds(c, key, lo, hi);
+    if (hi == kNegInf || hi < threshold) continue;
+    const int at = atomicAdd(&count, 1);
+    if (at < kJoin) kept[at] = candidate_of(beams, key, c / per_beam);
+  }
+  __syncthreads();
+  const int m = count;
+  if (m <= kJoin) {
+    for (int i = threadIdx.x; i < m; i += kJoinThreads) {
+      const Candidate mine = kept[i];
+      int rank = 0;
+      for (int j = 0; j < m; ++j) rank += before(kept[j], mine);
+      if (rank < p.num_candidates) write_out(p, seq, rank, mine);
+    }
+    for (int i = m + threadIdx.x; i < p.num_candidates; i += kJoinThreads) write_out(p, seq, i, {0.0, 0, 0});
+    return;
+  }
+  // more near-equal candidates than fit: one after the other
   Candidate last = {INFINITY, ~0ull, -1};
   for (int k = 0; k < p.num_candidates; ++k) {
     Candidate best = {0.0, 0, 0};
-    for (int c = threadIdx.x; c < n; c += kThreads) {
-      Candidate cand = {0.0, keys[c], c / per_beam};
-      if (cand.key == 0) continue;
-      float cum = p.beam_scores[seq * p.num_beams + cand.beam];
-      if (cum != cum || cum == kNegInf) continue;
-      cum = fminf(cum, 3.4028234663852886e38f);
-      cand.score = cum + ((key_value(cand.key) - norm[cand.beam].x) - norm[cand.beam].y);
-      if (before(last, cand) && before(cand, best)) best = cand;
+    for (int c = threadIdx.x; c < n; c += kJoinThreads) {
+      const Key key = keys[c];
+      if (key == 0) continue;
+      const Candidate cand = candidate_of(beams, key, c / per_beam);
+      if (cand.key != 0 && before(last, cand) && before(cand, best)) best = cand;
     }
     for (int o = 16; o; o >>= 1) {
       const Candidate other = {__shfl_xor_sync(~0u, best.score, o), __shfl_xor_sync(~0u, best.key, o),
@@ -139,42 +394,46 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
     }
     if (lane == 0) found[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w)
+    for (int w = 0; w < kJoinThreads / 32; ++w)
       if (before(found[w], best)) best = found[w];
     __syncthreads();
-    if (threadIdx.x == 0) {
-      const long long at = seq * p.num_candidates + k;
-      const bool none = best.key == 0;
-      p.out_scores[at] = none ? kNegInf : static_cast<float>(best.score);
-      p.out_tokens[at] = none ? -1 : static_cast<int>(key_index(best.key));
-      p.out_parents[at] = none ? -1 : static_cast<int>(seq * p.num_beams + best.beam);
-    }
+    if (threadIdx.x == 0) write_out(p, seq, k, best);
     last = best;
   }
 }
 
 }  // namespace
 
-// Elements of a row that one block takes: rows are cut until the grid has some four blocks
-// an SM, but no finer than 2048 elements.
-int beam_segment(long long rows, int vocab_size) {
-  const long long want = 152 * 4;
-  long long parts = (want + rows - 1) / rows;
-  const long long most = (vocab_size + 2047) / 2048;
-  if (parts > most) parts = most;
-  if (parts < 1) parts = 1;
-  const long long seg = (vocab_size + parts - 1) / parts;
-  return static_cast<int>((seg + 7) / 8 * 8);
+// Segments of a row: rows are cut until the grid has some eight blocks an SM (what fits at
+// once), but no finer than a tile.
+int beam_segments(long long rows, int vocab_size) {
+  const long long want = (152 * 8 + rows - 1) / rows, most = (vocab_size + kTile - 1) / kTile;
+  return static_cast<int>(want < most ? want : most);
+}
+
+template <int DT, bool kShifted>
+static cudaError_t launch_segments(const BeamParams& p, cudaStream_t stream) {
+  const int smem = sizeof(SegmentShared);
+  const cudaError_t e = set_smem<beam_segment_kernel<DT, kShifted>>(smem);
+  if (e != cudaSuccess) return e;
+  beam_segment_kernel<DT, kShifted><<<dim3(p.num_segments, p.num_seqs * p.num_beams), kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT>
+static cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
+  const bool one = p.num_seqs * p.num_beams == 1;
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+                       (one || p.row_stride * Elem<DT>::bytes % 16 == 0);
+  return aligned ? launch_segments<DT, false>(p, stream) : launch_segments<DT, true>(p, stream);
 }
 
 cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream) {
-  const dim3 grid(p.num_segments, p.num_seqs * p.num_beams);
-  if (dtype == PA_F32) beam_segment_kernel<PA_F32><<<grid, kThreads, 0, stream>>>(p);
-  else if (dtype == PA_F16) beam_segment_kernel<PA_F16><<<grid, kThreads, 0, stream>>>(p);
-  else beam_segment_kernel<PA_BF16><<<grid, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = dtype == PA_F32   ? launch_type<PA_F32>(p, stream)
+                        : dtype == PA_F16 ? launch_type<PA_F16>(p, stream)
+                                          : launch_type<PA_BF16>(p, stream);
   if (e != cudaSuccess) return e;
-  beam_join_kernel<<<p.num_seqs, kThreads, p.num_beams * sizeof(double2), stream>>>(p);
+  beam_join_kernel<<<p.num_seqs, kJoinThreads, p.num_beams * sizeof(Beam), stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -137,11 +137,10 @@ struct BeamParams {
   int num_beams;
   int vocab_size;
   int num_candidates;
-  int segment;               // elements of a row that one block takes
-  int num_segments;
+  int num_segments;          // blocks a row
 };
 
-int beam_segment(long long rows, int vocab_size);
+int beam_segments(long long rows, int vocab_size);
 cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream);
 
 // Pages of sequences.  Rows are the table rows a call changes; parents are pa_fork_blocks'.
