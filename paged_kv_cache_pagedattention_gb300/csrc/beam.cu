@@ -13,16 +13,15 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 16;                   // elements of a tile that one thread holds
 constexpr int kTile = kThreads * kPerThread;
 constexpr int kSpare = 256;                      // kept candidates that do not force a merge
-constexpr int kJoinThreads = 256;
 constexpr int kMaxKeep = PA_MAX_BEAM_CANDIDATES;
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kMaxKeep <= 32, "the threshold is one of 32 group maxima");
+static_assert(kMaxKeep <= 32 && kMaxKeep <= kSpare, "the threshold is one of 32 group maxima");
 
 template <int DT>
 constexpr float largest() {
@@ -52,46 +51,69 @@ __device__ __forceinline__ void join_state(float& m, float& s, float m2, float s
 
 // The k-th largest of the block's 32 groups of neighbouring threads, by each group's largest
 // v.  The values of k groups are at or above it, so the k largest of all are too.
-template <int kSize, class V>
-__device__ __forceinline__ V group_threshold(V v, int k, V* groups) {
-  constexpr int kGroup = kSize / 32;
+template <class V>
+__device__ __forceinline__ V group_threshold(V v, int k, V* groups, V* result) {
+  constexpr int kGroup = kThreads / 32;
 #pragma unroll
   for (int o = 1; o < kGroup; o <<= 1) v = max(v, __shfl_xor_sync(~0u, v, o));
   if (threadIdx.x % kGroup == 0) groups[threadIdx.x / kGroup] = v;
   __syncthreads();
-  const int lane = threadIdx.x % 32;
-  const V mine = groups[lane];
-  int rank = 0;
+  if (threadIdx.x < 32) {
+    const V mine = groups[threadIdx.x];
+    int rank = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const V other = groups[i];
-    rank += other > mine || (other == mine && i < lane);
+    for (int i = 0; i < 32; ++i) {
+      const V other = groups[i];
+      rank += other > mine || (other == mine && i < static_cast<int>(threadIdx.x));
+    }
+    if (rank == k - 1) *result = mine;
   }
-  const unsigned at = __ballot_sync(~0u, rank == k - 1);
-  const V result = __shfl_sync(~0u, mine, __ffs(at) - 1);
   __syncthreads();
-  return result;
+  return *result;
+}
+
+// The same of the block's threads, each a group of its own: a sharper bound for more work.
+__device__ __forceinline__ float thread_threshold(float v, int k, float* values, float* result) {
+  values[threadIdx.x] = v;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < kThreads; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(values + i);
+    const int behind = static_cast<int>(threadIdx.x) - i;  // of equal values the lower thread's is first
+    rank += (w.x > v || (w.x == v && behind > 0)) + (w.y > v || (w.y == v && behind > 1)) +
+            (w.z > v || (w.z == v && behind > 2)) + (w.w > v || (w.w == v && behind > 3));
+  }
+  if (rank == k - 1) *result = v;
+  __syncthreads();
+  return *result;
 }
 
 struct SegmentShared {
-  Key buffer[kTile + kSpare];  // candidates of this segment so far
+  Key buffer[kTile + kSpare];  // candidates: the k best so far as keys, then (value, index) as they come
   unsigned short picked[kTile + kSpare];  // merge: places of the ones above the threshold
   Key groups[32];
   float float_groups[32];
   Key best[kMaxKeep];
+  Key threshold;
+  float float_threshold;
   float m[kWarps], s[kWarps];
   int count, picked_count;
 };
 
-// Reduce the block's candidates to the k best, in order, at the buffer's start; the keys
-// behind them become 0 in `best`.  Returns the k-th best key, or 0 where there are fewer.
-__device__ Key merge_candidates(SegmentShared& sh, int k) {
+// Reduce the block's candidates to the k best, in order, at the buffer's start and, with 0
+// behind them, in `best`; the first `keys` entries are keys already.  Returns the k-th best
+// key, or 0 where there are fewer.
+__device__ Key merge_candidates(SegmentShared& sh, int k, int keys) {
   const int n = sh.count;
   Key top = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, sh.buffer[i]);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    Key key = sh.buffer[i];
+    if (i >= keys) sh.buffer[i] = key = make_key(__uint_as_float(static_cast<unsigned>(key >> 32)), static_cast<unsigned>(key));
+    top = max(top, key);
+  }
   if (threadIdx.x < kMaxKeep) sh.best[threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.picked_count = 0;
-  const Key threshold = group_threshold<kThreads>(top, k, sh.groups);
+  const Key threshold = group_threshold(top, k, sh.groups, &sh.threshold);
   for (int i = threadIdx.x; i < n; i += kThreads) {
     if (sh.buffer[i] >= threshold) sh.picked[atomicAdd(&sh.picked_count, 1)] = i;
   }
@@ -159,13 +181,15 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
   if (threadIdx.x == 0) sh.count = 0;
 
   float m = kNegInf, s = 0.f;
-  Key threshold = 0;
-  bool fresh = true;  // no threshold yet
+  Key threshold = 0;      // candidates below it are not among the segment's k best
+  float least = kNegInf;  // its value
+  int keys = 0;           // candidates at the buffer's start that are keys
+  bool fresh = true;      // no threshold yet
   // index_of(i): the row's element that v[i] is
   auto take = [&](float (&v)[kPerThread], auto index_of) {
-    float top = v[0];
+    float top = kNegInf;
 #pragma unroll
-    for (int i = 1; i < kPerThread; ++i) top = fmaxf(top, v[i]);  // NaN is passed over
+    for (int i = 0; i < kPerThread; ++i) top = fmaxf(top, v[i]);  // NaN is passed over
     float sum = 0.f;
     float m2 = fmaxf(m, top);
     if (m2 != kNegInf) {
@@ -191,23 +215,27 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
       m = m2;
     }
     if (fresh) {
-      const float t = group_threshold<kThreads>(top, k, sh.float_groups);
-      threshold = t == kNegInf ? 0 : make_key(t, 0xffffffffu);
+      least = group_threshold(top, k, sh.float_groups, &sh.float_threshold);
+      if (least != kNegInf) threshold = make_key(least, 0xffffffffu);
       fresh = false;
     }
     bool full = false;
-    if (top != kNegInf && (threshold == 0 || top >= key_value(threshold))) {
+    if (top >= least) {
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i) {
-        const Key key = make_key(v[i], static_cast<unsigned>(index_of(i)));
-        if (v[i] > kNegInf && key >= threshold) {
-          const int at = atomicAdd(&sh.count, 1);
-          sh.buffer[at] = key;
-          full |= at >= kSpare;
-        }
+        if (!(v[i] >= least) || v[i] == kNegInf) continue;
+        const unsigned index = index_of(i);
+        if (v[i] == least && index > key_index(threshold)) continue;
+        const int at = atomicAdd(&sh.count, 1);
+        sh.buffer[at] = static_cast<Key>(__float_as_uint(v[i])) << 32 | index;
+        full |= at >= kSpare;
       }
     }
-    if (__syncthreads_or(full)) threshold = max(threshold, merge_candidates(sh, k));
+    if (__syncthreads_or(full)) {
+      threshold = max(threshold, merge_candidates(sh, k, keys));
+      if (threshold != 0) least = key_value(threshold);
+      keys = k;  // the buffer held more than that
+    }
   };
 
   uint4 next[kLoads], over[kShifted ? kLoads : 1];
@@ -266,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
     sh.s[warp] = s;
   }
   __syncthreads();
-  merge_candidates(sh, k);
+  merge_candidates(sh, k, keys);
   const long long part = row * p.num_segments + seg;
   if (threadIdx.x == 0) {
     for (int w = 1; w < kWarps; ++w) join_state(m, s, sh.m[w], sh.s[w]);
@@ -275,10 +303,38 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
   if (threadIdx.x < k) p.keys[part * k + threadIdx.x] = sh.best[threadIdx.x];
 }
 
-// A candidate of a sequence, and the order of candidates: by score, then the lower beam,
-// then the key (larger logit, lower token).  Key 0 is none and comes last.
+// log of a sum of 1 or more, to 2^-25 or so: its power of two in fp64 and log1p of the rest
+// (within -0.3 .. 0.42) in fp32.  fp64's own log took half of the join's time: the SM has two
+// fp64 lanes.
+__device__ __forceinline__ double log_of(double sum) {
+  const long long bits = __double_as_longlong(sum);
+  int power = static_cast<int>(bits >> 52) - 1023;
+  long long rest = bits & 0xfffffffffffffll;  // the mantissa less one, times 2^52
+  float f = static_cast<float>(rest) * 0x1p-52f;
+  if (f > 0.41421356f) {
+    ++power;
+    f = static_cast<float>(rest - (1ll << 52)) * 0x1p-53f;
+  }
+  return power * 0.69314718055994530942 + static_cast<double>(log1pf(f));
+}
+
+// A beam of a sequence: its score, its row's maximum and the log of the sum against it.
+struct Beam {
+  double log_sum;
+  float score, m;
+};
+
+// The fp64 score of a candidate, as an integer of the same order.
+__device__ __forceinline__ long long score_of(const Beam& b, Key key) {
+  const long long bits =
+      __double_as_longlong(b.score + ((key_value(key) - static_cast<double>(b.m)) - b.log_sum));
+  return bits ^ ((bits >> 63) & 0x7fffffffffffffffll);
+}
+
+// Candidates in order: by score, then the lower beam, then the key (larger logit, lower
+// token).  Key 0 is none and comes last.
 struct Candidate {
-  double score;
+  long long score;
   Key key;
   int beam;
 };
@@ -289,41 +345,44 @@ __device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
   return a.key > b.key;
 }
 
-// A beam of a sequence: its score, its row's maximum and the log of the sum against it.
-struct Beam {
-  double log_sum;
-  float score, m;
-};
-
-__device__ __forceinline__ Candidate candidate_of(const Beam* beams, Key key, int beam) {
-  const Beam b = beams[beam];
-  return {b.score + ((key_value(key) - static_cast<double>(b.m)) - b.log_sum), b.score == kNegInf ? 0 : key, beam};
-}
-
 __device__ __forceinline__ void write_out(const BeamParams& p, long long seq, int k, const Candidate& c) {
   const long long at = seq * p.num_candidates + k;
   const bool none = c.key == 0;
-  p.out_scores[at] = none ? kNegInf : static_cast<float>(c.score);
+  const double score = __longlong_as_double(c.score ^ ((c.score >> 63) & 0x7fffffffffffffffll));
+  p.out_scores[at] = none ? kNegInf : static_cast<float>(score);
   p.out_tokens[at] = none ? -1 : static_cast<int>(key_index(c.key));
   p.out_parents[at] = none ? -1 : static_cast<int>(seq * p.num_beams + c.beam);
 }
 
 constexpr int kJoin = 1024;  // candidates that are ranked at once
+constexpr int kHeld = 4;     // keys a thread loads ahead
 
 // One block a sequence: the rows' states are joined, then the segments' candidates.  Most
 // fall to a threshold on their fp32 scores, held with the scores' error bounds so that
 // none of the best can be lost; the rest are ranked by their fp64 scores.
-__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
   extern __shared__ Beam beams[];  // [num_beams]
-  __shared__ Candidate kept[kJoin];
-  __shared__ float groups[32];
-  __shared__ Candidate found[kJoinThreads / 32];
+  __shared__ long long scores[kJoin];
+  __shared__ Key kept[kJoin];
+  __shared__ int owner[kJoin];
+  __shared__ __align__(16) float tops[kThreads];
+  __shared__ float bound;
+  __shared__ Candidate found[kThreads / 32];
   __shared__ int count;
   const long long seq = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per_beam = p.num_segments * p.num_candidates, n = p.num_beams * per_beam;
+  const Key* keys = p.keys + seq * n;
+  Key held[kHeld];  // on their way while the states are joined
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = threadIdx.x + i * kThreads;
+    held[i] = c < n ? keys[c] : 0;
+  }
   if (threadIdx.x == 0) count = 0;
-  for (int w = warp; w < p.num_beams; w += kJoinThreads / 32) {
+  for (int w = warp; w < p.num_beams; w += kThreads / 32) {
     const float2* st = p.state + (seq * p.num_beams + w) * p.num_segments;
+    const float cum = p.beam_scores[seq * p.num_beams + w];
     float m = kNegInf;
     for (int i = lane; i < p.num_segments; i += 32) m = fmaxf(m, st[i].x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
@@ -331,62 +390,73 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     if (m != kNegInf)
       for (int i = lane; i < p.num_segments; i += 32) sum += static_cast<double>(st[i].y * expf(st[i].x - m));
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (lane == 0) {
-      const float cum = p.beam_scores[seq * p.num_beams + w];
-      beams[w] = {log(sum), fminf(fmaxf(cum, kNegInf), largest<PA_F32>()), m};
-    }
+    if (lane == 0) beams[w] = {log_of(sum), m == kNegInf ? kNegInf : fminf(fmaxf(cum, kNegInf), largest<PA_F32>()), m};
   }
   __syncthreads();
-  const int per_beam = p.num_segments * p.num_candidates, n = p.num_beams * per_beam;
-  const Key* keys = p.keys + seq * n;
+  // f(candidate's beam, its key) for this thread's candidates
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (held[i] != 0) f((threadIdx.x + i * kThreads) / per_beam, held[i]);
+    for (int c = threadIdx.x + kHeld * kThreads; c < n; c += kThreads) {
+      const Key key = keys[c];
+      if (key != 0) f(c / per_beam, key);
+    }
+  };
   // fp32: each of the three terms and sums is rounded once, so a score is off by less than
   // 2^-22 of the terms' magnitudes
-  auto bounds = [&](int c, Key key, float& lo, float& hi) {
-    const Beam b = beams[c / per_beam];
+  auto score32 = [&](const Beam& b, Key key, float& error) {
     const float rel = key_value(key) - b.m, log_sum = static_cast<float>(b.log_sum);
-    const float score = b.score + (rel - log_sum);
-    const float error = 0x1p-21f * (fabsf(b.score) + fabsf(rel) + fabsf(log_sum));
-    const bool none = key == 0 || b.score == kNegInf;
-    lo = none ? kNegInf : score - error;
-    hi = none ? kNegInf : score + error;
+    error = 0x1p-21f * (fabsf(b.score) + fabsf(rel) + fabsf(log_sum));
+    return b.score + (rel - log_sum);
   };
   float top = kNegInf;
-  for (int c = threadIdx.x; c < n; c += kJoinThreads) {
-    float lo, hi;
-    bounds(c, keys[c], lo, hi);
-    top = fmaxf(top, lo);
-  }
-  const float threshold = group_threshold<kJoinThreads>(top, p.num_candidates, groups);
-  for (int c = threadIdx.x; c < n; c += kJoinThreads) {
-    const Key key = keys[c];
-    float lo, hi;
-    bounds(c, key, lo, hi);
-    if (hi == kNegInf || hi < threshold) continue;
+  each([&](int w, Key key) {
+    const Beam b = beams[w];
+    if (b.score == kNegInf) return;
+    float error;
+    const float score = score32(b, key, error);
+    top = fmaxf(top, score - error);
+  });
+  const float threshold = thread_threshold(top, p.num_candidates, tops, &bound);
+  each([&](int w, Key key) {
+    const Beam b = beams[w];
+    if (b.score == kNegInf) return;
+    float error;
+    const float score = score32(b, key, error);
+    if (score + error < threshold) return;
     const int at = atomicAdd(&count, 1);
-    if (at < kJoin) kept[at] = candidate_of(beams, key, c / per_beam);
-  }
+    if (at >= kJoin) return;
+    scores[at] = score_of(b, key);
+    kept[at] = key;
+    owner[at] = w;
+  });
   __syncthreads();
   const int m = count;
   if (m <= kJoin) {
-    for (int i = threadIdx.x; i < m; i += kJoinThreads) {
-      const Candidate mine = kept[i];
+    for (int i = warp; i < m; i += kThreads / 32) {
+      const Candidate mine = {scores[i], kept[i], owner[i]};
       int rank = 0;
-      for (int j = 0; j < m; ++j) rank += before(kept[j], mine);
-      if (rank < p.num_candidates) write_out(p, seq, rank, mine);
+      for (int j = lane; j < m; j += 32) {
+        const long long other = scores[j];
+        if (other >= mine.score) rank += other > mine.score || before({other, kept[j], owner[j]}, mine);
+      }
+      rank = __reduce_add_sync(~0u, rank);
+      if (lane == 0 && rank < p.num_candidates) write_out(p, seq, rank, mine);
     }
-    for (int i = m + threadIdx.x; i < p.num_candidates; i += kJoinThreads) write_out(p, seq, i, {0.0, 0, 0});
+    for (int i = m + threadIdx.x; i < p.num_candidates; i += kThreads) write_out(p, seq, i, {0, 0, 0});
     return;
   }
   // more near-equal candidates than fit: one after the other
-  Candidate last = {INFINITY, ~0ull, -1};
+  Candidate last = {0x7fffffffffffffffll, ~0ull, -1};
   for (int k = 0; k < p.num_candidates; ++k) {
-    Candidate best = {0.0, 0, 0};
-    for (int c = threadIdx.x; c < n; c += kJoinThreads) {
-      const Key key = keys[c];
-      if (key == 0) continue;
-      const Candidate cand = candidate_of(beams, key, c / per_beam);
-      if (cand.key != 0 && before(last, cand) && before(cand, best)) best = cand;
-    }
+    Candidate best = {0, 0, 0};
+    each([&](int w, Key key) {
+      const Beam b = beams[w];
+      if (b.score == kNegInf) return;
+      const Candidate cand = {score_of(b, key), key, w};
+      if (before(last, cand) && before(cand, best)) best = cand;
+    });
     for (int o = 16; o; o >>= 1) {
       const Candidate other = {__shfl_xor_sync(~0u, best.score, o), __shfl_xor_sync(~0u, best.key, o),
                                __shfl_xor_sync(~0u, best.beam, o)};
@@ -394,7 +464,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     }
     if (lane == 0) found[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w)
+    for (int w = 0; w < kThreads / 32; ++w)
       if (before(found[w], best)) best = found[w];
     __syncthreads();
     if (threadIdx.x == 0) write_out(p, seq, k, best);
@@ -404,10 +474,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
 
 }  // namespace
 
-// Segments of a row: rows are cut until the grid has some eight blocks an SM (what fits at
-// once), but no finer than a tile.
+// Segments of a row: rows are cut until the grid has some five blocks an SM (what fits at
+// once), but no finer than half a tile.
 int beam_segments(long long rows, int vocab_size) {
-  const long long want = (152 * 8 + rows - 1) / rows, most = (vocab_size + kTile - 1) / kTile;
+  const long long want = (152 * 5 + rows - 1) / rows, most = (vocab_size + kTile / 2 - 1) / (kTile / 2);
   return static_cast<int>(want < most ? want : most);
 }
 
@@ -433,7 +503,7 @@ cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stre
                         : dtype == PA_F16 ? launch_type<PA_F16>(p, stream)
                                           : launch_type<PA_BF16>(p, stream);
   if (e != cudaSuccess) return e;
-  beam_join_kernel<<<p.num_seqs, kJoinThreads, p.num_beams * sizeof(Beam), stream>>>(p);
+  beam_join_kernel<<<p.num_seqs, kThreads, p.num_beams * sizeof(Beam), stream>>>(p);
   return cudaGetLastError();
 }
 
