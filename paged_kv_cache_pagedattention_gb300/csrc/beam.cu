@@ -17,11 +17,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 16;                   // elements of a tile that one thread holds
 constexpr int kTile = kThreads * kPerThread;
-constexpr int kSpare = 256;                      // kept candidates that do not force a merge
+constexpr int kSpare = 64;                       // kept candidates that do not force a merge
 constexpr int kMaxKeep = PA_MAX_BEAM_CANDIDATES;
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kMaxKeep <= 32 && kMaxKeep <= kSpare, "the threshold is one of 32 group maxima");
+static_assert(kMaxKeep <= 32 && kSpare == 64, "the threshold is one of 32 group maxima");
 
 template <int DT>
 constexpr float largest() {
@@ -88,6 +88,11 @@ __device__ __forceinline__ float thread_threshold(float v, int k, float* values,
   return *result;
 }
 
+// The key of a candidate as it is pushed: its value's bits above its index.
+__device__ __forceinline__ Key key_of(Key pushed) {
+  return make_key(__uint_as_float(static_cast<unsigned>(pushed >> 32)), static_cast<unsigned>(pushed));
+}
+
 struct SegmentShared {
   Key buffer[kTile + kSpare];  // candidates: the k best so far as keys, then (value, index) as they come
   unsigned short picked[kTile + kSpare];  // merge: places of the ones above the threshold
@@ -105,10 +110,40 @@ struct SegmentShared {
 // key, or 0 where there are fewer.
 __device__ Key merge_candidates(SegmentShared& sh, int k, int keys) {
   const int n = sh.count;
+  if (n <= kSpare) {  // the usual case: one warp ranks them, two a lane
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      Key mine[2];
+      sh.best[lane] = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = lane + 32 * i;
+        mine[i] = at < n ? sh.buffer[at] : 0;
+        if (at < n && at >= keys) sh.buffer[at] = mine[i] = key_of(mine[i]);
+      }
+      __syncwarp();
+      int rank[2] = {0, 0};
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const Key other = sh.buffer[j];
+        rank[0] += other > mine[0];
+        rank[1] += other > mine[1];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < n && rank[i] < k) sh.buffer[rank[i]] = sh.best[rank[i]] = mine[i];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = min(n, k);
+    const Key last = sh.best[k - 1];
+    __syncthreads();
+    return last;
+  }
   Key top = 0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     Key key = sh.buffer[i];
-    if (i >= keys) sh.buffer[i] = key = make_key(__uint_as_float(static_cast<unsigned>(key >> 32)), static_cast<unsigned>(key));
+    if (i >= keys) sh.buffer[i] = key = key_of(key);
     top = max(top, key);
   }
   if (threadIdx.x < kMaxKeep) sh.best[threadIdx.x] = 0;
@@ -131,6 +166,26 @@ __device__ Key merge_candidates(SegmentShared& sh, int k, int keys) {
   const Key last = sh.best[k - 1];
   __syncthreads();
   return last;
+}
+
+// Sum of exp(v - m), two elements an instruction but for the exponential.
+__device__ __forceinline__ float exp_sum(const float (&v)[kPerThread], float m) {
+  float even = 0.f, odd = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPerThread; i += 2) {
+    float a, b;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 y, {%5, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "f"(v[i]), "f"(v[i + 1]), "f"(-m), "f"(kLog2e));
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(even), "+f"(odd)
+        : "f"(a), "f"(b));
+  }
+  return even + odd;
 }
 
 // 16 bytes from byte `shift` (0 .. 15) of the 32 in lo and hi.
@@ -190,12 +245,8 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) top = fmaxf(top, v[i]);  // NaN is passed over
-    float sum = 0.f;
     float m2 = fmaxf(m, top);
-    if (m2 != kNegInf) {
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) sum += ex2_approx((v[i] - m2) * kLog2e);
-    }
+    float sum = m2 != kNegInf ? exp_sum(v, m2) : 0.f;
     if (top == INFINITY || sum != sum) {  // NaN and +inf: once more, as -inf and the largest finite value
       top = kNegInf;
 #pragma unroll
@@ -204,11 +255,7 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
         top = fmaxf(top, v[i]);
       }
       m2 = fmaxf(m, top);
-      sum = 0.f;
-      if (m2 != kNegInf) {
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) sum += ex2_approx((v[i] - m2) * kLog2e);
-      }
+      sum = m2 != kNegInf ? exp_sum(v, m2) : 0.f;
     }
     if (m2 != kNegInf) {
       s = s * ex2_approx((m - m2) * kLog2e) + sum;
@@ -217,9 +264,9 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
     if (fresh) {
       least = group_threshold(top, k, sh.float_groups, &sh.float_threshold);
       if (least != kNegInf) threshold = make_key(least, 0xffffffffu);
-      fresh = false;
     }
-    bool full = false;
+    bool full = fresh;  // the first tile's candidates give a sharper threshold at once
+    fresh = false;
     if (top >= least) {
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i) {
@@ -232,9 +279,10 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
       }
     }
     if (__syncthreads_or(full)) {
+      const int kept = sh.count;
       threshold = max(threshold, merge_candidates(sh, k, keys));
       if (threshold != 0) least = key_value(threshold);
-      keys = k;  // the buffer held more than that
+      keys = min(k, kept);
     }
   };
 
@@ -257,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
   };
   load(first);
   for (int base = first; base < end; base += kLoads * kThreads) {
+    const bool whole = base + kLoads * kThreads <= end;
     float v[kPerThread];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -267,12 +316,16 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (DT == PA_F32) {
-          v[i * kVec + j] = at < end ? __uint_as_float(w[j]) : kNegInf;
+          v[i * kVec + j] = __uint_as_float(w[j]);
         } else {
           const float2 f = unpack2<DT>(w[j]);
-          v[i * kVec + 2 * j] = at < end ? f.x : kNegInf;
-          v[i * kVec + 2 * j + 1] = at < end ? f.y : kNegInf;
+          v[i * kVec + 2 * j] = f.x;
+          v[i * kVec + 2 * j + 1] = f.y;
         }
+      }
+      if (!whole && at >= end) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[i * kVec + j] = kNegInf;
       }
     }
     load(base + kLoads * kThreads);
