@@ -168,6 +168,17 @@ __device__ Key merge_candidates(SegmentShared& sh, int k, int keys) {
   return last;
 }
 
+// The largest of v, and of every four.
+__device__ __forceinline__ float maxima(const float (&v)[kPerThread], float (&four)[kPerThread / 4]) {
+  float top = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kPerThread / 4; ++i) {
+    four[i] = fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3]));
+    top = fmaxf(top, four[i]);
+  }
+  return top;
+}
+
 // Sum of exp(v - m), two elements an instruction but for the exponential.
 __device__ __forceinline__ float exp_sum(const float (&v)[kPerThread], float m) {
   float even = 0.f, odd = 0.f;
@@ -242,18 +253,14 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
   bool fresh = true;      // no threshold yet
   // index_of(i): the row's element that v[i] is
   auto take = [&](float (&v)[kPerThread], auto index_of) {
-    float top = kNegInf;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) top = fmaxf(top, v[i]);  // NaN is passed over
+    float four[kPerThread / 4];  // maxima of four elements each; NaN is passed over
+    float top = maxima(v, four);
     float m2 = fmaxf(m, top);
     float sum = m2 != kNegInf ? exp_sum(v, m2) : 0.f;
     if (top == INFINITY || sum != sum) {  // NaN and +inf: once more, as -inf and the largest finite value
-      top = kNegInf;
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        v[i] = fminf(fmaxf(v[i], kNegInf), largest<DT>());
-        top = fmaxf(top, v[i]);
-      }
+      for (int i = 0; i < kPerThread; ++i) v[i] = fminf(fmaxf(v[i], kNegInf), largest<DT>());
+      top = maxima(v, four);
       m2 = fmaxf(m, top);
       sum = m2 != kNegInf ? exp_sum(v, m2) : 0.f;
     }
@@ -269,13 +276,17 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
     fresh = false;
     if (top >= least) {
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        if (!(v[i] >= least) || v[i] == kNegInf) continue;
-        const unsigned index = index_of(i);
-        if (v[i] == least && index > key_index(threshold)) continue;
-        const int at = atomicAdd(&sh.count, 1);
-        sh.buffer[at] = static_cast<Key>(__float_as_uint(v[i])) << 32 | index;
-        full |= at >= kSpare;
+      for (int q = 0; q < kPerThread / 4; ++q) {
+        if (!(four[q] >= least)) continue;
+#pragma unroll
+        for (int i = 4 * q; i < 4 * q + 4; ++i) {
+          if (!(v[i] >= least) || v[i] == kNegInf) continue;
+          const unsigned index = index_of(i);
+          if (v[i] == least && index > key_index(threshold)) continue;
+          const int at = atomicAdd(&sh.count, 1);
+          sh.buffer[at] = static_cast<Key>(__float_as_uint(v[i])) << 32 | index;
+          full |= at >= kSpare;
+        }
       }
     }
     if (__syncthreads_or(full)) {
@@ -347,11 +358,13 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamParams
     sh.s[warp] = s;
   }
   __syncthreads();
-  merge_candidates(sh, k, keys);
+  if (fresh || sh.count > keys) merge_candidates(sh, k, keys);  // else `best` is up to date
   const long long part = row * p.num_segments + seg;
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) join_state(m, s, sh.m[w], sh.s[w]);
-    p.state[part] = make_float2(m, s);
+  if (warp == 0) {
+    m = lane < kWarps ? sh.m[lane] : kNegInf;
+    s = lane < kWarps ? sh.s[lane] : 0.f;
+    for (int o = kWarps / 2; o; o >>= 1) join_state(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+    if (lane == 0) p.state[part] = make_float2(m, s);
   }
   if (threadIdx.x < k) p.keys[part * k + threadIdx.x] = sh.best[threadIdx.x];
 }
@@ -527,11 +540,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
 
 }  // namespace
 
-// Segments of a row: rows are cut until the grid has some five blocks an SM (what fits at
-// once), but no finer than half a tile.
+// Segments of a row: rows are cut as long as the grid fits at once (four blocks an SM), but
+// no finer than half a tile.
 int beam_segments(long long rows, int vocab_size) {
-  const long long want = (152 * 5 + rows - 1) / rows, most = (vocab_size + kTile / 2 - 1) / (kTile / 2);
-  return static_cast<int>(want < most ? want : most);
+  const long long fit = 152 * 4 / rows, most = (vocab_size + kTile / 2 - 1) / (kTile / 2);
+  return static_cast<int>(fit < 1 ? 1 : fit < most ? fit : most);
 }
 
 template <int DT, bool kShifted>
