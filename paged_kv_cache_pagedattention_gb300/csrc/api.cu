@@ -676,6 +676,7 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
   if (cache_dtype == PA_NVFP4 ? !nvfp4_shape_ok(head_size, block_size) : (head_size * dtype_bytes(cache_dtype)) % 16)
     return PA_ERR_UNSUPPORTED;
   const int64_t q_width = (int64_t)num_q_heads * head_size, kv_width = (int64_t)num_kv_heads * head_size;
+  if (q_width > INT32_MAX || kv_width > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;  // a token's row by 32-bit places
   if (num_tokens > 1 && (key_stride < kv_width || value_stride < kv_width ||
                          (num_q_heads > 0 && (q_stride < q_width || q_out_stride < q_width))))
     return PA_ERR_INVALID_ARG;

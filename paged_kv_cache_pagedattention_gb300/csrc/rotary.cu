@@ -207,12 +207,25 @@ __device__ __forceinline__ void store_unit(const RotaryParams& p, void* cache, l
   }
 }
 
-// N elements of a row in whole pieces.
+// N elements of a row in whole pieces: loaded, and as fp32.
 template <int SRC, int N>
-__device__ __forceinline__ void load_unit(const typename Elem<SRC>::T* src, float (&x)[N]) {
+struct Unit {
+  static constexpr int kPieces = N / Piece<SRC>::n;
+  uint4 raw[kPieces];
+  __device__ __forceinline__ void load(const typename Elem<SRC>::T* src) {
 #pragma unroll
-  for (int i = 0; i < N; i += Piece<SRC>::n)
-    Piece<SRC>::unpack(reinterpret_cast<const uint4*>(src)[i / Piece<SRC>::n], x + i);
+    for (int i = 0; i < kPieces; ++i) raw[i] = reinterpret_cast<const uint4*>(src)[i];
+  }
+  __device__ __forceinline__ void values(float (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) Piece<SRC>::unpack(raw[i], x + i * Piece<SRC>::n);
+  }
+};
+
+__device__ __forceinline__ void rotate(float& x, float& y, float2 cs) {
+  const float a = x, b = y;
+  x = a * cs.x - b * cs.y;
+  y = b * cs.x + a * cs.y;
 }
 
 // The rotations of a token lie in shared memory by the pair's place in its piece, then by
@@ -224,7 +237,8 @@ __device__ __forceinline__ float2 rotation_of(const float2* table, int pieces, i
 
 // One block a token.  Its R / 2 rotations are formed once, for all heads, in shared memory;
 // then every thread moves units of rows: a piece of q (two, one of each half, for pairs
-// (i, i + R / 2)) or kv_unit elements of k or v.
+// (i, i + R / 2)) or kv_unit elements of k or v.  A thread's first unit of each kind is
+// loaded before anything else, so its way from memory and the rotations' overlap.
 template <int SRC, int CDT, bool kInterleaved>
 __global__ void __launch_bounds__(256) rotary_piece_kernel(const RotaryParams p) {
   using T = typename Elem<SRC>::T;
@@ -232,105 +246,106 @@ __global__ void __launch_bounds__(256) rotary_piece_kernel(const RotaryParams p)
   constexpr int kPairs = kInterleaved ? kQ / 2 : kQ;  // pairs whose rotations a q piece needs
   extern __shared__ float2 table[];
   const long long t = blockIdx.x;
-  const long long slot = p.slot_mapping[t];
-  if (slot < 0) return;
-  if (slot >= (long long)p.num_blocks * p.block_size) {
-    if (threadIdx.x == 0) flag_error(p.err, PA_ERRFLAG_SLOT);
-    return;
-  }
   const int d = p.head_size, rot = p.rotary_dim, half = rot / 2;
-  const int pieces = half / kPairs;
-  const int pos = p.positions[t];
-  for (int i = threadIdx.x; i < half; i += blockDim.x)
-    table[i % kPairs * pieces + i / kPairs] = rotation(pos, turn_fraction(p.inv_freq[i]), p.attn_factor);
-  __syncthreads();
   const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
   T* q_out = static_cast<T*>(p.q_out) + t * p.q_out_stride;
-  const int q_units = p.num_q_heads * pieces;
-  for (int u = threadIdx.x; u < q_units; u += blockDim.x) {
-    const int h = u / pieces, c = u % pieces;
-    if constexpr (kInterleaved) {
-      const int j = h * d + c * kQ;
-      float x[kQ];
-      load_unit<SRC>(q + j, x);
-#pragma unroll
-      for (int i = 0; i < kQ; i += 2) {
-        const float2 cs = rotation_of<kPairs>(table, pieces, c * kPairs + i / 2);
-        const float a = x[i], b = x[i + 1];
-        x[i] = a * cs.x - b * cs.y;
-        x[i + 1] = b * cs.x + a * cs.y;
-      }
-      *reinterpret_cast<uint4*>(q_out + j) = Piece<SRC>::pack(x);
-    } else {
-      const int j = h * d + c * kQ;
-      float x[kQ], y[kQ];
-      load_unit<SRC>(q + j, x);
-      load_unit<SRC>(q + j + half, y);
-#pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const float2 cs = rotation_of<kPairs>(table, pieces, c * kPairs + i);
-        const float a = x[i], b = y[i];
-        x[i] = a * cs.x - b * cs.y;
-        y[i] = b * cs.x + a * cs.y;
-      }
-      *reinterpret_cast<uint4*>(q_out + j) = Piece<SRC>::pack(x);
-      *reinterpret_cast<uint4*>(q_out + j + half) = Piece<SRC>::pack(y);
-    }
-  }
-  if (rot < d && q != q_out) {
-    const int rest = (d - rot) / kQ;
-    for (int u = threadIdx.x; u < p.num_q_heads * rest; u += blockDim.x) {
-      const int j = u / rest * d + rot + u % rest * kQ;
-      *reinterpret_cast<uint4*>(q_out + j) = *reinterpret_cast<const uint4*>(q + j);
-    }
-  }
   const T* key = static_cast<const T*>(p.key) + t * p.key_stride;
   const T* value = static_cast<const T*>(p.value) + t * p.value_stride;
+  const int pieces = half / kPairs, k_pieces = kInterleaved ? rot / kKv : half / kKv;
+  const int k_rest = (d - rot) / kKv, plain = k_rest + d / kKv;  // k behind the rotated elements, and v
+  const int q_units = p.num_q_heads * pieces, k_units = p.num_kv_heads * k_pieces, plain_units = p.num_kv_heads * plain;
+
+  // first elements of the units
+  auto q_at = [&](int u) { return u / pieces * d + u % pieces * kQ; };
+  auto k_at = [&](int u) { return u / k_pieces * d + u % k_pieces * kKv; };
+  Unit<SRC, kQ> qx, qy;
+  auto load_q = [&](int u) {
+    if (u >= q_units) return;
+    qx.load(q + q_at(u));
+    if constexpr (!kInterleaved) qy.load(q + q_at(u) + half);
+  };
+  Unit<SRC, kKv> kx, ky, vx;
+  auto load_k = [&](int u) {
+    if (u >= k_units) return;
+    kx.load(key + k_at(u));
+    if constexpr (!kInterleaved) ky.load(key + k_at(u) + half);
+  };
+  auto load_plain = [&](int u) {
+    if (u >= plain_units) return;
+    const int h = u / plain, c = u % plain;
+    vx.load(c < k_rest ? key + h * d + rot + c * kKv : value + h * d + (c - k_rest) * kKv);
+  };
+  // the units are dealt round, so that the threads without a second q unit take k and v
+  const int k_first = (threadIdx.x + 256 - q_units % 256) % 256;
+  const int plain_first = (threadIdx.x + 512 - (q_units + k_units) % 256) % 256;
+  load_q(threadIdx.x);
+  load_k(k_first);
+  load_plain(plain_first);
+
+  const long long slot = p.slot_mapping[t];
+  const int pos = p.positions[t];
+  for (int i = threadIdx.x; i < half; i += 256)
+    table[i % kPairs * pieces + i / kPairs] = rotation(pos, turn_fraction(p.inv_freq[i]), p.attn_factor);
+  if (slot < 0 || slot >= (long long)p.num_blocks * p.block_size) {
+    if (slot >= 0 && threadIdx.x == 0) flag_error(p.err, PA_ERRFLAG_SLOT);
+    return;
+  }
   const long long tile0 = slot / p.block_size * p.num_kv_heads;
   const int off = static_cast<int>(slot % p.block_size);
-  const int k_pieces = kInterleaved ? rot / kKv : half / kKv;
-  for (int u = threadIdx.x; u < p.num_kv_heads * k_pieces; u += blockDim.x) {
-    const int h = u / k_pieces, j = u % k_pieces * kKv;
-    const float scale = SRC == CDT ? 1.f : p.k_scale[h * p.scale_stride];
-    float x[kKv];
-    load_unit<SRC>(key + h * d + j, x);
+  for (int u = plain_first; u < plain_units; u += 256) {
+    if (u != plain_first) load_plain(u);
+    const int h = u / plain, c = u % plain;
+    const bool is_v = c >= k_rest;
+    const int j = is_v ? (c - k_rest) * kKv : rot + c * kKv;
+    void* cache = is_v ? p.v_cache : p.k_cache;
+    if constexpr (SRC == CDT) {
+      T* dst = static_cast<T*>(cache) + ((tile0 + h) * p.block_size + off) * d + j;
+      *reinterpret_cast<uint4*>(dst) = vx.raw[0];
+    } else {
+      float x[kKv];
+      vx.values(x);
+      store_unit<SRC, CDT>(p, cache, tile0 + h, off, j, x, (is_v ? p.v_scale : p.k_scale)[h * p.scale_stride]);
+    }
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < q_units; u += 256) {
+    if (u != static_cast<int>(threadIdx.x)) load_q(u);
+    const int c = u % pieces;
+    float x[kQ], y[kQ];
+    qx.values(x);
     if constexpr (kInterleaved) {
 #pragma unroll
-      for (int i = 0; i < kKv; i += 2) {
-        const float2 cs = rotation_of<kPairs>(table, pieces, (j + i) / 2);
-        const float a = x[i], b = x[i + 1];
-        x[i] = a * cs.x - b * cs.y;
-        x[i + 1] = b * cs.x + a * cs.y;
-      }
+      for (int i = 0; i < kQ; i += 2) rotate(x[i], x[i + 1], rotation_of<kPairs>(table, pieces, c * kPairs + i / 2));
     } else {
-      float y[kKv];
-      load_unit<SRC>(key + h * d + j + half, y);
+      qy.values(y);
 #pragma unroll
-      for (int i = 0; i < kKv; ++i) {
-        const float2 cs = rotation_of<kPairs>(table, pieces, j + i);
-        const float a = x[i], b = y[i];
-        x[i] = a * cs.x - b * cs.y;
-        y[i] = b * cs.x + a * cs.y;
-      }
+      for (int i = 0; i < kQ; ++i) rotate(x[i], y[i], rotation_of<kPairs>(table, pieces, c * kPairs + i));
+      *reinterpret_cast<uint4*>(q_out + q_at(u) + half) = Piece<SRC>::pack(y);
+    }
+    *reinterpret_cast<uint4*>(q_out + q_at(u)) = Piece<SRC>::pack(x);
+  }
+  for (int u = k_first; u < k_units; u += 256) {
+    if (u != k_first) load_k(u);
+    const int h = u / k_pieces, j = u % k_pieces * kKv;
+    const float scale = SRC == CDT ? 1.f : p.k_scale[h * p.scale_stride];
+    float x[kKv], y[kKv];
+    kx.values(x);
+    if constexpr (kInterleaved) {
+#pragma unroll
+      for (int i = 0; i < kKv; i += 2) rotate(x[i], x[i + 1], rotation_of<kPairs>(table, pieces, (j + i) / 2));
+    } else {
+      ky.values(y);
+#pragma unroll
+      for (int i = 0; i < kKv; ++i) rotate(x[i], y[i], rotation_of<kPairs>(table, pieces, j + i));
       store_unit<SRC, CDT>(p, p.k_cache, tile0 + h, off, j + half, y, scale);
     }
     store_unit<SRC, CDT>(p, p.k_cache, tile0 + h, off, j, x, scale);
   }
-  // what is not rotated: k behind the rotated elements, and v
-  const int k_rest = (d - rot) / kKv, v_pieces = d / kKv, plain = k_rest + v_pieces;
-  for (int u = threadIdx.x; u < p.num_kv_heads * plain; u += blockDim.x) {
-    const int h = u / plain, c = u % plain;
-    const bool is_v = c >= k_rest;
-    const int j = is_v ? (c - k_rest) * kKv : rot + c * kKv;
-    const T* src = (is_v ? value : key) + h * d + j;
-    void* cache = is_v ? p.v_cache : p.k_cache;
-    if constexpr (SRC == CDT) {
-      T* dst = static_cast<T*>(cache) + ((tile0 + h) * p.block_size + off) * d + j;
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-    } else {
-      float x[kKv];
-      load_unit<SRC>(src, x);
-      store_unit<SRC, CDT>(p, cache, tile0 + h, off, j, x, (is_v ? p.v_scale : p.k_scale)[h * p.scale_stride]);
+  if (rot < d && q != q_out) {
+    const int rest = (d - rot) / kQ;
+    for (int u = threadIdx.x; u < p.num_q_heads * rest; u += 256) {
+      const int j = u / rest * d + rot + u % rest * kQ;
+      *reinterpret_cast<uint4*>(q_out + j) = *reinterpret_cast<const uint4*>(q + j);
     }
   }
 }
