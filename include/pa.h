@@ -272,7 +272,7 @@ pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rot
  *   rotary_dim   even, 2 .. head_size; attn_factor positive and finite
  *   the rest as pa_reshape_and_cache; q, q_out, key and value need only their element's
  *   alignment.  Where they are 16-byte aligned with strides to match, and the rotated
- *   part is whole 16-byte pieces (16 elements for FP8 and NVFP4 caches; per half for
+ *   part is whole 16-byte pieces (8 elements for FP8, 16 for NVFP4 caches; per half for
  *   pairs (i, i + R/2)), rows move in 16-byte pieces, else element by element.
  */
 pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,

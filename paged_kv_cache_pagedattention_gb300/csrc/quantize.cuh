@@ -14,6 +14,13 @@ __device__ __forceinline__ uint8_t quant_fp8(float x, float scale) {
                                                     CDT == PA_FP8_E5M2 ? __NV_E5M2 : __NV_E4M3));
 }
 
+// The codes of two values, a's in the low byte.
+template <int CDT>
+__device__ __forceinline__ uint16_t quant_fp8x2(float a, float b, float scale) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE,
+                                  CDT == PA_FP8_E5M2 ? __NV_E5M2 : __NV_E4M3);
+}
+
 // E2M1 code of y: round to nearest with ties to the even code, saturating at 6,
 // sign kept.  The magnitude code counts the midpoints between neighbouring E2M1
 // magnitudes (0, 0.5, 1, 1.5, 2, 3, 4, 6) that |y| lies above; at a midpoint the

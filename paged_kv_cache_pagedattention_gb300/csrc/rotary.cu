@@ -179,9 +179,11 @@ struct Piece {  // 16 bytes of elements as fp32
   }
 };
 
-// Elements of a k or v row that one thread stores: one piece, or 16 codes.
+// Elements of a k or v row that one thread stores: one piece, 8 FP8 codes, or a group of 16
+// NVFP4 codes.  (A division an element makes the codes dear: with 16 FP8 codes a thread, 96 of
+// 256 threads had twice the work.)
 template <int SRC, int CDT>
-constexpr int kv_unit() { return SRC == CDT ? Piece<SRC>::n : 16; }
+constexpr int kv_unit() { return SRC == CDT ? Piece<SRC>::n : CDT == PA_NVFP4 ? 16 : 8; }
 
 // Store kv_unit elements x of row (tile, off) at element j of a cache.
 template <int SRC, int CDT>
@@ -199,11 +201,12 @@ __device__ __forceinline__ void store_unit(const RotaryParams& p, void* cache, l
     *reinterpret_cast<uint2*>(dst + (long long)off * (d / 2) + j / 2) = codes;
     dst[(long long)p.block_size * (d / 2) + (long long)off * (d / 16) + j / 16] = block_scale;
   } else {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i / 4] |= static_cast<uint32_t>(quant_fp8<CDT>(x[i], scale)) << (8 * (i % 4));
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + (tile * p.block_size + off) * d + j) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 8; i += 2)
+      w[i / 4] |= static_cast<uint32_t>(quant_fp8x2<CDT>(x[i], x[i + 1], scale)) << (8 * (i % 4));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + (tile * p.block_size + off) * d + j) =
+        make_uint2(w[0], w[1]);
   }
 }
 
@@ -239,8 +242,14 @@ __device__ __forceinline__ float2 rotation_of(const float2* table, int pieces, i
 // then every thread moves units of rows: a piece of q (two, one of each half, for pairs
 // (i, i + R / 2)) or kv_unit elements of k or v.  A thread's first unit of each kind is
 // loaded before anything else, so its way from memory and the rotations' overlap.
+//
+// Bound by memory once there are some thousand tokens, by its chain of latencies (slot,
+// position and rows, then the rotations) below; what counts is how many tokens are on their
+// way, so registers are held to 32 for eight blocks an SM (8,192 tokens of 64/8 heads, pairs
+// side by side: 52 us, 6.4 TB/s, against 61 us with five blocks and no spills; FP8 cache
+// 54 against 66 us).
 template <int SRC, int CDT, bool kInterleaved>
-__global__ void __launch_bounds__(256) rotary_piece_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(256, CDT == PA_NVFP4 ? 4 : 8) rotary_piece_kernel(const RotaryParams p) {
   using T = typename Elem<SRC>::T;
   constexpr int kQ = Piece<SRC>::n, kKv = kv_unit<SRC, CDT>();
   constexpr int kPairs = kInterleaved ? kQ / 2 : kQ;  // pairs whose rotations a q piece needs
@@ -307,17 +316,30 @@ __global__ void __launch_bounds__(256) rotary_piece_kernel(const RotaryParams p)
       store_unit<SRC, CDT>(p, cache, tile0 + h, off, j, x, (is_v ? p.v_scale : p.k_scale)[h * p.scale_stride]);
     }
   }
+  if (rot < d && q != q_out) {
+    const int rest = (d - rot) / kQ, rest_units = p.num_q_heads * rest;
+    for (int u = threadIdx.x; u < rest_units; u += 2 * 256) {
+      const int u2 = u + 256;
+      const int j = u / rest * d + rot + u % rest * kQ, j2 = u2 / rest * d + rot + u2 % rest * kQ;
+      const uint4 a = *reinterpret_cast<const uint4*>(q + j);
+      uint4 b;
+      if (u2 < rest_units) b = *reinterpret_cast<const uint4*>(q + j2);
+      *reinterpret_cast<uint4*>(q_out + j) = a;
+      if (u2 < rest_units) *reinterpret_cast<uint4*>(q_out + j2) = b;
+    }
+  }
   __syncthreads();
   for (int u = threadIdx.x; u < q_units; u += 256) {
-    if (u != static_cast<int>(threadIdx.x)) load_q(u);
     const int c = u % pieces;
     float x[kQ], y[kQ];
+    if (!kInterleaved && u != static_cast<int>(threadIdx.x)) load_q(u);
     qx.values(x);
+    if constexpr (kInterleaved) load_q(u + 256);
+    else qy.values(y);
     if constexpr (kInterleaved) {
 #pragma unroll
       for (int i = 0; i < kQ; i += 2) rotate(x[i], x[i + 1], rotation_of<kPairs>(table, pieces, c * kPairs + i / 2));
     } else {
-      qy.values(y);
 #pragma unroll
       for (int i = 0; i < kQ; ++i) rotate(x[i], y[i], rotation_of<kPairs>(table, pieces, c * kPairs + i));
       *reinterpret_cast<uint4*>(q_out + q_at(u) + half) = Piece<SRC>::pack(y);
@@ -325,28 +347,21 @@ __global__ void __launch_bounds__(256) rotary_piece_kernel(const RotaryParams p)
     *reinterpret_cast<uint4*>(q_out + q_at(u)) = Piece<SRC>::pack(x);
   }
   for (int u = k_first; u < k_units; u += 256) {
-    if (u != k_first) load_k(u);
     const int h = u / k_pieces, j = u % k_pieces * kKv;
     const float scale = SRC == CDT ? 1.f : p.k_scale[h * p.scale_stride];
     float x[kKv], y[kKv];
+    if (u != k_first) load_k(u);
     kx.values(x);
+    if constexpr (!kInterleaved) ky.values(y);
     if constexpr (kInterleaved) {
 #pragma unroll
       for (int i = 0; i < kKv; i += 2) rotate(x[i], x[i + 1], rotation_of<kPairs>(table, pieces, (j + i) / 2));
     } else {
-      ky.values(y);
 #pragma unroll
       for (int i = 0; i < kKv; ++i) rotate(x[i], y[i], rotation_of<kPairs>(table, pieces, j + i));
       store_unit<SRC, CDT>(p, p.k_cache, tile0 + h, off, j + half, y, scale);
     }
     store_unit<SRC, CDT>(p, p.k_cache, tile0 + h, off, j, x, scale);
-  }
-  if (rot < d && q != q_out) {
-    const int rest = (d - rot) / kQ;
-    for (int u = threadIdx.x; u < p.num_q_heads * rest; u += 256) {
-      const int j = u / rest * d + rot + u % rest * kQ;
-      *reinterpret_cast<uint4*>(q_out + j) = *reinterpret_cast<const uint4*>(q + j);
-    }
   }
 }
 
@@ -361,7 +376,7 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
   constexpr int kBytes = Elem<SRC>::bytes, kKv = kv_unit<SRC, CDT>();
   const int half = p.rotary_dim / 2;
   // Pieces where every row allows them: on 2,176 tokens of 32/8 heads of 128 bf16 the pieces
-  // took PIECE_US us and the generic kernel, which forms a rotation for every head, 82 us.
+  // take 13 us and the generic kernel, which forms a rotation for every head, 82 us.
   const bool pieces = (p.interleaved ? p.rotary_dim : half) % kKv == 0 &&
                       aligned16(p.key, p.key_stride, p.num_tokens, kBytes) &&
                       aligned16(p.value, p.value_stride, p.num_tokens, kBytes) &&
@@ -375,7 +390,7 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
     return cudaGetLastError();
   }
   const long long per_token = (long long)p.num_q_heads * ((half + 3) / 4 + (p.head_size - p.rotary_dim + 7) / 8) +
-                              2ll * (p.head_size / kKv) * p.num_kv_heads;
+                              2ll * (p.head_size / (SRC == CDT ? kKv : 16)) * p.num_kv_heads;
   const long long blocks = (per_token * p.num_tokens + 255) / 256;
   rotary_generic_kernel<SRC, CDT><<<static_cast<int>(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, stream>>>(p);
   return cudaGetLastError();
