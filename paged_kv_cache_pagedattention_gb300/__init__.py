@@ -140,16 +140,17 @@ def kv_code(cache: torch.Tensor, k_scale=None) -> int:
 def cache_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, head_size: int):
     """(num_blocks, num_kv_heads, block_size, head_size) of a K/V cache pair; the
     head size of an NVFP4 cache comes from the caller's query or key tensor."""
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must match")
-    if is_nvfp4(k_cache):
-        nb, hkv, tile = k_cache.shape
+    if len(shape) == 3 and k_cache.dtype == torch.uint8:
+        nb, hkv, tile = shape
         if head_size < 1 or (16 * tile) % (9 * head_size):
             raise ValueError("NVFP4 cache: tile_bytes must be 9 * block_size * head_size / 16")
         return nb, hkv, 16 * tile // (9 * head_size), head_size
-    if k_cache.dim() != 4:
+    if len(shape) != 4:
         raise ValueError("cache must be [num_blocks][num_kv_heads][block_size][head_size]")
-    return tuple(k_cache.shape)
+    return tuple(shape)
 
 
 def _ptr(t) -> int | None:
@@ -202,41 +203,41 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
     if not block_mapping.is_contiguous():
         raise ValueError("block_mapping must be contiguous")
     n = block_mapping.shape[0]
-    _check(_lib.pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_mapping) if n else None, n, nb, hkv, d,
-                               bs, kv_code(k_cache), _stream(stream)), "pa_copy_blocks")
+    k_ptr, v_ptr = _ptr(k_cache), _ptr(v_cache)
+    s = _raw_stream(_current_device()) if stream is None else stream.cuda_stream
+    _check(_lib.pa_copy_blocks(k_ptr, v_ptr, _ptr(block_mapping) if n else None, n, nb, hkv, d, bs,
+                               kv_code(k_cache), s), "pa_copy_blocks")
 
 
-# The raw handle of a device's current stream; torch.cuda.current_stream builds an object
-# first (1.1 against 0.1 us on the host).
+# A device's current stream and the current device as torch keeps them.  Their public forms
+# (torch.cuda.current_stream, torch.cuda.current_device) take 1.1 and 0.2 us on the host, these
+# 0.1; the calls below take 6 to 10.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_int32 = torch.int32
 
 
-def _launch(fn, where, tensors, stream, *args):
-    """Call fn(*args, stream) on the tensors' device: on the current stream of that device, or
-    on the caller's, which has to belong to it."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != index or index < 0:
-            raise ValueError(f"{where}: expected CUDA tensors on one device")
-    if stream is None:
-        raw = _raw_stream(index)
-    elif stream.device.index != index:
+def _on_device(index, call, *args, **kwargs):
+    """``call`` again with the tensors' device current; refuses tensors that are not CUDA's."""
+    if index < 0:
+        raise ValueError(f"{call.__name__}: expected CUDA tensors")
+    with torch.cuda.device(index):
+        return call(*args, **kwargs)
+
+
+def _stream_on(stream, index, where):
+    """The raw handle of the caller's stream, which has to be on device ``index``."""
+    if stream.device.index != index:
         raise ValueError(f"{where}: the stream belongs to another device than the tensors")
-    else:
-        raw = stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, raw)
-    if st != PA_OK:
-        raise PAError(st, where)
+    return stream.cuda_stream
 
 
-def _check_int32(t, shape, what):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+def _bad(t, shape, what):
+    """Refuse a tensor that is not contiguous int32 of ``shape``, or is on another device."""
+    if t.dtype is not _int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)}")
+    raise ValueError(f"{what}: all tensors must be on one CUDA device")
 
 
 def _row_stride(t, heads, d, what):
@@ -268,24 +269,25 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
     [T]), and write key and value into the paged caches at slot_mapping (int64 [T]; a negative
     slot skips the token).  inv_freq float32 [rotary_dim/2].  q, key and value may be slices of
     one projection (any distance between tokens).  q and q_out None: keys only."""
-    shape, dtype = key.shape, key.dtype
+    shape, dtype, dev = key.shape, key.dtype, key.get_device()
     if len(shape) != 3 or value.shape != shape or value.dtype is not dtype:
         raise ValueError("key/value must be [num_tokens][num_kv_heads][head_size] of one dtype")
     t, hkv, d = shape
     nb, heads, bs, head = cache_geometry(k_cache, v_cache, d)
     if heads != hkv or head != d or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous and match key's heads")
-    tensors = [key, value, k_cache, v_cache, positions, slot_mapping, inv_freq]
     hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None or q.dim() != 3 or q_out.shape != q.shape or q.dtype is not dtype or \
                 q_out.dtype is not dtype or q.shape[0] != t or q.shape[2] != d:
             raise ValueError("q/q_out must be [num_tokens][num_q_heads][head_size] of key's dtype")
+        if q.get_device() != dev or q_out.get_device() != dev:
+            raise ValueError("q/q_out: all tensors must be on one CUDA device")
         hq = q.shape[1]
         q_ptr, q_stride = q.data_ptr(), _row_stride(q, hq, d, "q")
         q_out_ptr, q_out_stride = q_out.data_ptr(), _row_stride(q_out, hq, d, "q_out")
-        tensors += [q, q_out]
-    _check_int32(positions, (t,), "positions")
+    if positions.dtype is not _int32 or positions.shape != (t,) or not positions.is_contiguous():
+        _bad(positions, (t,), "positions")
     if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (t,) or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [num_tokens]")
     if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -295,15 +297,23 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
     if code >= PA_FP8_E4M3 and k_scale is not None and v_scale is not None:
         for scale in (k_scale, v_scale):
             if scale.dtype is not torch.float32 or not scale.is_contiguous() or scale.numel() != k_scale.numel() or \
-                    scale.numel() not in (1, hkv):
-                raise ValueError("scales: float32, both one per tensor or both one per KV head")
+                    scale.numel() not in (1, hkv) or scale.get_device() != dev:
+                raise ValueError("scales: float32, both one per tensor or both one per KV head, on the caches' device")
         k_scale_ptr, v_scale_ptr = k_scale.data_ptr(), v_scale.data_ptr()
-        tensors += [k_scale, v_scale]
-    _launch(_lib.pa_rotary_and_cache, "pa_rotary_and_cache", tensors, stream, q_out_ptr, q_ptr, key.data_ptr(),
-            value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
-            inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.shape[0], bs, 1 if interleaved else 0, attn_factor,
-            q_out_stride, q_stride, _row_stride(key, hkv, d, "key"), _row_stride(value, hkv, d, "value"),
-            dtype_code(key), code, k_scale_ptr, v_scale_ptr)
+    if not (value.get_device() == k_cache.get_device() == v_cache.get_device() == positions.get_device() ==
+            slot_mapping.get_device() == inv_freq.get_device() == dev):
+        raise ValueError("pa_rotary_and_cache: all tensors must be on one CUDA device")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_rotary_and_cache, q_out, q, key, value, k_cache, v_cache, positions, slot_mapping,
+                          inv_freq, interleaved, attn_factor, k_scale, v_scale, stream)
+    st = _lib.pa_rotary_and_cache(
+        q_out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.shape[0],
+        bs, 1 if interleaved else 0, attn_factor, q_out_stride, q_stride, _row_stride(key, hkv, d, "key"),
+        _row_stride(value, hkv, d, "value"), dtype_code(key), code, k_scale_ptr, v_scale_ptr,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_rotary_and_cache"))
+    if st != PA_OK:
+        raise PAError(st, "pa_rotary_and_cache")
 
 
 def pa_beam_select_workspace_size(num_seqs, num_beams, vocab_size, num_candidates) -> int:
@@ -322,26 +332,41 @@ def pa_beam_select(out_scores, out_tokens, out_parents, logits, beam_scores, wor
     if out_scores.dim() != 2 or out_scores.shape[0] != b or out_scores.dtype is not torch.float32 or \
             not out_scores.is_contiguous():
         raise ValueError("out_scores must be a contiguous float32 tensor [num_seqs][num_candidates]")
-    shape = out_scores.shape
-    _check_int32(out_tokens, shape, "out_tokens")
-    _check_int32(out_parents, shape, "out_parents")
+    shape, dev = out_scores.shape, logits.get_device()
+    if out_tokens.dtype is not _int32 or out_tokens.shape != shape or not out_tokens.is_contiguous():
+        _bad(out_tokens, shape, "out_tokens")
+    if out_parents.dtype is not _int32 or out_parents.shape != shape or not out_parents.is_contiguous():
+        _bad(out_parents, shape, "out_parents")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _launch(_lib.pa_beam_select, "pa_beam_select", (logits, beam_scores, out_scores, out_tokens, out_parents, workspace),
-            stream, out_scores.data_ptr(), out_tokens.data_ptr(), out_parents.data_ptr(), logits.data_ptr(),
-            logits.stride(0), beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits),
-            workspace.data_ptr(), workspace.nbytes)
+    if not (beam_scores.get_device() == out_scores.get_device() == out_tokens.get_device() ==
+            out_parents.get_device() == workspace.get_device() == dev):
+        raise ValueError("pa_beam_select: all tensors must be on one CUDA device")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_beam_select, out_scores, out_tokens, out_parents, logits, beam_scores, workspace,
+                          stream)
+    st = _lib.pa_beam_select(
+        out_scores.data_ptr(), out_tokens.data_ptr(), out_parents.data_ptr(), logits.data_ptr(), logits.stride(0),
+        beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_beam_select"))
+    if st != PA_OK:
+        raise PAError(st, "pa_beam_select")
 
 
 def _pages(block_tables, seq_lens, ref_counts):
-    """(rows, max_blocks_per_seq, num_blocks) of a pool's arrays."""
-    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+    """(rows, max_blocks_per_seq, num_blocks, device) of a pool's arrays."""
+    shape, blocks, dev = block_tables.shape, ref_counts.shape, block_tables.get_device()
+    if len(shape) != 2 or len(blocks) != 1:
         raise ValueError("block_tables must be [rows][max_blocks_per_seq] and ref_counts [num_blocks]")
-    n, width = shape = block_tables.shape
-    _check_int32(block_tables, shape, "block_tables")
-    _check_int32(seq_lens, (n,), "seq_lens")
-    _check_int32(ref_counts, ref_counts.shape, "ref_counts")
-    return n, width, ref_counts.shape[0]
+    n, width = shape
+    if block_tables.dtype is not _int32 or not block_tables.is_contiguous():
+        _bad(block_tables, shape, "block_tables")
+    if seq_lens.dtype is not _int32 or seq_lens.shape != (n,) or not seq_lens.is_contiguous() or \
+            seq_lens.get_device() != dev:
+        _bad(seq_lens, (n,), "seq_lens")
+    if ref_counts.dtype is not _int32 or not ref_counts.is_contiguous() or ref_counts.get_device() != dev:
+        _bad(ref_counts, blocks, "ref_counts")
+    return n, width, blocks[0], dev
 
 
 def pa_fork_blocks(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts, block_size,
@@ -349,17 +374,25 @@ def pa_fork_blocks(block_tables_out, seq_lens_out, block_tables, seq_lens, paren
     """Children rows take the blocks and lengths of rows ``parents`` (int32 [children];
     negative: an empty row) of block_tables/seq_lens; ref_counts int32 [num_blocks] counts
     the holders of every block.  See pa.h."""
-    m, width, blocks = _pages(block_tables, seq_lens, ref_counts)
-    if parents.dim() != 1:
-        raise ValueError("parents must be int32 [children]")
-    n = parents.shape[0]
-    _check_int32(parents, (n,), "parents")
-    _check_int32(block_tables_out, (n, width), "block_tables_out")
-    _check_int32(seq_lens_out, (n,), "seq_lens_out")
-    _launch(_lib.pa_fork_blocks, "pa_fork_blocks",
-            (block_tables_out, seq_lens_out, block_tables, seq_lens, parents, ref_counts), stream,
-            block_tables_out.data_ptr(), seq_lens_out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            parents.data_ptr(), ref_counts.data_ptr(), n, m, width, blocks, block_size)
+    m, width, blocks, dev = _pages(block_tables, seq_lens, ref_counts)
+    n = parents.numel()
+    if parents.dtype is not _int32 or parents.dim() != 1 or not parents.is_contiguous() or parents.get_device() != dev:
+        _bad(parents, (n,), "parents")
+    if block_tables_out.dtype is not _int32 or block_tables_out.shape != (n, width) or \
+            not block_tables_out.is_contiguous() or block_tables_out.get_device() != dev:
+        _bad(block_tables_out, (n, width), "block_tables_out")
+    if seq_lens_out.dtype is not _int32 or seq_lens_out.shape != (n,) or not seq_lens_out.is_contiguous() or \
+            seq_lens_out.get_device() != dev:
+        _bad(seq_lens_out, (n,), "seq_lens_out")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_fork_blocks, block_tables_out, seq_lens_out, block_tables, seq_lens, parents,
+                          ref_counts, block_size, stream)
+    st = _lib.pa_fork_blocks(
+        block_tables_out.data_ptr(), seq_lens_out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        parents.data_ptr(), ref_counts.data_ptr(), n, m, width, blocks, block_size,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_fork_blocks"))
+    if st != PA_OK:
+        raise PAError(st, "pa_fork_blocks")
 
 
 def pa_append_workspace_size(num_seqs, total_q_tokens, block_size) -> int:
@@ -371,31 +404,47 @@ def pa_append_blocks(block_tables, seq_lens, query_start_loc, slot_mapping, bloc
     """Room for the next tokens of every row (query_start_loc int32 [rows+1]): blocks from the
     pool, slots (int64 [new tokens]) and copy-on-write pairs (block_mapping int64 [rows][2],
     for pa_copy_blocks).  All or nothing; see pa.h."""
-    n, width, blocks = _pages(block_tables, seq_lens, ref_counts)
-    _check_int32(query_start_loc, (n + 1,), "query_start_loc")
+    n, width, blocks, dev = _pages(block_tables, seq_lens, ref_counts)
+    if query_start_loc.dtype is not _int32 or query_start_loc.shape != (n + 1,) or \
+            not query_start_loc.is_contiguous() or query_start_loc.get_device() != dev:
+        _bad(query_start_loc, (n + 1,), "query_start_loc")
     if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [total_q_tokens]")
     if block_mapping.dtype is not torch.int64 or block_mapping.shape != (n, 2) or not block_mapping.is_contiguous():
         raise ValueError("block_mapping must be a contiguous int64 tensor [rows][2]")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _launch(_lib.pa_append_blocks, "pa_append_blocks",
-            (block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping, ref_counts, workspace), stream,
-            block_tables.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
-            block_mapping.data_ptr(), ref_counts.data_ptr(), n, slot_mapping.shape[0], width, blocks, block_size,
-            workspace.data_ptr(), workspace.nbytes)
+    if not (slot_mapping.get_device() == block_mapping.get_device() == workspace.get_device() == dev):
+        raise ValueError("pa_append_blocks: all tensors must be on one CUDA device")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_append_blocks, block_tables, seq_lens, query_start_loc, slot_mapping, block_mapping,
+                          ref_counts, block_size, workspace, stream)
+    st = _lib.pa_append_blocks(
+        block_tables.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
+        block_mapping.data_ptr(), ref_counts.data_ptr(), n, slot_mapping.numel(), width, blocks, block_size,
+        workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_append_blocks"))
+    if st != PA_OK:
+        raise PAError(st, "pa_append_blocks")
 
 
 def pa_release_blocks(block_tables, seq_lens, ref_counts, block_size, keep_lens=None, stream=None) -> None:
     """Give up what lies behind the first keep_lens (int32 [rows]; None: 0) tokens of every row:
     the blocks lose a holder and seq_lens is cut.  See pa.h."""
-    n, width, blocks = _pages(block_tables, seq_lens, ref_counts)
-    tensors, keep_ptr = (block_tables, seq_lens, ref_counts), None
+    n, width, blocks, dev = _pages(block_tables, seq_lens, ref_counts)
+    keep_ptr = None
     if keep_lens is not None:
-        _check_int32(keep_lens, (n,), "keep_lens")
-        tensors, keep_ptr = (*tensors, keep_lens), keep_lens.data_ptr()
-    _launch(_lib.pa_release_blocks, "pa_release_blocks", tensors, stream, block_tables.data_ptr(),
-            seq_lens.data_ptr(), keep_ptr, ref_counts.data_ptr(), n, width, blocks, block_size)
+        if keep_lens.dtype is not _int32 or keep_lens.shape != (n,) or not keep_lens.is_contiguous() or \
+                keep_lens.get_device() != dev:
+            _bad(keep_lens, (n,), "keep_lens")
+        keep_ptr = keep_lens.data_ptr()
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_release_blocks, block_tables, seq_lens, ref_counts, block_size, keep_lens, stream)
+    st = _lib.pa_release_blocks(
+        block_tables.data_ptr(), seq_lens.data_ptr(), keep_ptr, ref_counts.data_ptr(), n, width, blocks, block_size,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_release_blocks"))
+    if st != PA_OK:
+        raise PAError(st, "pa_release_blocks")
 
 
 def pa_default_partition_size(num_seqs, num_kv_heads, max_seq_len, block_size) -> int:
