@@ -362,6 +362,7 @@ pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const
  *   block_mapping   int64 [num_seqs][2] (written): the copies to be made by pa_copy_blocks,
  *                   in every layer, before the new tokens are written; (0, 0), a no-op
  *                   there, for rows without one
+ *   num_seqs        at most PA_MAX_APPEND_SEQS
  *   workspace       >= pa_append_workspace_size(...) bytes, 256-byte aligned; contents need
  *                   no initialisation
  * All or nothing: where the pool has fewer free blocks than the call needs (PA_ERRFLAG_POOL),
@@ -370,6 +371,8 @@ pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const
  * and every pair (0, 0), so that the calls that follow write nothing.  [LINEAGE]: running
  * out of memory is handled at admission, never while writing KV.
  */
+#define PA_MAX_APPEND_SEQS 8192
+
 size_t pa_append_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t block_size);
 pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32_t* query_start_loc,
                            int64_t* slot_mapping, int64_t* block_mapping, int32_t* ref_counts, int32_t num_seqs,

@@ -468,21 +468,10 @@ BeamLayout beam_layout(int num_seqs, int num_beams, int vocab_size, int num_cand
   return L;
 }
 
-struct AppendLayout {
-  size_t tail_off, need_off, first_off, fresh_off, total;
-};
-
-// Per row its shared tail, its need and where that starts; then the blocks given out: at
-// most one copy and one part-filled block a row, and the full blocks of the new tokens.
-AppendLayout append_layout(int num_seqs, int total_q, int block_size) {
-  AppendLayout L;
-  const size_t rows = align256((size_t)num_seqs * sizeof(int32_t));
-  L.tail_off = 0;
-  L.need_off = rows;
-  L.first_off = 2 * rows;
-  L.fresh_off = 3 * rows;
-  L.total = L.fresh_off + align256((2 * (size_t)num_seqs + total_q / block_size) * sizeof(int32_t));
-  return L;
+// The blocks given out: at most one copy and one part-filled block a row, and the full
+// blocks of the new tokens.
+size_t append_workspace(int num_seqs, int total_q, int block_size) {
+  return align256((2 * (size_t)num_seqs + total_q / block_size) * sizeof(int32_t));
 }
 
 pa::SequenceParams sequence_params(int32_t* block_tables, int32_t* seq_lens, int32_t* ref_counts, int32_t num_rows,
@@ -784,7 +773,7 @@ pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const
 
 size_t pa_append_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t block_size) {
   if (num_seqs < 1 || total_q_tokens < 0 || block_size < 1) return 256;
-  return append_layout(num_seqs, total_q_tokens, block_size).total;
+  return append_workspace(num_seqs, total_q_tokens, block_size);
 }
 
 pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32_t* query_start_loc,
@@ -798,19 +787,15 @@ pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32
     return PA_ERR_INVALID_ARG;
   if (total_q_tokens > 0 && !slot_mapping) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
-  const AppendLayout L = append_layout(num_seqs, total_q_tokens, block_size);
-  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (num_seqs > PA_MAX_APPEND_SEQS) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < append_workspace(num_seqs, total_q_tokens, block_size)) return PA_ERR_WORKSPACE;
   pa::SequenceParams p =
       sequence_params(block_tables, seq_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.query_start_loc = query_start_loc;
   p.slot_mapping = slot_mapping;
   p.block_mapping = block_mapping;
   p.total_tokens = total_q_tokens;
-  p.ws_tail = reinterpret_cast<int32_t*>(ws + L.tail_off);
-  p.ws_need = reinterpret_cast<int32_t*>(ws + L.need_off);
-  p.ws_first = reinterpret_cast<int32_t*>(ws + L.first_off);
-  p.ws_fresh = reinterpret_cast<int32_t*>(ws + L.fresh_off);
+  p.ws_fresh = static_cast<int32_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   TraceScope t(12, s);
   return cuda_status(pa::launch_append_blocks(p, s));

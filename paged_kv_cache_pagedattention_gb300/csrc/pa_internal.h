@@ -155,9 +155,6 @@ struct SequenceParams {
   const int32_t* query_start_loc;  // append: [num_rows + 1]
   int64_t* slot_mapping;         // append: [total_tokens]
   int64_t* block_mapping;        // append: [num_rows][2]
-  int32_t* ws_tail;              // append scratch: [num_rows] each
-  int32_t* ws_need;
-  int32_t* ws_first;
   int32_t* ws_fresh;             // append scratch: the blocks given out
   unsigned* err;
   int num_rows;

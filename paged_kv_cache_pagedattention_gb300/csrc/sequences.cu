@@ -6,23 +6,29 @@
 // ref_counts[b] is the number of table rows that hold block b; a block is free at 0.
 // Everything is whole numbers and every choice goes by row order and block number, so a
 // call's result does not depend on which thread comes first.
+#include <cooperative_groups.h>
+
 #include "pa_common.cuh"
 
 namespace pa {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kTableThreads = 256;
+constexpr int kTableUnroll = 4;
 
 __device__ __forceinline__ int blocks_of(int tokens, int block_size) {
-  return static_cast<int>(((long long)tokens + block_size - 1) / block_size);
+  return static_cast<int>((static_cast<unsigned>(tokens) + static_cast<unsigned>(block_size) - 1u) /
+                          static_cast<unsigned>(block_size));
 }
 
 __device__ __forceinline__ bool length_ok(const SequenceParams& p, int len) {
   return len >= 0 && len <= (long long)p.max_blocks_per_seq * p.block_size;
 }
 
-// Grid: x = child, y = slice of its row.
+// Grid: x = child, y = slice of its row.  Four entries a thread on their way at once.
 __global__ void __launch_bounds__(kTableThreads) fork_kernel(const SequenceParams p) {
   const int child = blockIdx.x;
   const int parent = p.parents[child];
@@ -37,187 +43,311 @@ __global__ void __launch_bounds__(kTableThreads) fork_kernel(const SequenceParam
     }
   }
   if (blockIdx.y == 0 && threadIdx.x == 0) p.seq_lens[child] = len;
-  if (len == 0) return;
   const int blocks = blocks_of(len, p.block_size);
   const int32_t* src = p.parent_tables + (long long)parent * p.max_blocks_per_seq;
   int32_t* dst = p.block_tables + (long long)child * p.max_blocks_per_seq;
-  for (int j = blockIdx.y * kTableThreads + threadIdx.x; j < blocks; j += gridDim.y * kTableThreads) {
-    const int b = src[j];
-    dst[j] = b;
-    if (b >= p.num_blocks) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
-    else if (b >= 0) atomicAdd(p.ref_counts + b, 1);
+  const int step = gridDim.y * kTableThreads;
+  for (int j0 = blockIdx.y * kTableThreads + threadIdx.x; j0 < blocks; j0 += kTableUnroll * step) {
+    int b[kTableUnroll];
+#pragma unroll
+    for (int u = 0; u < kTableUnroll; ++u) b[u] = j0 + u * step < blocks ? src[j0 + u * step] : -1;
+#pragma unroll
+    for (int u = 0; u < kTableUnroll; ++u) {
+      if (j0 + u * step < blocks) dst[j0 + u * step] = b[u];
+      if (b[u] >= p.num_blocks) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
+      else if (b[u] >= 0) atomicAdd(p.ref_counts + b[u], 1);
+    }
   }
 }
 
-// One block a row: its length is read by every thread before one of them writes it.
-__global__ void __launch_bounds__(1024) release_kernel(const SequenceParams p) {
-  const int row = blockIdx.x;
+// A cluster of blocks a row: every one reads the row's length before one of them writes it.
+__global__ void __launch_bounds__(kTableThreads) release_kernel(const SequenceParams p) {
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int row = blockIdx.x / cluster.num_blocks(), part = cluster.block_rank();
   const int len = p.seq_lens[row];
   const int keep = p.keep_lens ? p.keep_lens[row] : 0;
-  __syncthreads();
+  cluster.sync();
   if (!length_ok(p, len) || keep < 0) {
-    if (threadIdx.x == 0) flag_error(p.err, PA_ERRFLAG_SEQ_LEN);
+    if (part == 0 && threadIdx.x == 0) flag_error(p.err, PA_ERRFLAG_SEQ_LEN);
     return;
   }
   if (keep >= len) return;
-  if (threadIdx.x == 0) p.seq_lens[row] = keep;
+  if (part == 0 && threadIdx.x == 0) p.seq_lens[row] = keep;
   const int32_t* table = p.block_tables + (long long)row * p.max_blocks_per_seq;
-  const int last = blocks_of(len, p.block_size);
-  for (int j = blocks_of(keep, p.block_size) + threadIdx.x; j < last; j += blockDim.x) {
-    const int b = table[j];
-    if (b >= p.num_blocks) {
-      flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
-    } else if (b >= 0 && atomicSub(p.ref_counts + b, 1) <= 0) {  // held by no row: put it back
-      atomicAdd(p.ref_counts + b, 1);
+  const int last = blocks_of(len, p.block_size), step = cluster.num_blocks() * kTableThreads;
+  for (int j0 = blocks_of(keep, p.block_size) + part * kTableThreads + threadIdx.x; j0 < last;
+       j0 += kTableUnroll * step) {
+    int b[kTableUnroll], held[kTableUnroll];
+#pragma unroll
+    for (int u = 0; u < kTableUnroll; ++u) b[u] = j0 + u * step < last ? table[j0 + u * step] : -1;
+#pragma unroll
+    for (int u = 0; u < kTableUnroll; ++u) {
+      held[u] = 1;
+      if (b[u] >= p.num_blocks) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
+      else if (b[u] >= 0) held[u] = atomicSub(p.ref_counts + b[u], 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kTableUnroll; ++u) {
+      if (held[u] > 0) continue;  // else held by no row: put it back
+      atomicAdd(p.ref_counts + b[u], 1);
       flag_error(p.err, PA_ERRFLAG_REF_COUNT);
     }
   }
 }
 
-constexpr int kAppendThreads = 1024;
+// ---------------------------------------------------------------- append
 
-// Exclusive prefix sum of v over the block, and the block's total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int incl = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kAppendThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  __syncthreads();
-  return before + incl - v;
+constexpr int kAppendThreads = 1024;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendParts = 8;
+static_assert(kAppendThreads * kAppendParts == PA_MAX_APPEND_SEQS, "one row a thread");
+constexpr int kScan = 8;                                // 32-block groups of the pool that a warp looks at at once
+constexpr int kLook = kAppendWarps * 32 * kScan;        // blocks that all warps look at at once
+constexpr int kInline = 8;                              // new tokens of a row whose slots its thread writes itself
+
+// Bits of the 32 blocks from b0 + 32 u on that are free (count 0) and below `end`.
+__device__ __forceinline__ void free_masks(const int32_t* refs, int b0, int end, unsigned (&masks)[kScan]) {
+  const int lane = threadIdx.x % 32;
+  int r[kScan];
+#pragma unroll
+  for (int u = 0; u < kScan; ++u) r[u] = b0 + u * 32 + lane < end ? refs[b0 + u * 32 + lane] : 1;
+#pragma unroll
+  for (int u = 0; u < kScan; ++u) masks[u] = __ballot_sync(~0u, r[u] == 0);
 }
 
+// Exclusive prefix sum over the block of v, which every lane of a warp gives as its warp's
+// (kWarp) or each thread as its own; `total` is the block's sum.
+template <bool kWarp>
+__device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int upto = v;
+  if constexpr (!kWarp) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += up;
+    }
+  }
+  __syncthreads();  // sums may still be read
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int before = lane < warp ? sums[lane] : 0;
+  total = sums[lane];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(~0u, before, o);
+    total += __shfl_xor_sync(~0u, total, o);
+  }
+  return before + upto - v;
+}
+
+struct __align__(16) AppendShared {
+  int tails[kAppendThreads];  // block that a row would write into and shares, else -1
+  int sums[kAppendWarps];
+  unsigned flags;             // errors, and the two below
+  int needed;                 // blocks of this part's rows
+  int enough;                 // part 0: whether the pool has what all parts need
+};
+constexpr unsigned kSharedTail = 1u << 30, kLargeRow = 1u << 31;
+
+// One row a thread: one block up to kAppendThreads rows, a cluster of them above.  What a row
+// needs stays in its thread's registers.  The first block's warps look through the pool from
+// its lowest block on, until as many free ones are found as all rows need.  All of it is
+// latency, some six dependent trips to memory (256 rows of 17,000 blocks: APPEND_US us).
+template <bool kCluster>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequenceParams p) {
-  __shared__ int warp_sums[kAppendThreads / 32];
-  __shared__ int bad;
-  const int n = p.num_rows, bs = p.block_size;
-  int32_t* tail = p.ws_tail;    // block that row i would write into and shares, else -1
-  int32_t* need = p.ws_need;    // blocks row i takes, times two, plus one if the first replaces its tail
-  int32_t* first = p.ws_first;  // where they start in `fresh`
-  int32_t* fresh = p.ws_fresh;  // the blocks given out, in order
-  if (threadIdx.x == 0) bad = 0;
+  __shared__ AppendShared sh;
+  __shared__ __align__(16) int other[kCluster ? kAppendThreads : 4];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int parts = kCluster ? gridDim.x : 1, part = kCluster ? blockIdx.x : 0;
+  auto meet = [&]() {
+    if constexpr (kCluster) cg::this_cluster().sync();
+    else __syncthreads();
+  };
+  auto part_of = [&](int r) -> AppendShared* {
+    if constexpr (kCluster) return cg::this_cluster().map_shared_rank(&sh, r);
+    else return &sh;
+  };
+  const int n = p.num_rows, i = part * kAppendThreads + threadIdx.x;
+  const unsigned bs = p.block_size;
+  const bool mine = i < n;
+  int len = 0, start = 0, stop = 0;
+  if (mine) {
+    len = p.seq_lens[i];
+    start = p.query_start_loc[i];
+    stop = p.query_start_loc[i + 1];
+  }
+  unsigned masks[kScan];  // the pool's first kLook blocks, on their way with the rows
+  if (part == 0) free_masks(p.ref_counts, warp * 32 * kScan, p.num_blocks, masks);
+  if (threadIdx.x == 0) sh.flags = 0;
   __syncthreads();
+
+  // the row: its last block if that is partly filled, who holds it, and the blocks it grows by
   unsigned flags = 0;
-  if (threadIdx.x == 0 && (p.query_start_loc[0] != 0 || p.query_start_loc[n] != p.total_tokens))
-    flags |= PA_ERRFLAG_QUERY;
-  for (int i = threadIdx.x; i < n; i += kAppendThreads) {
-    const int len = p.seq_lens[i];
-    const long long add = (long long)p.query_start_loc[i + 1] - p.query_start_loc[i];
-    tail[i] = -1;
-    need[i] = 0;
-    if (add < 0) {
-      flags |= PA_ERRFLAG_QUERY;
-      continue;
-    }
-    if (!length_ok(p, len) || len + add > (long long)p.max_blocks_per_seq * bs || len + add > 0x7fffffff) {
-      flags |= PA_ERRFLAG_SEQ_LEN;
-      continue;
-    }
-    if (add == 0) continue;
-    need[i] = 2 * (blocks_of(static_cast<int>(len + add), bs) - blocks_of(len, bs));
-    if (len % bs) {
-      const int b = p.block_tables[(long long)i * p.max_blocks_per_seq + len / bs];
-      if (b < 0 || b >= p.num_blocks) flags |= PA_ERRFLAG_BLOCK_TABLE;
-      else if (p.ref_counts[b] < 1) flags |= PA_ERRFLAG_REF_COUNT;
-      else if (p.ref_counts[b] > 1) tail[i] = b;
-    }
-  }
-  if (flags) {
-    flag_error(p.err, flags);
-    atomicOr(&bad, 1);
-  }
-  __syncthreads();
-  if (!bad) {
-    // a shared tail is copied by every row that writes it but, where they are all of its
-    // holders, the last
-    for (int i = threadIdx.x; i < n; i += kAppendThreads) {
-      const int b = tail[i];
-      if (b < 0) continue;
-      int lower = 0;
-      for (int j = 0; j < i; ++j) lower += tail[j] == b;
-      if (lower < p.ref_counts[b] - 1) need[i] += 1;
-    }
-  }
-  __syncthreads();
-  int base = 0;
-  if (!bad) {
-    for (int i0 = 0; i0 < n; i0 += kAppendThreads) {
-      const int i = i0 + threadIdx.x;
-      const int v = i < n ? (need[i] >> 1) + (need[i] & 1) : 0;
-      int total;
-      const int before = block_scan(v, warp_sums, total);
-      if (i < n) first[i] = base + before;
-      base += total;
-    }
-    int found = 0;
-    for (int b0 = 0; b0 < p.num_blocks && found < base; b0 += kAppendThreads) {
-      const int b = b0 + threadIdx.x;
-      const int v = b < p.num_blocks && p.ref_counts[b] == 0;
-      int total;
-      const int at = found + block_scan(v, warp_sums, total);
-      if (v && at < base) fresh[at] = b;
-      found += total;
-    }
-    if (found < base) {
-      if (threadIdx.x == 0) {
-        flag_error(p.err, PA_ERRFLAG_POOL);
-        bad = 1;
+  const long long add = (long long)stop - start;
+  int last = -1, held = 0, grows = 0, grown = 0, offset = 0;
+  if (mine) {
+    if ((i == 0 && start != 0) || (i == n - 1 && stop != p.total_tokens) || add < 0) {
+      flags = PA_ERRFLAG_QUERY;
+    } else if (!length_ok(p, len) || len + add > (long long)p.max_blocks_per_seq * p.block_size ||
+               len + add > 0x7fffffff) {
+      flags = PA_ERRFLAG_SEQ_LEN;
+    } else if (add > 0) {
+      grown = blocks_of(len, bs);
+      grows = blocks_of(static_cast<int>(len + add), bs) - grown;
+      offset = static_cast<int>(static_cast<unsigned>(len) % bs);
+      if (offset) {
+        last = p.block_tables[(long long)i * p.max_blocks_per_seq + grown - 1];
+        if (last < 0 || last >= p.num_blocks) {
+          flags = PA_ERRFLAG_BLOCK_TABLE;
+        } else {
+          held = p.ref_counts[last];
+          if (held < 1) flags = PA_ERRFLAG_REF_COUNT;
+        }
       }
     }
+    if (flags) flag_error(p.err, flags);
+    if (held > 1) flags |= kSharedTail;
+    if (add > kInline) flags |= kLargeRow;
   }
-  __syncthreads();
-  const bool refused = bad != 0;
-  for (int i = threadIdx.x; i < n; i += kAppendThreads) {
+  flags = __reduce_or_sync(~0u, flags);
+  if (flags && lane == 0) atomicOr(&sh.flags, flags);
+  sh.tails[threadIdx.x] = held > 1 ? last : -1;
+  meet();
+
+  unsigned all_flags = 0;
+  for (int r = 0; r < parts; ++r) all_flags |= part_of(r)->flags;
+  bool refused = (all_flags & ~(kSharedTail | kLargeRow)) != 0;
+  // A shared tail is copied by every row that writes it but, where these are all of its
+  // holders, the last: by those with fewer rows before them than the others that hold it.
+  bool copies = false;
+  if (all_flags & kSharedTail) {
+    int lower = 0;
+    for (int r = 0; r <= part; ++r) {
+      const int* tails = sh.tails;
+      if constexpr (kCluster) {
+        __syncthreads();
+        other[threadIdx.x] = part_of(r)->tails[threadIdx.x];
+        __syncthreads();
+        tails = other;
+      }
+      const int until = r < part ? kAppendThreads : static_cast<int>(threadIdx.x);
+      if (held > 1) {
+        int j = 0;
+        for (; j + 4 <= until; j += 4) {
+          const int4 t = *reinterpret_cast<const int4*>(tails + j);
+          lower += (t.x == last) + (t.y == last) + (t.z == last) + (t.w == last);
+        }
+        for (; j < until; ++j) lower += tails[j] == last;
+      }
+    }
+    copies = held > 1 && lower < held - 1;
+  }
+  // where the row's blocks start among all that are given out
+  int needed;
+  int at = block_prefix<false>(refused ? 0 : grows + (copies ? 1 : 0), sh.sums, needed);
+  if constexpr (kCluster) {
+    if (threadIdx.x == 0) sh.needed = needed;
+    meet();
+    needed = 0;
+    for (int r = 0; r < parts; ++r) {
+      const int theirs = part_of(r)->needed;
+      if (r < part) at += theirs;
+      needed += theirs;
+    }
+  }
+  // the free blocks by ascending number, as many as are needed
+  int32_t* fresh = p.ws_fresh;
+  if (part == 0) {
+    int found = 0;
+    for (int look = 0; !refused && found < needed && look < p.num_blocks; look += kLook) {
+      const int b0 = look + warp * 32 * kScan;
+      if (look > 0) free_masks(p.ref_counts, b0, p.num_blocks, masks);
+      int count = 0, sum;
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) count += __popc(masks[u]);
+      int place = found + block_prefix<true>(count, sh.sums, sum);
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) {
+        const int to = place + __popc(masks[u] & ((1u << lane) - 1));
+        if ((masks[u] >> lane & 1) && to < needed) fresh[to] = b0 + u * 32 + lane;
+        place += __popc(masks[u]);
+      }
+      found += sum;
+    }
+    if (threadIdx.x == 0) sh.enough = found >= needed;
+  }
+  meet();
+  if (!refused && !part_of(0)->enough) {
+    if (i == 0) flag_error(p.err, PA_ERRFLAG_POOL);
+    refused = true;
+  }
+
+  if (mine) {
     long long src = 0, dst = 0;
     if (!refused) {
       int32_t* table = p.block_tables + (long long)i * p.max_blocks_per_seq;
-      const int len = p.seq_lens[i];
-      int at = first[i];
-      if (need[i] & 1) {
-        src = tail[i];
-        dst = fresh[at++];
-        table[len / bs] = static_cast<int32_t>(dst);
+      if (copies) {
+        src = last;
+        last = fresh[at++];
+        dst = last;
+        table[grown - 1] = last;
         atomicSub(p.ref_counts + src, 1);
-        p.ref_counts[dst] = 1;
+        p.ref_counts[last] = 1;
       }
-      int j = blocks_of(len, bs);
-      for (int k = need[i] >> 1; k; --k, ++j) {
-        const int b = fresh[at++];
-        table[j] = b;
-        p.ref_counts[b] = 1;
+      int block = last;
+      unsigned slot_at = offset;
+      int t = start;
+      for (int k = 0; k <= grows; ++k) {  // the last block's rest, then the new blocks
+        if (k > 0) {
+          block = fresh[at + k - 1];
+          table[grown + k - 1] = block;
+          p.ref_counts[block] = 1;
+          slot_at = 0;
+        } else if (offset == 0) {
+          continue;
+        }
+        if (!(all_flags & kLargeRow))
+          for (; t < stop && slot_at < bs; ++t, ++slot_at) p.slot_mapping[t] = (long long)block * bs + slot_at;
       }
+      p.seq_lens[i] = stop - start + len;
     }
     p.block_mapping[2 * (long long)i] = src;
     p.block_mapping[2 * (long long)i + 1] = dst;
   }
-  __syncthreads();
-  for (int t = threadIdx.x; t < p.total_tokens; t += kAppendThreads) {
+  meet();  // a part's shared memory is read until here, the tables below
+  if (!(all_flags & kLargeRow) && !refused) return;
+
+  for (int t = i; t < p.total_tokens; t += parts * kAppendThreads) {
     long long slot = -1;
     if (!refused) {
-      int lo = 0, hi = n;  // first row with query_start_loc[row + 1] > t
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (p.query_start_loc[mid + 1] <= t) lo = mid + 1;
-        else hi = mid;
+      int row = 0, past = n;  // first row with query_start_loc[row + 1] > t
+      while (row < past) {
+        const int mid = (row + past) / 2;
+        if (p.query_start_loc[mid + 1] <= t) row = mid + 1;
+        else past = mid;
       }
-      const int pos = p.seq_lens[lo] + (t - p.query_start_loc[lo]);
-      slot = (long long)p.block_tables[(long long)lo * p.max_blocks_per_seq + pos / bs] * bs + pos % bs;
+      const unsigned pos = p.seq_lens[row] - (p.query_start_loc[row + 1] - t);  // the lengths count the new tokens
+      slot = (long long)p.block_tables[(long long)row * p.max_blocks_per_seq + pos / bs] * bs + pos % bs;
     }
     p.slot_mapping[t] = slot;
   }
-  __syncthreads();
-  if (!refused)
-    for (int i = threadIdx.x; i < n; i += kAppendThreads)
-      p.seq_lens[i] += p.query_start_loc[i + 1] - p.query_start_loc[i];
+}
+
+cudaError_t launch_cluster(void (*kernel)(SequenceParams), const SequenceParams& p, int grid, int cluster,
+                           int threads, cudaStream_t stream) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(grid);
+  config.blockDim = dim3(threads);
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -229,13 +359,19 @@ cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_release_blocks(const SequenceParams& p, cudaStream_t stream) {
-  release_kernel<<<p.num_rows, 1024, 0, stream>>>(p);
-  return cudaGetLastError();
+  // blocks a row: enough for its longest table, at kTableUnroll entries a thread
+  int cluster = 1;
+  while (cluster < 8 && p.num_rows < (1 << 27) && cluster * kTableThreads * kTableUnroll < p.max_blocks_per_seq) cluster *= 2;
+  return launch_cluster(release_kernel, p, p.num_rows * cluster, cluster, kTableThreads, stream);
 }
 
 cudaError_t launch_append_blocks(const SequenceParams& p, cudaStream_t stream) {
-  append_kernel<<<1, kAppendThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (p.num_rows <= kAppendThreads) {
+    append_kernel<false><<<1, kAppendThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const int parts = (p.num_rows + kAppendThreads - 1) / kAppendThreads;
+  return launch_cluster(append_kernel<true>, p, parts, parts, kAppendThreads, stream);
 }
 
 }  // namespace pa

@@ -239,6 +239,7 @@ def test_pages_host_validation_without_a_gpu(pa):  # noqa: F811
     for edits in ({6: -1}, {7: -1}, {8: 0}, {9: 0}, {10: 0}, {6: 0}, {0: None}, {1: None}, {2: None}, {3: None},
                   {4: None}, {5: None}, {11: None}):
         assert append(*_edited(good, edits)) == bad, edits
+    assert append(*_edited(good, {6: 8193, 12: 1 << 30})) == pa.PA_ERR_UNSUPPORTED
     assert append(*_edited(good, {11: FAKE + 8})) == pa.PA_ERR_WORKSPACE
     assert append(*_edited(good, {12: need - 1})) == pa.PA_ERR_WORKSPACE
     release = _fn(pa, "pa_release_blocks")

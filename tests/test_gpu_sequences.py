@@ -105,7 +105,7 @@ def test_random_histories(pa, rows, width, blocks, bs, most):
     assert not p.refs.any()
 
 
-@pytest.mark.parametrize("rows", [1000, 1024, 1025, 2600])
+@pytest.mark.parametrize("rows", [1000, 1024, 1025, 2600, 8192])
 def test_many_rows_share_few_tails(pa, rows):
     rng = np.random.default_rng(32)
     p = Pool(5, 6, 4 * rows + 50, 16)
