@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
   constexpr int kLoads = kPerThread / kVec;   // pieces of a tile that a thread takes
   constexpr int kStep = kLoads * kThreads;    // pieces of a tile
   constexpr int kStages = ring_stages<DT>(), kSlots = ring_slots<DT, kShifted>();
+  asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks come up while the last segments run
   extern __shared__ __align__(16) unsigned char raw[];
   SegmentShared& sh = *reinterpret_cast<SegmentShared*>(raw);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -531,6 +532,7 @@ constexpr int kHeld = 4;     // keys a thread loads ahead
 // fall to a threshold on their fp32 scores, held with the scores' error bounds so that
 // none of the best can be lost; the rest are ranked by their fp64 scores.
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the segments are done and their results there
   extern __shared__ Beam beams[];  // [num_beams]
   __shared__ Key kept[kJoin];
   __shared__ float2 bounds[kJoin];
@@ -715,8 +717,18 @@ cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stre
                         : dtype == PA_F16 ? launch_type<PA_F16>(p, stream)
                                           : launch_type<PA_BF16>(p, stream);
   if (e != cudaSuccess) return e;
-  beam_join_kernel<<<p.num_seqs, kThreads, p.num_beams * sizeof(Beam), stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(p.num_seqs);
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = p.num_beams * sizeof(Beam);
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  const cudaError_t j = cudaLaunchKernelEx(&config, beam_join_kernel, p);
+  return j != cudaSuccess ? j : cudaGetLastError();
 }
 
 }  // namespace pa
