@@ -18,7 +18,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 16;  // elements of a tile that one thread takes
 constexpr int kTile = kThreads * kPerThread;
 constexpr int kWindow = 8;      // tiles between the block's barriers
-constexpr int kSpare = 64;      // kept candidates that do not force a merge
 constexpr int kRoom = 1024;     // candidates a block can hold
 constexpr int kRescan = 2048;   // elements that are looked at again at a time
 constexpr int kGroups = 64;     // of threads, for bounds
@@ -26,7 +25,7 @@ constexpr int kFew = 48;        // candidates that are ranked without a bound fi
 constexpr int kMaxKeep = PA_MAX_BEAM_CANDIDATES;
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kMaxKeep <= kGroups && kMaxKeep <= kSpare, "");
+static_assert(kMaxKeep <= kGroups, "");
 
 template <int DT>
 constexpr float largest() {
@@ -172,11 +171,11 @@ __device__ int drop_candidates(SegmentShared& sh, int k, unsigned start) {
 // Push a candidate; returns whether they are to be merged.  One equal to the threshold's
 // value counts up to the threshold's place.
 __device__ __forceinline__ bool push_candidate(SegmentShared& sh, float value, unsigned index, float least,
-                                               Key threshold) {
+                                               Key threshold, int spare) {
   if (value == kNegInf || (value == least && index > key_index(threshold))) return false;
   const int at = atomicAdd(&sh.count, 1);
   if (at < kRoom) sh.buffer[at] = static_cast<Key>(__float_as_uint(value)) << 32 | index;
-  return at >= kSpare;
+  return at >= spare;
 }
 
 // 16 bytes from byte `shift` (0 .. 15) of the 32 in lo and hi.
@@ -235,12 +234,18 @@ struct Part {
     if constexpr (DT != PA_F32) f = unpack2<DT>(top);
     return fminf(fmaxf(fmaxf(f.x, f.y), kNegInf), largest<DT>());
   }
-  // Bits of the elements that are at or above `least` and not -inf.
-  __device__ __forceinline__ unsigned reach(float least) const {
-    least = fmaxf(least, -largest<PA_F32>());
+  // Bits of the elements that are at or above `least` and not -inf, of the fourths whose sum
+  // is not below `bound`.
+  __device__ __forceinline__ unsigned reach(float least, float4 sums, float bound) const {
+    const float lowest = fmaxf(least, -largest<PA_F32>());
+    const float sum[4] = {sums.x, sums.y, sums.z, sums.w};
     unsigned bits = 0;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) bits |= (at(i) >= least ? 1u : 0u) << i;
+    for (int c = 0; c < 4; ++c) {
+      if (sum[c] < bound) continue;
+#pragma unroll
+      for (int i = c; i < kPerThread; i += 4) bits |= (at(i) >= lowest ? 1u : 0u) << i;
+    }
     return bits;
   }
   // Sums of exp(x - m), of every fourth element each.  m comes off before the product with
@@ -312,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
   SegmentShared& sh = *reinterpret_cast<SegmentShared*>(raw);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seg = blockIdx.x, k = p.num_candidates;
+  const int spare = 2 * k;  // candidates that do not force a merge
   const long long row = blockIdx.y;
   const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
   // the row's whole pieces, cut evenly; the elements behind the last go to the last segment
@@ -370,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
 
   int stage = 0;
   for (int base = first; base < end;) {
-    const int stop = min(end, base + kWindow * kStep);
+    // windows double up to kWindow tiles: a threshold from as many elements as came before
+    // lets some k of a window pass
+    const int stop = min(end, base + min(kWindow * kStep, max(kStep, base - first)));
     bool full = false;
     for (int tile = base; tile < stop; tile += kStep) {
       const int mine = tile + own;
@@ -396,23 +404,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
       }
       float4 sums = m != kNegInf ? v.exp_sums(m) : make_float4(0.f, 0.f, 0.f, 0.f);
       if (!(sums.x < bound && sums.y < bound && sums.z < bound && sums.w < bound)) {
-        const float top = v.maximum();
-        if (top > m || !((sums.x + sums.y) + (sums.z + sums.w) < INFINITY)) {  // a new reference; or NaN or +inf
-          const float m2 = fmaxf(m, top);
-          v.clean();
-          s *= m2 != kNegInf ? ex2_approx((m - m2) * kLog2e) : 0.f;
-          m = m2;
-          set_bound();
-          sums = m != kNegInf ? v.exp_sums(m) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (top >= least)
-          for (unsigned left = v.reach(least); left; left &= left - 1) {
-            const int i = __ffs(left) - 1;  // its value comes from the ring: registers have no index
-            const T* at =
-                reinterpret_cast<const T*>(reinterpret_cast<const unsigned char*>(slot + i / kVec * 32) + shift);
-            full |= push_candidate(sh, clean_logit<DT>(at[i % kVec]), (mine + i / kVec * 32) * kVec + i % kVec, least,
-                                   threshold);
+        constexpr float kBelow = 1.f - 0x1p-10f;  // of no element above m
+        if (!(sums.x < kBelow && sums.y < kBelow && sums.z < kBelow && sums.w < kBelow)) {
+          const float top = v.maximum();
+          if (top > m || !((sums.x + sums.y) + (sums.z + sums.w) < INFINITY)) {  // a new reference; or NaN or +inf
+            const float m2 = fmaxf(m, top);
+            v.clean();
+            s *= m2 != kNegInf ? ex2_approx((m - m2) * kLog2e) : 0.f;
+            m = m2;
+            set_bound();
+            sums = m != kNegInf ? v.exp_sums(m) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
+        }
+        for (unsigned left = v.reach(least, sums, bound); left; left &= left - 1) {
+          const int i = __ffs(left) - 1;  // its value comes from the ring: registers have no index
+          const T* at =
+              reinterpret_cast<const T*>(reinterpret_cast<const unsigned char*>(slot + i / kVec * 32) + shift);
+          full |= push_candidate(sh, clean_logit<DT>(at[i % kVec]), (mine + i / kVec * 32) * kVec + i % kVec, least,
+                                 threshold, spare);
+        }
       }
       s += (sums.x + sums.y) + (sums.z + sums.w);
       __syncwarp();  // the stage has been read
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
     if (__syncthreads_or(full) && !merge()) {
       // The window held more candidates than the block has room for: it is looked at again,
       // kRescan elements at a time.  Where these overflow too, the threshold (the k-th best
-      // of those that fitted) leaves at least kRoom - kSpare - k of them below.
+      // of those that fitted) leaves at least kRoom - 3 k of them below.
       keys = drop_candidates(sh, k, base * kVec);
       for (int e0 = base * kVec; e0 < stop * kVec; e0 += kRescan) {
         bool again = true;
@@ -430,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
           bool over = false;
           for (int e = e0 + threadIdx.x; e < min(stop * kVec, e0 + kRescan); e += kThreads) {
             const float value = clean_logit<DT>(x[e]);
-            if (value >= least) over |= push_candidate(sh, value, e, least, threshold);
+            if (value >= least) over |= push_candidate(sh, value, e, least, threshold, spare);
           }
           again = __syncthreads_or(over) && !merge();
           if (again) keys = drop_candidates(sh, k, e0);
@@ -450,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
         const float m2 = fmaxf(m, value);
         s = s * ex2_approx((m - m2) * kLog2e) + ex2_approx((value - m2) * kLog2e);
         m = m2;
-        if (value >= least) push_candidate(sh, value, tail + threadIdx.x, least, threshold);
+        if (value >= least) push_candidate(sh, value, tail + threadIdx.x, least, threshold, spare);
       }
     }
   }
