@@ -339,7 +339,7 @@ pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_pa
  *   parents      int32 [num_children]; a negative parent leaves child i empty (length 0), one
  *                >= num_parents does too and sets PA_ERRFLAG_PARENT
  *   block_tables_out, seq_lens_out must not overlap block_tables, seq_lens (they may be other
- *   rows of the same arrays); overlapping ranges are PA_ERR_INVALID_ARG.  What a child row
+ *   rows of the same arrays) or parents; overlapping ranges are PA_ERR_INVALID_ARG.  What a child row
  *   held before is overwritten, not released.
  */
 pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const int32_t* block_tables,

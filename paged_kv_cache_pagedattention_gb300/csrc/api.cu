@@ -758,8 +758,10 @@ pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const
   if (num_parents > 0 && (!block_tables || !seq_lens)) return PA_ERR_INVALID_ARG;
   const size_t row = (size_t)max_blocks_per_seq * sizeof(int32_t);
   if (overlap(block_tables_out, num_children * row, block_tables, num_parents * row) ||
-      overlap(seq_lens_out, num_children * sizeof(int32_t), seq_lens, num_parents * sizeof(int32_t)))
-    return PA_ERR_INVALID_ARG;  // a child would overwrite a parent that another child still reads
+      overlap(seq_lens_out, num_children * sizeof(int32_t), seq_lens, num_parents * sizeof(int32_t)) ||
+      overlap(block_tables_out, num_children * row, parents, num_children * sizeof(int32_t)) ||
+      overlap(seq_lens_out, num_children * sizeof(int32_t), parents, num_children * sizeof(int32_t)))
+    return PA_ERR_INVALID_ARG;  // a child would overwrite what another one still reads
   pa::SequenceParams p = sequence_params(block_tables_out, seq_lens_out, ref_counts, num_children,
                                          max_blocks_per_seq, num_blocks, block_size);
   p.parent_tables = block_tables;

@@ -154,6 +154,7 @@ constexpr int kAppendParts = 8;
 static_assert(kAppendThreads * kAppendParts == PA_MAX_APPEND_SEQS, "one row a thread");
 constexpr int kScan = 8;                                // 32-block groups of the pool that a warp looks at at once
 constexpr int kLook = kAppendWarps * 32 * kScan;        // blocks that all warps look at at once
+constexpr int kFewBlocks = 2;                           // new blocks of a row that its thread writes alone
 constexpr int kInline = 8;                              // new tokens of a row whose slots its thread writes itself
 
 // Bits of the 32 blocks from b0 + 32 u on that are free (count 0) and below `end`.
@@ -334,10 +335,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequencePa
     refused = true;
   }
 
+  int32_t* table = p.block_tables + (long long)i * p.max_blocks_per_seq;
   if (mine) {
     long long src = 0, dst = 0;
     if (!refused) {
-      int32_t* table = p.block_tables + (long long)i * p.max_blocks_per_seq;
       if (copies) {
         src = last;
         last = fresh[at++];
@@ -346,25 +347,41 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequencePa
         atomicSub(p.ref_counts + src, 1);
         p.ref_counts[last] = 1;
       }
-      int block = last;
-      unsigned slot_at = offset;
-      int t = start;
-      for (int k = 0; k <= grows; ++k) {  // the last block's rest, then the new blocks
-        if (k > 0) {
-          block = fresh[at + k - 1];
-          table[grown + k - 1] = block;
-          p.ref_counts[block] = 1;
-          slot_at = 0;
-        } else if (offset == 0) {
-          continue;
+      if (!(all_flags & kLargeRow)) {  // the slots: the last block's rest, then the new blocks
+        unsigned slot_at = offset;
+        int block = last, next = at;
+        for (int t = start; t < stop; ++t, ++slot_at) {
+          if (slot_at == bs || (t == start && offset == 0)) {
+            block = fresh[next++];
+            slot_at = 0;
+          }
+          p.slot_mapping[t] = (long long)block * bs + slot_at;
         }
-        if (!(all_flags & kLargeRow))
-          for (; t < stop && slot_at < bs; ++t, ++slot_at) p.slot_mapping[t] = (long long)block * bs + slot_at;
       }
       p.seq_lens[i] = stop - start + len;
     }
     p.block_mapping[2 * (long long)i] = src;
     p.block_mapping[2 * (long long)i + 1] = dst;
+  }
+  // the new blocks into the tables: a thread its own, a warp together those of a long prompt
+  if (refused) grows = 0;
+  if (grows <= kFewBlocks)
+    for (int k = 0; k < grows; ++k) {
+      const int block = fresh[at + k];
+      table[grown + k] = block;
+      p.ref_counts[block] = 1;
+    }
+  for (unsigned left = __ballot_sync(~0u, grows > kFewBlocks); left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    const int many = __shfl_sync(~0u, grows, from), first = __shfl_sync(~0u, at, from);
+    int32_t* to = p.block_tables + (long long)__shfl_sync(~0u, i, from) * p.max_blocks_per_seq +
+                  __shfl_sync(~0u, grown, from);
+#pragma unroll 4
+    for (int k = lane; k < many; k += 32) {
+      const int block = fresh[first + k];
+      to[k] = block;
+      p.ref_counts[block] = 1;
+    }
   }
   meet();  // a part's shared memory is read until here, the tables below
   if (!(all_flags & kLargeRow) && !refused) return;

@@ -225,10 +225,10 @@ def test_pages_host_validation_without_a_gpu(pa):  # noqa: F811
     fork = _fn(pa, "pa_fork_blocks")
     far = FAKE + (1 << 16)
     # out_tables out_lens tables lens parents refs | children parents width blocks bs stream
-    good = [FAKE, FAKE + 4096, far, far + 4096, FAKE, FAKE, 4, 3, 8, 100, 16, None]
+    good = [FAKE, FAKE + 4096, far, far + 4096, far + 8192, FAKE, 4, 3, 8, 100, 16, None]
     assert fork(*_edited(good, {6: 0})) == pa.PA_OK
     for edits in ({6: -1}, {7: -1}, {8: 0}, {9: 0}, {10: 0}, {0: None}, {1: None}, {2: None}, {3: None}, {4: None},
-                  {5: None}, {2: FAKE}, {2: FAKE + 4 * 8 * 4 - 4}, {3: FAKE + 4096}):
+                  {5: None}, {2: FAKE}, {2: FAKE + 4 * 8 * 4 - 4}, {3: FAKE + 4096}, {4: FAKE + 4096}, {4: FAKE + 8}):
         assert fork(*_edited(good, edits)) == bad, edits
     append = _fn(pa, "pa_append_blocks")
     need = pa.pa_append_workspace_size(4, 40, 16)

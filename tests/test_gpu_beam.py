@@ -131,6 +131,40 @@ def test_constant_rows(pa, v, fill):
     check(x, cum, run(pa, torch.from_numpy(x).float().to(DEV), torch.from_numpy(cum).to(DEV), 12), 12, "f32", True)
 
 
+@pytest.mark.parametrize("w,v", [(10, 64), (40, 3000), (700, 40)])
+def test_many_equal_beams(pa, w, v):
+    """More candidates with the best score than are ranked at once."""
+    x = np.zeros((2 * w, v))
+    cum = np.full((2, w), -1.5, np.float32)
+    check(x, cum, run(pa, torch.zeros(2 * w, v, device=DEV), torch.from_numpy(cum).to(DEV), 32), 32, "f32", exact=True)
+
+
+@pytest.mark.parametrize("k", [1, 7, 32])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rising_and_falling_references(pa, dtype, k):
+    """Rows whose later parts lie far above, or below, the first part that sets the reference
+    of the sums, a few segments long; flat rows; one that overflows fp32 exponentials of the
+    first reference."""
+    rng = np.random.default_rng(26)
+    v = 40000
+    x = rng.standard_normal((6, v))
+    x[0] += np.linspace(0, 200, v)
+    x[1] -= np.linspace(0, 200, v)
+    x[2] *= 1e-3
+    x[3, v // 2:] += 300
+    x[4, :5000] -= 1e4
+    x[5, ::4096] = 150.0
+    dev = torch.from_numpy(x).float().to(workloads.torch_dtype(dtype)).to(DEV)
+    x = dev.double().cpu().numpy()
+    cum = np.zeros((6, 1), np.float32)
+    check(x, cum, run(pa, dev, torch.from_numpy(cum).to(DEV), k), k, dtype, exact=True)
+    many = dev.repeat(120, 1)                    # one segment a row
+    got = run(pa, many, torch.zeros(720, 1, device=DEV), k)
+    for r in range(0, 720, 6):
+        assert np.array_equal(got[1][r:r + 6], got[1][:6]) and np.array_equal(got[0][r:r + 6], got[0][:6])
+    check(x, cum, [g[:6] for g in got], k, dtype, exact=False)
+
+
 @pytest.mark.parametrize("order", [1, -1])
 @pytest.mark.parametrize("v", [3000, 120000])
 def test_sorted_rows(pa, v, order):

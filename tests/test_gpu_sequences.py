@@ -154,6 +154,40 @@ def test_prompts_of_one_token_to_thousands(pa):
     assert pa.pa_get_error_flags(clear=True) == 0
 
 
+@pytest.mark.parametrize("bs", [1, 7, 16])
+def test_long_prompts_among_short_ones(pa, bs):
+    """Rows that grow by nothing, one block and thousands of blocks in one call, and then one
+    token each: threads write some blocks alone, others together."""
+    rng = np.random.default_rng(34)
+    p = Pool(70, 9100, 40000, bs)
+    add = rng.integers(0, 4, 70) * bs
+    add[[3, 4, 40, 69]] = [9000 * bs, 33 * bs + 1, 3 * bs, 8191 * bs - 1]
+    p.append(pa, add)
+    p.append(pa, np.ones(70, int))
+    p.append(pa, rng.integers(0, 9, 70))         # slots across block borders, eight tokens at most
+    p.release(pa)
+    assert pa.pa_get_error_flags(clear=True) == 0 and not p.refs.any()
+
+
+def test_fork_by_children_and_by_parents(pa):
+    """More children than the parents' way takes, more parents than children, none."""
+    rng = np.random.default_rng(35)
+    p = Pool(40, 30, 3000, 16)
+    p.append(pa, rng.integers(0, 480, 40))
+    for n in (1, 39, 40, 41, 1024, 1025):
+        t2, l2, dt, dl = p.fork(pa, rng.integers(-2, 40, n))
+        q = Pool(n, 30, 3000, 16)
+        q.refs, q.d_refs = p.refs, p.d_refs
+        q.take((t2, l2, dt, dl))
+        q.release(pa)
+    p.same()
+    empty = torch.zeros(0, 30, dtype=torch.int32, device=DEV)
+    out, lens = torch.full((3, 30), 5, dtype=torch.int32, device=DEV), torch.full((3,), 5, dtype=torch.int32, device=DEV)
+    pa.pa_fork_blocks(out, lens, empty, empty[:, 0].contiguous(), dev(np.array([-1, -7, -1], np.int32)), p.d_refs, 16)
+    assert lens.tolist() == [0, 0, 0] and bool((out == 5).all())
+    assert pa.pa_get_error_flags(clear=True) == 0
+
+
 def test_too_few_free_blocks_change_nothing(pa):
     p = Pool(4, 8, 10, 16)
     assert p.append(pa, [40, 40, 40, 0]) == 0    # nine of ten
