@@ -129,7 +129,9 @@ def kv_code(cache: torch.Tensor, k_scale=None) -> int:
     """Cache dtype code; scales holding more than one value (one per KV head, the
     cache's dimension 1) select the per-head format."""
     code = PA_NVFP4 if is_nvfp4(cache) else dtype_code(cache)
-    if code in (PA_FP8_E4M3, PA_FP8_E5M2, PA_NVFP4) and k_scale is not None and k_scale.numel() > 1:
+    if k_scale is None:
+        return code
+    if code in (PA_FP8_E4M3, PA_FP8_E5M2, PA_NVFP4) and k_scale.numel() > 1:
         if k_scale.numel() != cache.shape[1]:
             raise ValueError("scales: one per tensor or one per KV head")
         return {PA_FP8_E4M3: PA_FP8_E4M3_PER_HEAD, PA_FP8_E5M2: PA_FP8_E5M2_PER_HEAD,
@@ -215,7 +217,7 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_int32 = torch.int32
+_int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
 
 
 def _on_device(index, call, *args, **kwargs):
@@ -240,12 +242,11 @@ def _bad(t, shape, what):
     raise ValueError(f"{what}: all tensors must be on one CUDA device")
 
 
-def _row_stride(t, heads, d, what):
-    """Elements between the tokens of a [tokens][heads][d] tensor whose heads are contiguous."""
-    token, head, elem = t.stride()
-    if (elem != 1 and d > 1) or (head != d and heads > 1):
+def _check_heads(t, what):
+    """Refuse a [tokens][heads][head_size] tensor whose heads are not contiguous."""
+    _, head, elem = t.stride()
+    if (elem != 1 and t.shape[2] > 1) or (head != t.shape[2] and t.shape[1] > 1):
         raise ValueError(f"{what}: every token's [heads][head_size] must be contiguous")
-    return token
 
 
 def pa_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_max_position=0.0,
@@ -276,6 +277,12 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
     nb, heads, bs, head = cache_geometry(k_cache, v_cache, d)
     if heads != hkv or head != d or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous and match key's heads")
+    # rows: heads are contiguous, tokens any distance apart
+    k_stride, k_head, k_elem = key.stride()
+    v_stride, v_head, v_elem = value.stride()
+    if k_elem != 1 or v_elem != 1 or k_head != d or v_head != d:
+        _check_heads(key, "key")
+        _check_heads(value, "value")
     hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None or q.dim() != 3 or q_out.shape != q.shape or q.dtype is not dtype or \
@@ -283,22 +290,26 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
             raise ValueError("q/q_out must be [num_tokens][num_q_heads][head_size] of key's dtype")
         if q.get_device() != dev or q_out.get_device() != dev:
             raise ValueError("q/q_out: all tensors must be on one CUDA device")
-        hq = q.shape[1]
-        q_ptr, q_stride = q.data_ptr(), _row_stride(q, hq, d, "q")
-        q_out_ptr, q_out_stride = q_out.data_ptr(), _row_stride(q_out, hq, d, "q_out")
+        hq, q_ptr, q_out_ptr = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        q_stride, q_head, q_elem = q.stride()
+        q_out_stride, q_out_head, q_out_elem = q_out.stride()
+        if q_elem != 1 or q_out_elem != 1 or q_head != d or q_out_head != d:
+            _check_heads(q, "q")
+            _check_heads(q_out, "q_out")
     if positions.dtype is not _int32 or positions.shape != (t,) or not positions.is_contiguous():
         _bad(positions, (t,), "positions")
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (t,) or not slot_mapping.is_contiguous():
+    if slot_mapping.dtype is not _int64 or slot_mapping.shape != (t,) or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [num_tokens]")
-    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not _float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float32 tensor [rotary_dim/2]")
     code = kv_code(k_cache, k_scale)
     k_scale_ptr = v_scale_ptr = None
     if code >= PA_FP8_E4M3 and k_scale is not None and v_scale is not None:
-        for scale in (k_scale, v_scale):
-            if scale.dtype is not torch.float32 or not scale.is_contiguous() or scale.numel() != k_scale.numel() or \
-                    scale.numel() not in (1, hkv) or scale.get_device() != dev:
-                raise ValueError("scales: float32, both one per tensor or both one per KV head, on the caches' device")
+        n = k_scale.numel()
+        if (n != 1 and n != hkv) or v_scale.numel() != n or k_scale.dtype is not _float32 or \
+                v_scale.dtype is not _float32 or not (k_scale.is_contiguous() and v_scale.is_contiguous()) or \
+                not k_scale.get_device() == v_scale.get_device() == dev:
+            raise ValueError("scales: float32, both one per tensor or both one per KV head, on the caches' device")
         k_scale_ptr, v_scale_ptr = k_scale.data_ptr(), v_scale.data_ptr()
     if not (value.get_device() == k_cache.get_device() == v_cache.get_device() == positions.get_device() ==
             slot_mapping.get_device() == inv_freq.get_device() == dev):
@@ -308,10 +319,9 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
                           inv_freq, interleaved, attn_factor, k_scale, v_scale, stream)
     st = _lib.pa_rotary_and_cache(
         q_out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.shape[0],
-        bs, 1 if interleaved else 0, attn_factor, q_out_stride, q_stride, _row_stride(key, hkv, d, "key"),
-        _row_stride(value, hkv, d, "value"), dtype_code(key), code, k_scale_ptr, v_scale_ptr,
-        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_rotary_and_cache"))
+        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.numel(),
+        bs, 1 if interleaved else 0, attn_factor, q_out_stride, q_stride, k_stride, v_stride, dtype_code(key), code,
+        k_scale_ptr, v_scale_ptr, _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_rotary_and_cache"))
     if st != PA_OK:
         raise PAError(st, "pa_rotary_and_cache")
 
@@ -408,9 +418,9 @@ def pa_append_blocks(block_tables, seq_lens, query_start_loc, slot_mapping, bloc
     if query_start_loc.dtype is not _int32 or query_start_loc.shape != (n + 1,) or \
             not query_start_loc.is_contiguous() or query_start_loc.get_device() != dev:
         _bad(query_start_loc, (n + 1,), "query_start_loc")
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+    if slot_mapping.dtype is not _int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [total_q_tokens]")
-    if block_mapping.dtype is not torch.int64 or block_mapping.shape != (n, 2) or not block_mapping.is_contiguous():
+    if block_mapping.dtype is not _int64 or block_mapping.shape != (n, 2) or not block_mapping.is_contiguous():
         raise ValueError("block_mapping must be a contiguous int64 tensor [rows][2]")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
