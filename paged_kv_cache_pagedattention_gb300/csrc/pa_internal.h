@@ -159,6 +159,7 @@ struct SequenceParams {
   unsigned* err;
   int num_rows;
   int num_parents;
+  int fork_part;                 // fork by parents: children of a part
   int num_blocks;
   int max_blocks_per_seq;
   int block_size;

@@ -8,6 +8,8 @@
 // call's result does not depend on which thread comes first.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -60,20 +62,20 @@ __global__ void __launch_bounds__(kTableThreads) fork_kernel(const SequenceParam
   }
 }
 
-// The same by parents, grid: x = parent, y = slice of its row.  A parent's entries are read
-// once for all of its children and counted up once, by the number of them: with eight
-// children a parent an eighth of the atomics (32 parents of 32K to 131K tokens, 256
-// children: 7.6 us against 12.6 by children).  Every block looks through all children
-// for its own, so this is for kForkChildren at most.
-constexpr int kForkChildren = 1024;
+// The same by parents, grid: x = parent, y = slice of its row, z = part of the children, each
+// of p.fork_part.  A parent's entries are read once for all of a part's children and counted
+// up once, by the number of them, so there are as many fewer atomics.
+constexpr int kForkPart = 1024;  // children of a part at most
+constexpr int kForkMost = 1 << 20;
 __global__ void __launch_bounds__(kTableThreads) fork_parents_kernel(const SequenceParams p) {
-  __shared__ int children[kForkChildren];
+  __shared__ int children[kForkPart];
   __shared__ int count;
   const int parent = blockIdx.x;
   if (threadIdx.x == 0) count = 0;
   const int len_given = p.parent_lens[parent];
   __syncthreads();
-  for (int c = threadIdx.x; c < p.num_rows; c += kTableThreads) {
+  const int first = blockIdx.z * p.fork_part, past = min(p.num_rows, first + p.fork_part);
+  for (int c = first + threadIdx.x; c < past; c += kTableThreads) {
     const int from = p.parents[c];
     if (from == parent) {
       children[atomicAdd(&count, 1)] = c;
@@ -422,11 +424,25 @@ cudaError_t launch_cluster(void (*kernel)(SequenceParams), const SequenceParams&
 
 cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
   const int slices = (p.max_blocks_per_seq + 4 * kTableThreads - 1) / (4 * kTableThreads);
-  // by parents where they are no more than the children, else most of their blocks have none
-  const bool by_parents = p.num_rows <= kForkChildren && p.num_parents > 0 && p.num_parents <= p.num_rows;
-  const dim3 grid(by_parents ? p.num_parents : p.num_rows, slices < 1024 ? slices : 1024);
-  if (by_parents) fork_parents_kernel<<<grid, kTableThreads, 0, stream>>>(p);
-  else fork_kernel<<<grid, kTableThreads, 0, stream>>>(p);
+  const int rows = p.num_rows, y = slices < 1024 ? slices : 1024;
+  // By parents where at least two children on average share a parent and the rows are long, else
+  // the look for a parent's children costs more than its atomics (by parents against by
+  // children: 128 parents and 1,024 children of 131,072 tokens 8.3 against 13.4 us, one parent
+  // 7.6 against 36; of 1,024 tokens in tables of 64 blocks 3.5 against 2.5, and 1,024 parents
+  // of 131,072 tokens with as many children 19 against 14).
+  if (p.num_parents > 0 && rows / 2 >= p.num_parents && rows <= kForkMost &&
+      (long long)rows * p.max_blocks_per_seq >= 1 << 19) {
+    // parts of the children until the grid fills the device, of eight for each parent or more
+    const long long blocks = (long long)p.num_parents * y;
+    const int least = (rows + kForkPart - 1) / kForkPart, most = rows / 8 / p.num_parents;
+    const int fill = static_cast<int>(152 * 8 / blocks);
+    SequenceParams q = p;
+    const int parts = std::max(least, std::min(fill, most));
+    q.fork_part = (rows + parts - 1) / parts;
+    fork_parents_kernel<<<dim3(p.num_parents, y, parts), kTableThreads, 0, stream>>>(q);
+  } else {
+    fork_kernel<<<dim3(rows, y), kTableThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

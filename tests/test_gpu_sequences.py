@@ -188,6 +188,24 @@ def test_fork_by_children_and_by_parents(pa):
     assert pa.pa_get_error_flags(clear=True) == 0
 
 
+@pytest.mark.parametrize("parents,children", [(1, 70), (1, 1100), (5, 300), (5, 2500), (150, 300), (151, 300)])
+def test_fork_of_long_tables(pa, parents, children):
+    """Tables wide enough that children are dealt with by their parents."""
+    rng = np.random.default_rng(36)
+    width = 8000
+    p = Pool(parents, width, 40000, 1)
+    p.append(pa, [min(width, n) for n in rng.integers(0, 40000 // parents, parents)])
+    for low, high in ((-1, parents), (parents - 1, parents), (-3, -1), (-1, parents + 2)):
+        chosen = rng.integers(low, high, children)
+        t2, l2, dt, dl = p.fork(pa, chosen)
+        assert pa.pa_get_error_flags(clear=True) == (pa.PA_ERRFLAG_PARENT if (chosen >= parents).any() else 0)
+        q = Pool(children, width, 40000, 1)
+        q.refs, q.d_refs = p.refs, p.d_refs
+        q.take((t2, l2, dt, dl))
+        q.release(pa)
+        p.same()
+
+
 def test_too_few_free_blocks_change_nothing(pa):
     p = Pool(4, 8, 10, 16)
     assert p.append(pa, [40, 40, 40, 0]) == 0    # nine of ten
