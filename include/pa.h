@@ -262,7 +262,8 @@ pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rot
  *   *_stride     elements from one token's row to the next, >= the row (unused for one
  *                token): slices of one [num_tokens][q + k + v] projection are served as
  *                they are.  q_out may be q itself (same stride); otherwise nothing that is
- *                written may overlap anything that is read
+ *                written may overlap anything that is read (q_out over rows of q, key or
+ *                value at its own distance: PA_ERR_INVALID_ARG)
  *   positions    int32 [num_tokens]
  *   slot_mapping int64 [num_tokens], as pa_reshape_and_cache; a token with a negative
  *                slot is padding and one with a slot out of range an error
@@ -289,7 +290,7 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
  *   beam_scores[w] + logits[w][v] - log sum_u exp(logits[w][u]),
  * and the num_candidates best of each sequence's num_beams x vocab_size come back, best
  * first.  Scores are compared in fp64 (the sums of exponentials are held in fp32 and joined
- * in fp64); equal ones go to the lower beam, within it to the larger logit, then to the
+ * in 64-bit whole numbers of 2^-32); equal ones go to the lower beam, within it to the larger logit, then to the
  * lower token.
  *
  *   out_scores   float [num_seqs][num_candidates]
@@ -304,13 +305,15 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
  * ended, or does not exist yet) gives no candidates.  Where a sequence has fewer
  * candidates than num_candidates, the rest are score -inf, token -1, parent -1.
  *   num_candidates 1 .. PA_MAX_BEAM_CANDIDATES (num_beams, or twice that where some may
- *                end); num_beams <= PA_MAX_BEAMS; num_seqs x num_beams <= 65535
+ *                end); num_beams <= PA_MAX_BEAMS; num_seqs x num_beams <= 65535;
+ *                vocab_size <= PA_MAX_VOCAB
  *   workspace    >= pa_beam_select_workspace_size(...) bytes, 256-byte aligned; contents
  *                need no initialisation
- * The outputs must not overlap the inputs.
+ * The outputs must not overlap the inputs or the workspace (PA_ERR_INVALID_ARG).
  */
 #define PA_MAX_BEAM_CANDIDATES 32
 #define PA_MAX_BEAMS 1024
+#define PA_MAX_VOCAB 0x40000000
 
 size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,
                                      int32_t num_candidates);
@@ -330,7 +333,9 @@ pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_pa
  * num_blocks sets PA_ERRFLAG_BLOCK_TABLE and is never counted.  A length below 0 or above
  * max_blocks_per_seq x block_size sets PA_ERRFLAG_SEQ_LEN.  Entries behind a row's blocks
  * are neither read nor written.  Block numbers handed out depend on the arrays alone.  Calls
- * that share ref_counts must be ordered (one stream, or events between streams).
+ * that share ref_counts must be ordered (one stream, or events between streams).  Counts
+ * of tokens, blocks, rows and a row's entries above 2^30 are PA_ERR_UNSUPPORTED where a call
+ * steps through them.
  *
  * pa_fork_blocks -- children take their parents' blocks and lengths: row i of
  * block_tables_out and seq_lens_out becomes a copy of row parents[i], and every block of it

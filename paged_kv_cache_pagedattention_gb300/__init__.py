@@ -40,7 +40,7 @@ PA_ERRFLAG_BLOCK_TABLE, PA_ERRFLAG_SLOT, PA_ERRFLAG_SEQ_LEN, PA_ERRFLAG_QUERY, P
 # diagnostic only: a declared shared block differed for some member (the output is unaffected)
 PA_ERRFLAG_SHARED_MISMATCH = 0x20
 PA_ERRFLAG_PARENT, PA_ERRFLAG_POOL, PA_ERRFLAG_REF_COUNT = 0x40, 0x80, 0x100
-PA_MAX_BEAM_CANDIDATES, PA_MAX_BEAMS = 32, 1024
+PA_MAX_BEAM_CANDIDATES, PA_MAX_BEAMS, PA_MAX_VOCAB = 32, 1024, 1 << 30
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 # Names of the kernel kinds reported by pa_trace_read.

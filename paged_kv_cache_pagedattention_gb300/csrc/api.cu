@@ -489,10 +489,25 @@ pa::SequenceParams sequence_params(int32_t* block_tables, int32_t* seq_lens, int
   return p;
 }
 
+// The pages' kernels step through blocks and tokens by 32-bit places; a count above this could
+// step past them.
+constexpr int32_t kMostPages = 1 << 30;
+
 // Whether two byte ranges share a byte.
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
+// Whether n rows of `a` and of `b`, the same distance apart (bytes), share a byte: slices of
+// one array may lie between one another.
+bool rows_overlap(const void* a, int64_t a_width, const void* b, int64_t b_width, int64_t n, int64_t stride) {
+  if (n == 1) return overlap(a, a_width, b, b_width);
+  const int64_t span = (n - 1) * stride;
+  if (!overlap(a, span + a_width, b, span + b_width)) return false;
+  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t behind = (apart % stride + stride) % stride;  // b's row behind the start of a's
+  return behind < a_width || behind + b_width > stride;
 }
 
 }  // namespace
@@ -618,6 +633,7 @@ pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rot
     case PA_ROTARY_NTK:
       if (rotary_dim < 4) return PA_ERR_INVALID_ARG;  // the exponent R / (R - 2)
       b = base * pow(factor, (double)rotary_dim / (rotary_dim - 2));
+      if (!(b < INFINITY)) return PA_ERR_INVALID_ARG;
       break;
     case PA_ROTARY_BY_PARTS:
       if (!(original_max_position > 0.0) || !(original_max_position < INFINITY) || !(low_turns < high_turns) ||
@@ -673,6 +689,14 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key, eb) || !aligned(value, eb) ||
       (num_q_heads > 0 && (!aligned(q, eb) || !aligned(q_out, eb))))
     return PA_ERR_INVALID_ARG;
+  // a token's q_out over what another one still reads (rows of other distances are the caller's)
+  auto written_over = [&](const void* src, int64_t width, int64_t stride) {
+    return (num_tokens == 1 || stride == q_out_stride) &&
+           rows_overlap(q_out, q_width * eb, src, width * eb, num_tokens, stride * eb);
+  };
+  if (num_q_heads > 0 && ((q != q_out && written_over(q, q_width, q_stride)) ||
+                          written_over(key, kv_width, key_stride) || written_over(value, kv_width, value_stride)))
+    return PA_ERR_INVALID_ARG;
   pa::RotaryParams p;
   p.q_out = q_out;
   p.q = q;
@@ -707,7 +731,7 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
 
 size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,
                                      int32_t num_candidates) {
-  if (num_seqs < 1 || num_beams < 1 || vocab_size < 1 || num_candidates < 1) return 256;
+  if (num_seqs < 1 || num_beams < 1 || vocab_size < 1 || vocab_size > PA_MAX_VOCAB || num_candidates < 1) return 256;
   return beam_layout(num_seqs, num_beams, vocab_size, num_candidates).total;
 }
 
@@ -722,12 +746,19 @@ pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_pa
   if (num_candidates > PA_MAX_BEAM_CANDIDATES) return PA_ERR_UNSUPPORTED;
   const long long rows = (long long)num_seqs * num_beams;
   if (rows > 65535) return PA_ERR_UNSUPPORTED;
-  if (num_beams > PA_MAX_BEAMS) return PA_ERR_UNSUPPORTED;
+  if (num_beams > PA_MAX_BEAMS || vocab_size > PA_MAX_VOCAB) return PA_ERR_UNSUPPORTED;
   if (rows > 1 && row_stride < vocab_size) return PA_ERR_INVALID_ARG;
   if (!aligned(logits, dtype_bytes(logits_dtype))) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
   const BeamLayout L = beam_layout(num_seqs, num_beams, vocab_size, num_candidates);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  // a sequence's results over what another one still reads
+  const size_t read = ((size_t)(rows - 1) * row_stride + vocab_size) * dtype_bytes(logits_dtype);
+  const size_t scores = (size_t)rows * sizeof(float), out = (size_t)num_seqs * num_candidates * sizeof(float);
+  for (const void* o : {static_cast<const void*>(out_scores), static_cast<const void*>(out_tokens),
+                        static_cast<const void*>(out_parents)})
+    if (overlap(o, out, logits, read) || overlap(o, out, beam_scores, scores) || overlap(o, out, workspace, L.total))
+      return PA_ERR_INVALID_ARG;
   pa::BeamParams p;
   p.logits = logits;
   p.beam_scores = beam_scores;
@@ -754,6 +785,7 @@ pa_status pa_fork_blocks(int32_t* block_tables_out, int32_t* seq_lens_out, const
   if (num_children < 0 || num_parents < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1)
     return PA_ERR_INVALID_ARG;
   if (num_children == 0) return PA_OK;
+  if (max_blocks_per_seq > kMostPages || num_children > kMostPages) return PA_ERR_UNSUPPORTED;
   if (!block_tables_out || !seq_lens_out || !parents || !ref_counts) return PA_ERR_INVALID_ARG;
   if (num_parents > 0 && (!block_tables || !seq_lens)) return PA_ERR_INVALID_ARG;
   const size_t row = (size_t)max_blocks_per_seq * sizeof(int32_t);
@@ -789,7 +821,8 @@ pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32
     return PA_ERR_INVALID_ARG;
   if (total_q_tokens > 0 && !slot_mapping) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
-  if (num_seqs > PA_MAX_APPEND_SEQS) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > PA_MAX_APPEND_SEQS || total_q_tokens > kMostPages || num_blocks > kMostPages)
+    return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < append_workspace(num_seqs, total_q_tokens, block_size)) return PA_ERR_WORKSPACE;
   pa::SequenceParams p =
       sequence_params(block_tables, seq_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size);
@@ -808,6 +841,7 @@ pa_status pa_release_blocks(const int32_t* block_tables, int32_t* seq_lens, cons
                             int32_t block_size, pa_stream_t stream) {
   if (num_seqs < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
+  if (max_blocks_per_seq > kMostPages) return PA_ERR_UNSUPPORTED;
   if (!block_tables || !seq_lens || !ref_counts) return PA_ERR_INVALID_ARG;
   pa::SequenceParams p =
       sequence_params(const_cast<int32_t*>(block_tables), seq_lens, ref_counts, num_seqs, max_blocks_per_seq,

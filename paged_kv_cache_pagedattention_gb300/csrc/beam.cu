@@ -490,8 +490,8 @@ struct Beam {
   float rest;
 };
 
-// Sums are joined as whole numbers of 2^-32 (exact in any order; a sum is 1 or more, so one
-// costs 2^-33 at most), and their logarithm is kept in the two parts of struct Beam, each to
+// Sums are joined as whole numbers of 2^-32 (exact in any order; their sum is 1 or more, so
+// the rounding of each costs 2^-33 of it at most), and their logarithm is kept in the two parts of struct Beam, each to
 // 2^-25 or so: the SM has two fp64 lanes, and fp64 sums and logarithms took half the join's
 // time.
 __device__ __forceinline__ void set_log(Beam& b, unsigned long long sum) {
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
     unsigned long long sum = 0;
     for (int i = lane; i < p.num_segments; i += 32) {
       if (i != lane) own = st[i];
-      if (m != kNegInf) sum += static_cast<unsigned long long>(own.y * ex2_approx((own.x - m) * kLog2e) * 0x1p32f);
+      if (m != kNegInf) sum += __float2ull_rn(own.y * ex2_approx((own.x - m) * kLog2e) * 0x1p32f);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);

@@ -249,6 +249,43 @@ def test_pages_host_validation_without_a_gpu(pa):  # noqa: F811
         assert release(*_edited(good, edits)) == bad, edits
 
 
+def test_outputs_over_inputs_are_refused(pa):  # noqa: F811
+    bad, far = pa.PA_ERR_INVALID_ARG, [FAKE + (i << 24) for i in range(12)]
+    rotary = _fn(pa, "pa_rotary_and_cache")
+    # three tokens of 8 and 2 heads of 128 bf16, rows of 1536 elements
+    row = 1536
+    good = [far[0], far[1], far[2], far[3], far[4], far[5], far[6], far[7], far[8], 3, 10, 8, 2, 128, 64, 16, 0, 1.0,
+            row, row, row, row, pa.PA_BF16, pa.PA_BF16, None, None, None]
+    packed = {1: far[0], 2: far[0] + 2048, 3: far[0] + 2048 + 512}
+    for edits in ({1: far[0] + 16}, {1: far[0] - 16}, {1: far[0] + 2 * row}, {2: far[0] + 2048 - 16},
+                  {3: far[0] + 2 * row - 16}, {3: far[0] - 512 + 2}, {**packed, 0: far[0] + 1024},
+                  {**packed, 0: far[0] + 2048},
+                  {9: 1, 1: far[0] + 2046}, {9: 1, 2: far[0] - 510}):
+        assert rotary(*_edited(good, edits)) == bad, edits
+    beam = _fn(pa, "pa_beam_select")
+    need = pa.pa_beam_select_workspace_size(2, 4, 1000, 8)
+    good = [far[0], far[1], far[2], far[3], 1000, far[4], 2, 4, 1000, 8, pa.PA_BF16, far[5], need, None]
+    for i in range(3):
+        for at in (far[3], far[3] + 2 * 7999, far[4], far[4] + 28, far[5] + need - 4, far[3] - 63, far[4] - 60):
+            assert beam(*_edited(good, {i: at})) == bad, (i, at)
+
+
+def test_counts_past_32_bit_steps_are_refused(pa):  # noqa: F811
+    unsup, most = pa.PA_ERR_UNSUPPORTED, 1 << 30
+    far = [FAKE + (i << 50) for i in range(8)]
+    assert _fn(pa, "pa_fork_blocks")(*far[:6], 4, 3, most + 1, 100, 16, None) == unsup
+    append = _fn(pa, "pa_append_blocks")
+    assert append(*far[:6], 4, most + 1, 8, 100, 16, far[6], 1 << 40, None) == unsup
+    assert append(*far[:6], 4, 40, 8, most + 1, 16, far[6], 1 << 40, None) == unsup
+    assert _fn(pa, "pa_release_blocks")(far[0], far[1], None, far[2], 4, most + 1, 100, 16, None) == unsup
+    assert pa.pa_beam_select_workspace_size(1, 1, pa.PA_MAX_VOCAB + 1, 1) == 256
+    assert _fn(pa, "pa_beam_select")(*far[:4], most + 1, far[4], 1, 1, pa.PA_MAX_VOCAB + 1, 8, pa.PA_BF16, far[5],
+                                     1 << 40, None) == unsup
+    freq = (ctypes.c_float * 2)()
+    assert _fn(pa, "pa_rotary_frequencies")(freq, None, 4, 1e300, pa.ROTARY_SCALINGS["ntk"], 1e10, 0.0, 0.0,
+                                            0.0) == pa.PA_ERR_INVALID_ARG
+
+
 def test_bindings_refuse_wrong_tensors_on_the_cpu(pa):  # noqa: F811
     z = torch.zeros
     i32, i64 = torch.int32, torch.int64

@@ -2,8 +2,9 @@
 
 A returned score may be off from the fp64 score by the fp32 rounding of the output (2^-24 of
 it) and by the error of log-sum-exp: every exponential and rescale is good to 2^-21, and a
-thread adds at most 2^13 / 256 terms in fp32 before sums are joined in a tree of depth 8
-(TOL).  Candidates closer than that across beams may swap, so general inputs are checked by
+thread adds in fp32, one after the other, at most 32 terms (four of a tile of 4096 elements,
+two joins of these, and the tiles of its segment, few in these tests) before sums are joined
+in a tree of depth 8 (TOL).  Candidates closer than that across beams may swap, so general inputs are checked by
 the oracle's score of what came back; where scores are equal by construction, or one beam
 is alone, tokens and parents have to be the oracle's.
 """
@@ -258,3 +259,30 @@ def test_another_stream_two_workspaces_and_graphs(pa):
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))  # the same bits every time
+
+
+@pytest.mark.parametrize("dtype,gap", [("bf16", 8), ("f32", 7)])
+def test_rows_behind_2_to_31_elements(pa, dtype, gap):
+    """Rows far apart: the last one starts behind 2^31 elements."""
+    rng = np.random.default_rng(26)
+    v, rows, stride = 5003, 4, 2 ** 30 + gap
+    flat = torch.empty((rows - 1) * stride + v, dtype=workloads.torch_dtype(dtype), device=DEV)
+    far = flat.as_strided((rows, v), (stride, 1))
+    near, x = make(rng, rows, v, dtype)
+    far.copy_(near)
+    cum = -np.cumsum(rng.random((2, 2)).astype(np.float32), 1)
+    got = run(pa, far, torch.from_numpy(cum).to(DEV), 8)
+    check(x, cum, got, 8, dtype, exact=False)
+    for a, b in zip(got, run(pa, near, torch.from_numpy(cum).to(DEV), 8)):
+        assert np.array_equal(a, b)
+
+
+def test_outputs_over_inputs_are_refused(pa):
+    logits, cum = torch.zeros(4, 50, device=DEV), torch.zeros(2, 2, device=DEV)
+    out = (torch.empty(2, 2, device=DEV), torch.empty(2, 2, dtype=torch.int32, device=DEV),
+           torch.empty(2, 2, dtype=torch.int32, device=DEV))
+    ws = pa.workspace_tensor(pa.pa_beam_select_workspace_size(2, 2, 50, 2))
+    for bad in ((cum, out[1], out[2]), (out[0], cum.view(torch.int32), out[2]),
+                (out[0], out[1], ws[:16].view(torch.int32).view(2, 2))):
+        with pytest.raises(pa.PAError):
+            pa.pa_beam_select(*bad, logits, cum, ws)

@@ -262,3 +262,37 @@ def test_another_stream_and_a_graph(pa):
         torch.cuda.synchronize()
         c.check(False)
         assert torch.equal(c.q_out, eager) == (shift == 0) and torch.equal(c.kc, k_eager) == (shift == 0)
+
+
+@pytest.mark.parametrize("rot,kv", [(128, "bf16"), (24, "bf16"), (128, "fp8_e4m3"), (24, "nvfp4")])
+def test_slots_behind_2_to_32_elements(pa, rot, kv):
+    """A block's rows are the same wherever it lies: in a cache of more than 2^32 elements too."""
+    nb, far = 4 * 10 ** 5, 399990               # blocks of 8 heads x 16 x 128 elements (6.5 GB of bf16)
+    c = Case(23, 8, 8, 128, rot, "bf16", kv, seed=20)
+    c.call(pa, False)
+    k_far, v_far = (torch.zeros((nb,) + tuple(t.shape[1:]), dtype=t.dtype, device=DEV) for t in (c.kc, c.vc))
+    k_far[far:far + c.nb], v_far[far:far + c.nb] = (workloads.bits_to_torch(b, kv, DEV) for b in (c.kb, c.vb))
+    q_out = torch.zeros_like(c.q_out)
+    pa.pa_rotary_and_cache(q_out, c.q, c.key, c.value, k_far, v_far, c.dev_pos, c.dev_slots + far * c.bs, c.dev_freq,
+                           k_scale=c.ks, v_scale=c.vs)
+    assert torch.equal(q_out, c.q_out) and pa.pa_get_error_flags(clear=True) == 0
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    assert torch.equal(raw(k_far[far:far + c.nb]), raw(c.kc)) and torch.equal(raw(v_far[far:far + c.nb]), raw(c.vc))
+    assert not bool(raw(k_far[:c.nb]).any()) and not bool(raw(v_far[:c.nb]).any())
+
+
+def test_q_out_between_the_rows_it_comes_from(pa):
+    """Slices of one array that lie side by side: written ones and read ones do not touch."""
+    c = Case(40, 8, 2, 128, 128, "bf16", "bf16", seed=22)
+    c.call(pa, False)
+    want = c.q_out.clone()
+    rows = torch.zeros(40, 2 * 8 * 128 + 4 * 128, dtype=torch.bfloat16, device=DEV)
+    rows[:, :12 * 128] = torch.cat([c.q.flatten(1), c.key.flatten(1), c.value.flatten(1)], 1)
+    q, key, value = (rows[:, a * 128:b * 128].unflatten(1, (-1, 128)) for a, b in ((0, 8), (8, 10), (10, 12)))
+    q_out = rows[:, 12 * 128:].unflatten(1, (8, 128))
+    pa.pa_rotary_and_cache(q_out, q, key, value, c.kc, c.vc, c.dev_pos, c.dev_slots, c.dev_freq)
+    assert torch.equal(q_out, want)
+    for over in (rows[:, 128:9 * 128], rows[:, 9 * 128:17 * 128], rows[:, 11 * 128:19 * 128]):
+        with pytest.raises(pa.PAError):
+            pa.pa_rotary_and_cache(over.unflatten(1, (8, 128)), q, key, value, c.kc, c.vc, c.dev_pos, c.dev_slots,
+                                   c.dev_freq)

@@ -194,7 +194,9 @@ def test_fork_of_long_tables(pa, parents, children):
     rng = np.random.default_rng(36)
     width = 8000
     p = Pool(parents, width, 40000, 1)
-    p.append(pa, [min(width, n) for n in rng.integers(0, 40000 // parents, parents)])
+    lens = rng.integers(0, 100, parents)
+    lens[0] = 1200 if children <= 300 else 300
+    p.append(pa, lens)
     for low, high in ((-1, parents), (parents - 1, parents), (-3, -1), (-1, parents + 2)):
         chosen = rng.integers(low, high, children)
         t2, l2, dt, dl = p.fork(pa, chosen)
@@ -344,3 +346,19 @@ def test_replayed_from_a_graph_on_another_stream(pa):
         assert np.array_equal(slots.cpu().numpy(), want[0]) and np.array_equal(pairs.cpu().numpy(), want[1])
         assert np.array_equal(between.cpu().numpy(), r2)
         assert torch.equal(p.d_refs, refs0) and not bool(lens.any())
+
+
+def test_slots_behind_2_to_32(pa):
+    """A pool whose last blocks alone are free, their slots behind 2^32."""
+    blocks, bs = 2 ** 27 + 5, 64
+    refs = torch.ones(blocks, dtype=torch.int32, device=DEV)
+    refs[-3:] = 0
+    tables, lens = torch.full((2, 4), -1, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    slots, pairs = torch.zeros(80, dtype=torch.int64, device=DEV), torch.zeros(2, 2, dtype=torch.int64, device=DEV)
+    ws = pa.workspace_tensor(pa.pa_append_workspace_size(2, 80, bs))
+    pa.pa_append_blocks(tables, lens, dev(np.array([0, 70, 80], np.int32)), slots, pairs, refs, bs, ws)
+    first = (blocks - 3) * bs
+    assert slots.tolist() == list(range(first, first + 70)) + list(range(first + 2 * bs, first + 2 * bs + 10))
+    assert refs[-4:].tolist() == [1, 1, 1, 1] and not bool(pairs.any())
+    pa.pa_release_blocks(tables, lens, refs, bs)
+    assert refs[-4:].tolist() == [1, 0, 0, 0] and pa.pa_get_error_flags(clear=True) == 0
