@@ -457,10 +457,11 @@ struct BeamLayout {
   size_t state_off, keys_off, total;
 };
 
-BeamLayout beam_layout(int num_seqs, int num_beams, int vocab_size, int num_candidates) {
+// The workspace is sized for fp32, whose rows are cut the finest.
+BeamLayout beam_layout(int num_seqs, int num_beams, int vocab_size, int num_candidates, int elem_bytes) {
   BeamLayout L;
   const long long rows = (long long)num_seqs * num_beams;
-  L.segments = pa::beam_segments(rows, vocab_size);
+  L.segments = pa::beam_segments(rows, vocab_size, elem_bytes);
   const size_t parts = (size_t)rows * L.segments;
   L.state_off = 0;
   L.keys_off = align256(parts * sizeof(float2));
@@ -732,7 +733,7 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
 size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,
                                      int32_t num_candidates) {
   if (num_seqs < 1 || num_beams < 1 || vocab_size < 1 || vocab_size > PA_MAX_VOCAB || num_candidates < 1) return 256;
-  return beam_layout(num_seqs, num_beams, vocab_size, num_candidates).total;
+  return beam_layout(num_seqs, num_beams, vocab_size, num_candidates, 4).total;
 }
 
 pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_parents, const void* logits,
@@ -750,8 +751,8 @@ pa_status pa_beam_select(float* out_scores, int32_t* out_tokens, int32_t* out_pa
   if (rows > 1 && row_stride < vocab_size) return PA_ERR_INVALID_ARG;
   if (!aligned(logits, dtype_bytes(logits_dtype))) return PA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
-  const BeamLayout L = beam_layout(num_seqs, num_beams, vocab_size, num_candidates);
-  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (workspace_bytes < beam_layout(num_seqs, num_beams, vocab_size, num_candidates, 4).total) return PA_ERR_WORKSPACE;
+  const BeamLayout L = beam_layout(num_seqs, num_beams, vocab_size, num_candidates, dtype_bytes(logits_dtype));
   // a sequence's results over what another one still reads
   const size_t read = ((size_t)(rows - 1) * row_stride + vocab_size) * dtype_bytes(logits_dtype);
   const size_t scores = (size_t)rows * sizeof(float), out = (size_t)num_seqs * num_candidates * sizeof(float);

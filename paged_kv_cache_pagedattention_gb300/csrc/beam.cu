@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerThread = 16;  // elements of a tile that one thread takes
-constexpr int kTile = kThreads * kPerThread;
+constexpr int kLoads = 4;       // 16-byte pieces of a tile that one thread takes
+constexpr int kTileBytes = kThreads * kLoads * 16;
 constexpr int kWindow = 8;      // tiles between the block's barriers
 constexpr int kRoom = 1024;     // candidates a block can hold
 constexpr int kRescan = 2048;   // elements that are looked at again at a time
@@ -194,10 +194,10 @@ __device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, unsigned shift) {
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 
-// A thread's part of a tile: kPerThread elements as they lie in memory.
+// A thread's part of a tile: kLoads pieces as they lie in memory.
 template <int DT>
 struct Part {
-  static constexpr int kWords = kPerThread * Elem<DT>::bytes / 4;
+  static constexpr int kWords = 4 * kLoads, n = 4 * kWords / Elem<DT>::bytes;
   uint32_t w[kWords];
 
   __device__ __forceinline__ float at(int i) const {
@@ -244,7 +244,7 @@ struct Part {
     for (int c = 0; c < 4; ++c) {
       if (sum[c] < bound) continue;
 #pragma unroll
-      for (int i = c; i < kPerThread; i += 4) bits |= (at(i) >= lowest ? 1u : 0u) << i;
+      for (int i = c; i < n; i += 4) bits |= (at(i) >= lowest ? 1u : 0u) << i;
     }
     return bits;
   }
@@ -255,7 +255,7 @@ struct Part {
     const float2 off = make_float2(-m, -m), scale = make_float2(kLog2e, kLog2e);
     float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
-    for (int i = 0; i < kPerThread; i += 4) {
+    for (int i = 0; i < n; i += 4) {
       const float2 d = __fmul2_rn(__fadd2_rn(make_float2(at(i), at(i + 1)), off), scale);
       const float2 e = __fmul2_rn(__fadd2_rn(make_float2(at(i + 2), at(i + 3)), off), scale);
       a = __fadd2_rn(a, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
@@ -285,14 +285,13 @@ __device__ __forceinline__ void async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Tiles on their way, and the pieces of one that a warp fetches (with a shift also the one
-// behind its own).
-template <int DT>
-constexpr int ring_stages() { return DT == PA_F32 ? 2 : 3; }
-template <int DT, bool kShifted>
-constexpr int ring_slots() { return 32 * kPerThread * Elem<DT>::bytes / 16 + (kShifted ? 1 : 0); }
+// Tiles on their way, and the pieces of one that a warp fetches (with a shift also those
+// behind its runs of 32).
+constexpr int kStages = 2;
+template <bool kShifted>
+constexpr int ring_slots() { return kLoads * (kShifted ? 33 : 32); }
 
-// One block a segment of a row, in one pass: tiles of kTile elements, the next ones on their
+// One block a segment of a row, in one pass: tiles of kTileBytes, the next one on its
 // way to shared memory while one is in registers.  Per thread the sum of exp against a
 // reference m: the first tile's maximum, later the thread's own where it is larger, so that
 // m of the largest element's thread is that element.  Where the sums of a part's
@@ -307,16 +306,17 @@ constexpr int ring_slots() { return 32 * kPerThread * Elem<DT>::bytes / 16 + (kS
 // kShifted) 16 bytes of elements are put together from the two aligned pieces they lie in.
 //
 // Bound by memory with fp32 logits (256 rows of 262,144: 48 us with the join, 5.6 TB/s), by
-// the issue of instructions with 16-bit ones (600 rows of 131,072 bf16: 39 us, 4.0 TB/s), and
-// by the way of the first tile and the merges in short segments (128 rows of 131,072 bf16, four
-// segments each: 23 us, of which the join's 5).
+// the issue of instructions with 16-bit ones (600 rows of 131,072 bf16: 36 us, 4.3 TB/s; four
+// pieces a thread and tile for every type, as what a tile costs besides its elements is half of
+// it: two pieces, 4,096 elements a tile, took 39 us), and by the way of the first tile and the
+// merges in short segments (128 rows of 131,072 bf16, four segments each: 21 us with the
+// join).
 template <int DT, bool kShifted>
 __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kVec = 16 / Elem<DT>::bytes;  // elements of a 16-byte piece
-  constexpr int kLoads = kPerThread / kVec;   // pieces of a tile that a thread takes
   constexpr int kStep = kLoads * kThreads;    // pieces of a tile
-  constexpr int kStages = ring_stages<DT>(), kSlots = ring_slots<DT, kShifted>();
+  constexpr int kSlots = ring_slots<kShifted>();
   asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks come up while the last segments run
   extern __shared__ __align__(16) unsigned char raw[];
   SegmentShared& sh = *reinterpret_cast<SegmentShared*>(raw);
@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
   const unsigned shift = kShifted ? reinterpret_cast<uintptr_t>(x) % 16 : 0;
   const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - shift);
 
-  // a warp's pieces of a tile follow one another, and it alone reads what it fetches
-  const int own = warp * 32 * kLoads + lane;
+  // a thread's pieces of a tile lie kThreads apart, and a warp alone reads what it fetches
+  constexpr int kRun = kSlots / kLoads;  // slots of 32 neighbouring pieces
+  const int own = threadIdx.x;
   uint4* ring = reinterpret_cast<uint4*>(raw + sizeof(SegmentShared)) + warp * kSlots + lane;
   auto fetch = [&](uint4* dst, int at) {
     if constexpr (kShifted) {  // a piece that reaches over the row's ends: its elements alone
@@ -352,9 +353,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
     const int at = base + own, stop = end + (kShifted ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      if (at + i * 32 < stop) fetch(slot + i * 32, at + i * 32);
-    if constexpr (kShifted)
-      if (lane == 0 && at + kLoads * 32 < stop) fetch(slot + kLoads * 32, at + kLoads * 32);
+      if (at + i * kThreads < stop) fetch(slot + i * kRun, at + i * kThreads);
+    if constexpr (kShifted) {  // the pieces behind the runs: lane i fetches run i's
+      const int behind = at - lane + lane * kThreads + 32;
+      if (lane < kLoads && behind < stop) fetch(slot - lane + lane * kRun + 32, behind);
+    }
     async_commit();
   };
 #pragma unroll
@@ -393,13 +396,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
       Part<DT> v;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        if constexpr (kShifted) v.put(i, shifted(slot[i * 32], slot[i * 32 + 1], shift));
-        else v.put(i, slot[i * 32]);
+        if constexpr (kShifted) v.put(i, shifted(slot[i * kRun], slot[i * kRun + 1], shift));
+        else v.put(i, slot[i * kRun]);
       }
       if (tile + kStep > end) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-          if (mine + i * 32 >= end) v.put(i, make_uint4(v.empty(), v.empty(), v.empty(), v.empty()));
+          if (mine + i * kThreads >= end) v.put(i, make_uint4(v.empty(), v.empty(), v.empty(), v.empty()));
       }
       if (tile == first) {
         least = group_bound(v.maximum(), k, sh.groups);
@@ -424,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
         for (unsigned left = v.reach(least, sums, bound); left; left &= left - 1) {
           const int i = __ffs(left) - 1;  // its value comes from the ring: registers have no index
           const T* at =
-              reinterpret_cast<const T*>(reinterpret_cast<const unsigned char*>(slot + i / kVec * 32) + shift);
-          full |= push_candidate(sh, clean_logit<DT>(at[i % kVec]), (mine + i / kVec * 32) * kVec + i % kVec, least,
+              reinterpret_cast<const T*>(reinterpret_cast<const unsigned char*>(slot + i / kVec * kRun) + shift);
+          full |= push_candidate(sh, clean_logit<DT>(at[i % kVec]), (mine + i / kVec * kThreads) * kVec + i % kVec, least,
                                  threshold, spare);
         }
       }
@@ -707,16 +710,17 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
 }  // namespace
 
 // Segments of a row: rows are cut as long as the grid fits at once (four blocks an SM), but
-// no finer than half a tile.  (As many as six blocks an SM would take: 128 rows of 131,072 bf16
-// 30 us against 23, 256 of 262,144 fp32 63 against 48.)
-int beam_segments(long long rows, int vocab_size) {
-  const long long fit = 152 * 4 / rows, most = (vocab_size + kTile / 2 - 1) / (kTile / 2);
+// no finer than a tile.  (128 rows of 131,072 bf16, 256 of 262,144 fp32: 23 and 48 us, with as
+// many as six blocks an SM would take 30 and 63.  16 rows of 131,072 bf16: 8.3 us, with half
+// tiles 9.7; four of 32,000 fp32: 7.1, with two tiles 8.1.)
+int beam_segments(long long rows, int vocab_size, int elem_bytes) {
+  const long long fit = 152 * 4 / rows, least = kTileBytes / elem_bytes, most = (vocab_size + least - 1) / least;
   return static_cast<int>(fit < 1 ? 1 : fit < most ? fit : most);
 }
 
 template <int DT, bool kShifted>
 static cudaError_t launch_segments(const BeamParams& p, cudaStream_t stream) {
-  const int smem = sizeof(SegmentShared) + ring_stages<DT>() * kWarps * ring_slots<DT, kShifted>() * 16;
+  const int smem = sizeof(SegmentShared) + kStages * kWarps * ring_slots<kShifted>() * 16;
   const cudaError_t e = set_smem<beam_segment_kernel<DT, kShifted>>(smem);
   if (e != cudaSuccess) return e;
   beam_segment_kernel<DT, kShifted><<<dim3(p.num_segments, p.num_seqs * p.num_beams), kThreads, smem, stream>>>(p);
@@ -728,8 +732,8 @@ static cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
   const bool one = p.num_seqs * p.num_beams == 1;
   const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                        (one || p.row_stride * Elem<DT>::bytes % 16 == 0);
-  // rows on the grid are read as they lie (256 rows of 262,144 fp32: 48 us, 62 the shifted way;
-  // 128 of 131,072 bf16: 23 and 26)
+  // rows on the grid are read as they lie (256 rows of 262,144 fp32: 48 us, 66 the shifted way;
+  // 128 of 131,072 bf16: 21 and 24)
   return aligned ? launch_segments<DT, false>(p, stream) : launch_segments<DT, true>(p, stream);
 }
 

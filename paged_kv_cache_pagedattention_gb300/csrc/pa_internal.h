@@ -140,7 +140,7 @@ struct BeamParams {
   int num_segments;          // blocks a row
 };
 
-int beam_segments(long long rows, int vocab_size);
+int beam_segments(long long rows, int vocab_size, int elem_bytes);
 cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream);
 
 // Pages of sequences.  Rows are the table rows a call changes; parents are pa_fork_blocks'.
