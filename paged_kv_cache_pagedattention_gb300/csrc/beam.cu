@@ -21,7 +21,7 @@ constexpr int kWindow = 8;      // tiles between the block's barriers
 constexpr int kRoom = 1024;     // candidates a block can hold
 constexpr int kRescan = 2048;   // elements that are looked at again at a time
 constexpr int kGroups = 64;     // of threads, for bounds
-constexpr int kFew = 48;        // candidates that are ranked without a bound first
+constexpr int kFew = 96;        // candidates that are ranked without a bound first
 constexpr int kMaxKeep = PA_MAX_BEAM_CANDIDATES;
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -309,7 +309,7 @@ constexpr int ring_slots() { return kLoads * (kShifted ? 33 : 32); }
 // the issue of instructions with 16-bit ones (600 rows of 131,072 bf16: 36 us, 4.3 TB/s; four
 // pieces a thread and tile for every type, as what a tile costs besides its elements is half of
 // it: two pieces, 4,096 elements a tile, took 39 us), and by the way of the first tile and the
-// merges in short segments (128 rows of 131,072 bf16, four segments each: 21 us with the
+// merges in short segments (128 rows of 131,072 bf16, four segments each: 20 us with the
 // join).
 template <int DT, bool kShifted>
 __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamParams p) {
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
 }  // namespace
 
 // Segments of a row: rows are cut as long as the grid fits at once (four blocks an SM), but
-// no finer than a tile.  (128 rows of 131,072 bf16, 256 of 262,144 fp32: 23 and 48 us, with as
+// no finer than a tile.  (128 rows of 131,072 bf16, 256 of 262,144 fp32: 20 and 48 us, with as
 // many as six blocks an SM would take 30 and 63.  16 rows of 131,072 bf16: 8.3 us, with half
 // tiles 9.7; four of 32,000 fp32: 7.1, with two tiles 8.1.)
 int beam_segments(long long rows, int vocab_size, int elem_bytes) {
@@ -733,7 +733,7 @@ static cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
   const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                        (one || p.row_stride * Elem<DT>::bytes % 16 == 0);
   // rows on the grid are read as they lie (256 rows of 262,144 fp32: 48 us, 66 the shifted way;
-  // 128 of 131,072 bf16: 21 and 24)
+  // 128 of 131,072 bf16: 20 and 23)
   return aligned ? launch_segments<DT, false>(p, stream) : launch_segments<DT, true>(p, stream);
 }
 
