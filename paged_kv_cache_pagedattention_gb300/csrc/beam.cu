@@ -7,6 +7,8 @@
 // row the order is the logits' own, so the rows are cut into segments; each gives its
 // maximum and sum of the softmax and its best logits, and a second kernel joins the
 // segments of a sequence's rows.
+#include <type_traits>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -178,20 +180,15 @@ __device__ __forceinline__ bool push_candidate(SegmentShared& sh, float value, u
   return at >= spare;
 }
 
-// 16 bytes from byte `shift` (0 .. 15) of the 32 in lo and hi.
-__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, unsigned shift) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (shift & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (shift & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const unsigned bits = 8 * (shift & 3);
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+// 16 bytes from byte 4 kWord + bits / 8 of the 32 in lo and hi; kHalves: bits may be 16.
+template <int kWord, bool kHalves>
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, unsigned bits) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if constexpr (kHalves)
+    return make_uint4(__funnelshift_r(w[kWord], w[kWord + 1], bits), __funnelshift_r(w[kWord + 1], w[kWord + 2], bits),
+                      __funnelshift_r(w[kWord + 2], w[kWord + 3], bits),
+                      __funnelshift_r(w[kWord + 3], w[kWord + 4], bits));
+  else return make_uint4(w[kWord], w[kWord + 1], w[kWord + 2], w[kWord + 3]);
 }
 
 // A thread's part of a tile: kLoads pieces as they lie in memory.
@@ -351,6 +348,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
   auto load = [&](int base, int stage) {
     uint4* slot = ring + stage * (kSlots * kWarps);
     const int at = base + own, stop = end + (kShifted ? 1 : 0);
+    // a whole tile inside the row: no piece is asked for its place (without a shift this gained nothing)
+    if (kShifted && base > 0 && base + kStep < pieces && base + kStep <= end) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) async_copy16(slot + i * kRun, src + at + i * kThreads);
+      if (lane < kLoads) async_copy16(slot - lane + lane * kRun + 32, src + (at - lane + lane * kThreads + 32));
+      async_commit();
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       if (at + i * kThreads < stop) fetch(slot + i * kRun, at + i * kThreads);
@@ -394,10 +399,23 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
       if constexpr (kShifted) __syncwarp();
       const uint4* slot = ring + stage * (kSlots * kWarps);
       Part<DT> v;
+      auto read = [&](auto word) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        if constexpr (kShifted) v.put(i, shifted(slot[i * kRun], slot[i * kRun + 1], shift));
-        else v.put(i, slot[i * kRun]);
+        for (int i = 0; i < kLoads; ++i) {
+          if constexpr (kShifted)
+            v.put(i, shifted<word.value, sizeof(T) < 4>(slot[i * kRun], slot[i * kRun + 1], 8 * (shift % 4)));
+          else v.put(i, slot[i * kRun]);
+        }
+      };
+      if constexpr (kShifted) {  // the same way for the whole block, so no word is chosen by data
+        switch (shift / 4) {
+          case 0: read(std::integral_constant<int, 0>()); break;
+          case 1: read(std::integral_constant<int, 1>()); break;
+          case 2: read(std::integral_constant<int, 2>()); break;
+          default: read(std::integral_constant<int, 3>());
+        }
+      } else {
+        read(std::integral_constant<int, 0>());
       }
       if (tile + kStep > end) {
 #pragma unroll
@@ -732,8 +750,8 @@ static cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
   const bool one = p.num_seqs * p.num_beams == 1;
   const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                        (one || p.row_stride * Elem<DT>::bytes % 16 == 0);
-  // rows on the grid are read as they lie (256 rows of 262,144 fp32: 48 us, 66 the shifted way;
-  // 128 of 131,072 bf16: 20 and 23)
+  // rows on the grid are read as they lie (256 rows of 262,144 fp32: 48 us, 56 the shifted way;
+  // 128 of 131,072 bf16: 20 and 22)
   return aligned ? launch_segments<DT, false>(p, stream) : launch_segments<DT, true>(p, stream);
 }
 
