@@ -165,3 +165,66 @@ def test_beam_search(reference, graph):
     assert state[0][1].tolist() == [n + STEPS - 1 for n in PROMPTS for _ in range(BEAMS)]
     pa.pa_release_blocks(*state[0], refs, BS)
     assert not bool(refs.any()) and pa.pa_get_error_flags(clear=True) == 0
+
+
+def test_traced_calls_and_two_streams_at_once():
+    """Every call is traced under its own kind; with tracing off again, two streams run steps side by
+    side on pools and buffers of their own and get what one after the other gives."""
+    import paged_kv_cache_pagedattention_gb300 as pa
+
+    def state(seed):
+        g = torch.Generator().manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+        n, blocks = 6, 64
+        s = {"tables": i32(n, 8), "lens": i32(n), "refs": i32(blocks), "t2": i32(n, 8), "l2": i32(n),
+             "qsl": (torch.arange(n + 1) * 9).int().to(DEV), "slots": torch.zeros(9 * n, dtype=torch.int64, device=DEV),
+             "pairs": torch.zeros(n, 2, dtype=torch.int64, device=DEV),
+             "ws": pa.workspace_tensor(pa.pa_append_workspace_size(n, 9 * n, BS)),
+             "q": rnd(9 * n, HQ, D), "k": rnd(9 * n, HKV, D), "v": rnd(9 * n, HKV, D), "q_out": rnd(9 * n, HQ, D),
+             "kc": torch.zeros(blocks, HKV, BS, D, device=DEV), "vc": torch.zeros(blocks, HKV, BS, D, device=DEV),
+             "pos": (torch.arange(9 * n) % 9).int().to(DEV), "freq": pa.pa_rotary_frequencies(ROT)[0],
+             "logits": rnd(n, VOCAB), "cum": rnd(2, 3), "scores": rnd(2, 3), "tokens": i32(2, 3), "parents": i32(2, 3),
+             "bws": pa.workspace_tensor(pa.pa_beam_select_workspace_size(2, 3, VOCAB, 3))}
+        return s
+
+    def step(s):
+        pa.pa_append_blocks(s["tables"], s["lens"], s["qsl"], s["slots"], s["pairs"], s["refs"], BS, s["ws"])
+        pa.pa_copy_blocks(s["kc"], s["vc"], s["pairs"])
+        pa.pa_rotary_and_cache(s["q_out"], s["q"], s["k"], s["v"], s["kc"], s["vc"], s["pos"], s["slots"], s["freq"])
+        pa.pa_beam_select(s["scores"], s["tokens"], s["parents"], s["logits"], s["cum"], s["bws"])
+        pa.pa_fork_blocks(s["t2"], s["l2"], s["tables"], s["lens"], s["parents"].view(-1), s["refs"], BS)
+        pa.pa_release_blocks(s["tables"], s["lens"], s["refs"], BS)
+        for a, b in (("tables", "t2"), ("lens", "l2")):
+            s[a], s[b] = s[b], s[a]
+
+    kinds = ("rotary_and_cache", "beam_select", "fork_blocks", "append_blocks", "release_blocks")
+    want = [state(1), state(2)]
+    pa.pa_trace_enable(True)
+    try:
+        pa.pa_trace_read(0, reset=True)
+        for s in want:
+            for _ in range(4):
+                step(s)
+        torch.cuda.synchronize()
+        for kind, name in enumerate(pa.TRACE_KINDS):
+            count, ms = pa.pa_trace_read(kind)
+            assert count == (8 if name in kinds or name == "copy_blocks" else 0), name
+            assert ms > 0 or count == 0
+    finally:
+        pa.pa_trace_enable(False)
+        pa.pa_trace_read(0, reset=True)
+    got, streams = [state(1), state(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, stream in zip(got, streams):
+            with torch.cuda.stream(stream):
+                step(s)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[k], b[k]) for k in ("lens", "refs", "slots", "pairs", "kc", "vc", "q_out", "scores",
+                                                     "tokens", "parents"))
+        held = -(-a["lens"] // BS)
+        for row, n in enumerate(held.tolist()):
+            assert torch.equal(a["tables"][row, :n], b["tables"][row, :n])
+    assert pa.pa_get_error_flags(clear=True) == 0
