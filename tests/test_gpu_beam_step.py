@@ -167,6 +167,7 @@ def test_beam_search(reference, graph):
     assert not bool(refs.any()) and pa.pa_get_error_flags(clear=True) == 0
 
 
+@pytest.mark.gpu
 def test_traced_calls_and_two_streams_at_once():
     """Every call is traced under its own kind; with tracing off again, two streams run steps side by
     side on pools and buffers of their own and get what one after the other gives."""
