@@ -285,12 +285,13 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
         _check_heads(value, "value")
     hq = q_ptr = q_out_ptr = q_stride = q_out_stride = 0
     if q is not None or q_out is not None:
-        if q is None or q_out is None or q.dim() != 3 or q_out.shape != q.shape or q.dtype is not dtype or \
-                q_out.dtype is not dtype or q.shape[0] != t or q.shape[2] != d:
+        q_shape = None if q is None else q.shape
+        if q_out is None or q_shape is None or q_out.shape != q_shape or len(q_shape) != 3 or \
+                q.dtype is not dtype or q_out.dtype is not dtype or q_shape[0] != t or q_shape[2] != d:
             raise ValueError("q/q_out must be [num_tokens][num_q_heads][head_size] of key's dtype")
         if q.get_device() != dev or q_out.get_device() != dev:
             raise ValueError("q/q_out: all tensors must be on one CUDA device")
-        hq, q_ptr, q_out_ptr = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        hq, q_ptr, q_out_ptr = q_shape[1], q.data_ptr(), q_out.data_ptr()
         q_stride, q_head, q_elem = q.stride()
         q_out_stride, q_out_head, q_out_elem = q_out.stride()
         if q_elem != 1 or q_out_elem != 1 or q_head != d or q_out_head != d:
@@ -334,15 +335,15 @@ def pa_beam_select(out_scores, out_tokens, out_parents, logits, beam_scores, wor
     """The best candidates of each sequence's beams: out_scores float32, out_tokens and
     out_parents int32, all [num_seqs][num_candidates]; logits [num_seqs*num_beams][vocab]
     (rows may be padded), beam_scores float32 [num_seqs][num_beams]."""
-    if beam_scores.dtype is not torch.float32 or beam_scores.dim() != 2 or not beam_scores.is_contiguous():
+    beams, rows, shape, dev = beam_scores.shape, logits.shape, out_scores.shape, logits.get_device()
+    if beam_scores.dtype is not _float32 or len(beams) != 2 or not beam_scores.is_contiguous():
         raise ValueError("beam_scores must be a contiguous float32 tensor [num_seqs][num_beams]")
-    b, w = beam_scores.shape
-    if logits.dim() != 2 or logits.shape[0] != b * w or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    b, w = beams
+    stride = logits.stride()
+    if len(rows) != 2 or rows[0] != b * w or (stride[1] != 1 and rows[1] > 1):
         raise ValueError("logits must be [num_seqs*num_beams][vocab_size] with contiguous rows")
-    if out_scores.dim() != 2 or out_scores.shape[0] != b or out_scores.dtype is not torch.float32 or \
-            not out_scores.is_contiguous():
+    if len(shape) != 2 or shape[0] != b or out_scores.dtype is not _float32 or not out_scores.is_contiguous():
         raise ValueError("out_scores must be a contiguous float32 tensor [num_seqs][num_candidates]")
-    shape, dev = out_scores.shape, logits.get_device()
     if out_tokens.dtype is not _int32 or out_tokens.shape != shape or not out_tokens.is_contiguous():
         _bad(out_tokens, shape, "out_tokens")
     if out_parents.dtype is not _int32 or out_parents.shape != shape or not out_parents.is_contiguous():
@@ -356,8 +357,8 @@ def pa_beam_select(out_scores, out_tokens, out_parents, logits, beam_scores, wor
         return _on_device(dev, pa_beam_select, out_scores, out_tokens, out_parents, logits, beam_scores, workspace,
                           stream)
     st = _lib.pa_beam_select(
-        out_scores.data_ptr(), out_tokens.data_ptr(), out_parents.data_ptr(), logits.data_ptr(), logits.stride(0),
-        beam_scores.data_ptr(), b, w, logits.shape[1], shape[1], dtype_code(logits), workspace.data_ptr(),
+        out_scores.data_ptr(), out_tokens.data_ptr(), out_parents.data_ptr(), logits.data_ptr(), stride[0],
+        beam_scores.data_ptr(), b, w, rows[1], shape[1], dtype_code(logits), workspace.data_ptr(),
         workspace.nbytes, _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_beam_select"))
     if st != PA_OK:
         raise PAError(st, "pa_beam_select")
