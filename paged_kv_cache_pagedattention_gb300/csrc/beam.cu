@@ -9,6 +9,7 @@
 // segments of a sequence's rows.
 #include <type_traits>
 
+#include "launch.cuh"
 #include "pa_common.cuh"
 
 namespace pa {
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
   constexpr int kVec = 16 / Elem<DT>::bytes;  // elements of a 16-byte piece
   constexpr int kStep = kLoads * kThreads;    // pieces of a tile
   constexpr int kSlots = ring_slots<kShifted>();
-  asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks come up while the last segments run
+  previous_done();
+  next_may_start();  // the join's blocks come up while the last segments run
   extern __shared__ __align__(16) unsigned char raw[];
   SegmentShared& sh = *reinterpret_cast<SegmentShared*>(raw);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -571,7 +573,7 @@ constexpr int kHeld = 4;     // keys a thread loads ahead
 // segments; its blocks are brought up while these still run (as a launch of its own behind
 // them it cost 2 us more).
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the segments are done and their results there
+  previous_done();  // the segments are done and their results there
   extern __shared__ Beam beams[];  // [num_beams]
   __shared__ Key kept[kJoin];
   __shared__ float2 bounds[kJoin];
@@ -741,8 +743,8 @@ static cudaError_t launch_segments(const BeamParams& p, cudaStream_t stream) {
   const int smem = sizeof(SegmentShared) + kStages * kWarps * ring_slots<kShifted>() * 16;
   const cudaError_t e = set_smem<beam_segment_kernel<DT, kShifted>>(smem);
   if (e != cudaSuccess) return e;
-  beam_segment_kernel<DT, kShifted><<<dim3(p.num_segments, p.num_seqs * p.num_beams), kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(beam_segment_kernel<DT, kShifted>, dim3(p.num_segments, p.num_seqs * p.num_beams), kThreads,
+                      smem, 1, p, stream);
 }
 
 template <int DT>
@@ -760,18 +762,7 @@ cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stre
                         : dtype == PA_F16 ? launch_type<PA_F16>(p, stream)
                                           : launch_type<PA_BF16>(p, stream);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(p.num_seqs);
-  config.blockDim = dim3(kThreads);
-  config.dynamicSmemBytes = p.num_beams * sizeof(Beam);
-  config.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = attr;
-  config.numAttrs = 1;
-  const cudaError_t j = cudaLaunchKernelEx(&config, beam_join_kernel, p);
-  return j != cudaSuccess ? j : cudaGetLastError();
+  return launch_early(beam_join_kernel, dim3(p.num_seqs), kThreads, p.num_beams * sizeof(Beam), 1, p, stream);
 }
 
 }  // namespace pa

@@ -8,6 +8,7 @@
 // once (fp64, 53 bits), and p times it modulo 2^64 drops whole turns exactly, so far
 // positions lose nothing to a range reduction (fp32 angles at position 262,144 would be
 // off by up to 2^-7 rad).  The rotation runs in fp32 and is rounded or quantised once.
+#include "launch.cuh"
 #include "pa_common.cuh"
 #include "quantize.cuh"
 
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(256) rotary_generic_kernel(const RotaryParams 
   const long long per_token = q_units + 2 * kv_units;
   const long long total = per_token * p.num_tokens;
   const long long limit = (long long)p.num_blocks * p.block_size;
+  previous_done();
   for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < total;
        u += (long long)gridDim.x * blockDim.x) {
     const long long t = u / per_token;
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(256, CDT == PA_NVFP4 ? 4 : 8) rotary_piece_ker
   // the units are dealt round, so that the threads without a second q unit take k and v
   const int k_first = (threadIdx.x + 256 - q_units % 256) % 256;
   const int plain_first = (threadIdx.x + 512 - (q_units + k_units) % 256) % 256;
+  previous_done();
   load_q(threadIdx.x);
   load_k(k_first);
   load_plain(plain_first);
@@ -387,15 +390,14 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
                       half * sizeof(float2) <= 48 * 1024;
   if (pieces) {
     const size_t smem = half * sizeof(float2);
-    if (p.interleaved) rotary_piece_kernel<SRC, CDT, true><<<p.num_tokens, 256, smem, stream>>>(p);
-    else rotary_piece_kernel<SRC, CDT, false><<<p.num_tokens, 256, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(p.interleaved ? rotary_piece_kernel<SRC, CDT, true> : rotary_piece_kernel<SRC, CDT, false>,
+                        dim3(p.num_tokens), 256, smem, 1, p, stream);
   }
   const long long per_token = (long long)p.num_q_heads * ((half + 3) / 4 + (p.head_size - p.rotary_dim + 7) / 8) +
                               2ll * (p.head_size / (SRC == CDT ? kKv : 16)) * p.num_kv_heads;
   const long long blocks = (per_token * p.num_tokens + 255) / 256;
-  rotary_generic_kernel<SRC, CDT><<<static_cast<int>(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(rotary_generic_kernel<SRC, CDT>, dim3(static_cast<unsigned>(blocks < 152 * 64 ? blocks : 152 * 64)),
+                      256, 0, 1, p, stream);
 }
 
 template <int SRC>

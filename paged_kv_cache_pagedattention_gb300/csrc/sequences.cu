@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "pa_common.cuh"
 
 namespace pa {
@@ -34,6 +35,7 @@ __device__ __forceinline__ bool length_ok(const SequenceParams& p, int len) {
 // latency in short rows (2 us), by the counts' atomics in long ones (1,024 children of 8,192
 // blocks: 13 us).
 __global__ void __launch_bounds__(kTableThreads) fork_kernel(const SequenceParams p) {
+  previous_done();
   const int child = blockIdx.x;
   const int parent = p.parents[child];
   int len = 0;
@@ -74,6 +76,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_parents_kernel(const Seque
   __shared__ int count;
   const int parent = blockIdx.x;
   if (threadIdx.x == 0) count = 0;
+  previous_done();
   const int len_given = p.parent_lens[parent];
   __syncthreads();
   const int first = blockIdx.z * p.fork_part, past = min(p.num_rows, first + p.fork_part);
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_parents_kernel(const Seque
 __global__ void __launch_bounds__(kTableThreads) release_kernel(const SequenceParams p) {
   const cg::cluster_group cluster = cg::this_cluster();
   const int row = blockIdx.x / cluster.num_blocks(), part = cluster.block_rank();
+  previous_done();
   const int len = p.seq_lens[row];
   const int keep = p.keep_lens ? p.keep_lens[row] : 0;
   cluster.sync();
@@ -231,6 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequencePa
   const unsigned bs = p.block_size;
   const bool mine = i < n;
   int len = 0, start = 0, stop = 0;
+  previous_done();
   if (mine) {
     len = p.seq_lens[i];
     start = p.query_start_loc[i];
@@ -409,22 +414,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequencePa
   }
 }
 
-cudaError_t launch_cluster(void (*kernel)(SequenceParams), const SequenceParams& p, int grid, int cluster,
-                           int threads, cudaStream_t stream) {
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(grid);
-  config.blockDim = dim3(threads);
-  config.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  config.attrs = attr;
-  config.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
@@ -444,28 +433,23 @@ cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
     SequenceParams q = p;
     const int parts = std::max(least, std::min(fill, most));
     q.fork_part = (rows + parts - 1) / parts;
-    fork_parents_kernel<<<dim3(p.num_parents, y, parts), kTableThreads, 0, stream>>>(q);
-  } else {
-    fork_kernel<<<dim3(rows, y), kTableThreads, 0, stream>>>(p);
+    return launch_early(fork_parents_kernel, dim3(p.num_parents, y, parts), kTableThreads, 0, 1, q, stream);
   }
-  return cudaGetLastError();
+  return launch_early(fork_kernel, dim3(rows, y), kTableThreads, 0, 1, p, stream);
 }
 
 cudaError_t launch_release_blocks(const SequenceParams& p, cudaStream_t stream) {
   // blocks a row: enough for its longest table, at kTableUnroll entries a thread
   int cluster = 1;
   while (cluster < 8 && p.num_rows < (1 << 27) && cluster * kTableThreads * kTableUnroll < p.max_blocks_per_seq) cluster *= 2;
-  return launch_cluster(release_kernel, p, p.num_rows * cluster, cluster, kTableThreads, stream);
+  return launch_early(release_kernel, dim3(p.num_rows * cluster), kTableThreads, 0, cluster, p, stream);
 }
 
 cudaError_t launch_append_blocks(const SequenceParams& p, cudaStream_t stream) {
   // one block where it has a thread for every row: a cluster of one takes 3 us longer
-  if (p.num_rows <= kAppendThreads) {
-    append_kernel<false><<<1, kAppendThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-  }
+  if (p.num_rows <= kAppendThreads) return launch_early(append_kernel<false>, dim3(1), kAppendThreads, 0, 1, p, stream);
   const int parts = (p.num_rows + kAppendThreads - 1) / kAppendThreads;
-  return launch_cluster(append_kernel<true>, p, parts, parts, kAppendThreads, stream);
+  return launch_early(append_kernel<true>, dim3(parts), kAppendThreads, 0, parts, p, stream);
 }
 
 }  // namespace pa

@@ -167,37 +167,47 @@ def test_beam_search(reference, graph):
     assert not bool(refs.any()) and pa.pa_get_error_flags(clear=True) == 0
 
 
+def state(seed):
+    import paged_kv_cache_pagedattention_gb300 as pa
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    n, blocks = 6, 64
+    s = {"tables": i32(n, 8), "lens": i32(n), "refs": i32(blocks), "t2": i32(n, 8), "l2": i32(n),
+         "qsl": (torch.arange(n + 1) * 9).int().to(DEV), "slots": torch.zeros(9 * n, dtype=torch.int64, device=DEV),
+         "pairs": torch.zeros(n, 2, dtype=torch.int64, device=DEV),
+         "ws": pa.workspace_tensor(pa.pa_append_workspace_size(n, 9 * n, BS)),
+         "q": rnd(9 * n, HQ, D), "k": rnd(9 * n, HKV, D), "v": rnd(9 * n, HKV, D), "q_out": rnd(9 * n, HQ, D),
+         "kc": torch.zeros(blocks, HKV, BS, D, device=DEV), "vc": torch.zeros(blocks, HKV, BS, D, device=DEV),
+         "pos": (torch.arange(9 * n) % 9).int().to(DEV), "freq": pa.pa_rotary_frequencies(ROT)[0],
+         "logits": rnd(n, VOCAB), "cum": rnd(2, 3), "scores": rnd(2, 3), "tokens": i32(2, 3), "parents": i32(2, 3),
+         "bws": pa.workspace_tensor(pa.pa_beam_select_workspace_size(2, 3, VOCAB, 3))}
+    return s
+
+
+def step(s, between=lambda: None):
+    import paged_kv_cache_pagedattention_gb300 as pa
+    between()
+    pa.pa_append_blocks(s["tables"], s["lens"], s["qsl"], s["slots"], s["pairs"], s["refs"], BS, s["ws"])
+    between()
+    pa.pa_copy_blocks(s["kc"], s["vc"], s["pairs"])
+    between()
+    pa.pa_rotary_and_cache(s["q_out"], s["q"], s["k"], s["v"], s["kc"], s["vc"], s["pos"], s["slots"], s["freq"])
+    between()
+    pa.pa_beam_select(s["scores"], s["tokens"], s["parents"], s["logits"], s["cum"], s["bws"])
+    between()
+    pa.pa_fork_blocks(s["t2"], s["l2"], s["tables"], s["lens"], s["parents"].view(-1), s["refs"], BS)
+    between()
+    pa.pa_release_blocks(s["tables"], s["lens"], s["refs"], BS)
+    for a, b in (("tables", "t2"), ("lens", "l2")):
+        s[a], s[b] = s[b], s[a]
+
+
 @pytest.mark.gpu
 def test_traced_calls_and_two_streams_at_once():
     """Every call is traced under its own kind; with tracing off again, two streams run steps side by
     side on pools and buffers of their own and get what one after the other gives."""
     import paged_kv_cache_pagedattention_gb300 as pa
-
-    def state(seed):
-        g = torch.Generator().manual_seed(seed)
-        rnd = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
-        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
-        n, blocks = 6, 64
-        s = {"tables": i32(n, 8), "lens": i32(n), "refs": i32(blocks), "t2": i32(n, 8), "l2": i32(n),
-             "qsl": (torch.arange(n + 1) * 9).int().to(DEV), "slots": torch.zeros(9 * n, dtype=torch.int64, device=DEV),
-             "pairs": torch.zeros(n, 2, dtype=torch.int64, device=DEV),
-             "ws": pa.workspace_tensor(pa.pa_append_workspace_size(n, 9 * n, BS)),
-             "q": rnd(9 * n, HQ, D), "k": rnd(9 * n, HKV, D), "v": rnd(9 * n, HKV, D), "q_out": rnd(9 * n, HQ, D),
-             "kc": torch.zeros(blocks, HKV, BS, D, device=DEV), "vc": torch.zeros(blocks, HKV, BS, D, device=DEV),
-             "pos": (torch.arange(9 * n) % 9).int().to(DEV), "freq": pa.pa_rotary_frequencies(ROT)[0],
-             "logits": rnd(n, VOCAB), "cum": rnd(2, 3), "scores": rnd(2, 3), "tokens": i32(2, 3), "parents": i32(2, 3),
-             "bws": pa.workspace_tensor(pa.pa_beam_select_workspace_size(2, 3, VOCAB, 3))}
-        return s
-
-    def step(s):
-        pa.pa_append_blocks(s["tables"], s["lens"], s["qsl"], s["slots"], s["pairs"], s["refs"], BS, s["ws"])
-        pa.pa_copy_blocks(s["kc"], s["vc"], s["pairs"])
-        pa.pa_rotary_and_cache(s["q_out"], s["q"], s["k"], s["v"], s["kc"], s["vc"], s["pos"], s["slots"], s["freq"])
-        pa.pa_beam_select(s["scores"], s["tokens"], s["parents"], s["logits"], s["cum"], s["bws"])
-        pa.pa_fork_blocks(s["t2"], s["l2"], s["tables"], s["lens"], s["parents"].view(-1), s["refs"], BS)
-        pa.pa_release_blocks(s["tables"], s["lens"], s["refs"], BS)
-        for a, b in (("tables", "t2"), ("lens", "l2")):
-            s[a], s[b] = s[b], s[a]
 
     kinds = ("rotary_and_cache", "beam_select", "fork_blocks", "append_blocks", "release_blocks")
     want = [state(1), state(2)]
@@ -228,4 +238,65 @@ def test_traced_calls_and_two_streams_at_once():
         held = -(-a["lens"] // BS)
         for row, n in enumerate(held.tolist()):
             assert torch.equal(a["tables"][row, :n], b["tables"][row, :n])
+    assert pa.pa_get_error_flags(clear=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("before", ["nothing", "memset", "copy", "join", "kernel"])
+def test_calls_behind_other_work(before):
+    """The calls may begin while the work before them ends: a fill, a copy, another stream's kernel
+    or a long kernel that writes what they read is waited for, eagerly and as a graph."""
+    import paged_kv_cache_pagedattention_gb300 as pa
+
+    side = torch.cuda.Stream()
+    filler, big = torch.zeros(1 << 24, device=DEV), torch.ones(1 << 24, device=DEV)
+
+    def between():
+        if before == "memset":
+            filler.zero_()
+        elif before == "copy":
+            filler.copy_(big)
+        elif before == "kernel":
+            torch.add(big, 1.0, out=filler)
+        elif before == "join":
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                torch.add(big, 1.0, out=filler)
+            main.wait_stream(side)
+
+    def late_inputs(s, g):
+        """Every input of the calls is written by the kernel right before them."""
+        def between_writes():
+            between()
+            for name in ("q", "k", "v", "logits", "cum"):
+                s[name].copy_(g[name])
+            torch.mul(g["pos"], 1, out=s["pos"])
+        return between_writes
+
+    want, good = state(5), state(5)
+    for _ in range(3):
+        step(want)
+    torch.cuda.synchronize()
+    got = state(5)
+    for name in ("q", "k", "v", "logits", "cum", "pos"):
+        got[name].zero_()
+    for _ in range(3):
+        step(got, late_inputs(got, good))
+    torch.cuda.synchronize()
+    same = ("lens", "refs", "slots", "pairs", "kc", "vc", "q_out", "scores", "tokens", "parents")
+    assert all(torch.equal(want[k], got[k]) for k in same)
+    # captured: two steps a graph, so that tables and lengths end in the arrays they began in
+    ref, cap = state(6), state(6)
+    for _ in range(6):
+        step(ref)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(cap, between)
+        step(cap, between)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref[k], cap[k]) for k in same)
     assert pa.pa_get_error_flags(clear=True) == 0
