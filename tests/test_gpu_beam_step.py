@@ -300,3 +300,39 @@ def test_calls_behind_other_work(before):
     torch.cuda.synchronize()
     assert all(torch.equal(ref[k], cap[k]) for k in same)
     assert pa.pa_get_error_flags(clear=True) == 0
+
+
+@pytest.mark.gpu
+def test_default_stream_waits_for_blocking_streams():
+    """The default stream waits by itself for streams that are not created as non-blocking: inputs that
+    such a stream writes behind long kernels are there when the calls read them, without an event."""
+    import ctypes
+
+    import paged_kv_cache_pagedattention_gb300 as pa
+
+    handle = ctypes.c_size_t(0)
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(handle))) == 0
+    other = torch.cuda.ExternalStream(handle.value)
+    big, filler = torch.ones(1 << 26, device=DEV), torch.zeros(1 << 26, device=DEV)
+    want, got, good = state(8), state(8), state(8)
+    for name in ("q", "k", "v", "logits", "cum"):
+        got[name].zero_()
+    assert torch.cuda.current_stream().cuda_stream == 0
+
+    def between():
+        with torch.cuda.stream(other):
+            torch.add(big, 1.0, out=filler)
+            for name in ("q", "k", "v", "logits", "cum"):
+                got[name].copy_(good[name])
+            torch.mul(good["pos"], 1, out=got["pos"])
+
+    for _ in range(3):
+        step(want)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        step(got, between)
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[k], got[k]) for k in ("lens", "refs", "slots", "pairs", "kc", "vc", "q_out", "scores",
+                                                      "tokens", "parents"))
+    assert int(torch.cuda.cudart().cudaStreamDestroy(handle.value)) == 0
+    assert pa.pa_get_error_flags(clear=True) == 0
