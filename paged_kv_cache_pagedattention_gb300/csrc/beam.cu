@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamPar
       float4 sums = m != kNegInf ? v.exp_sums(m) : make_float4(0.f, 0.f, 0.f, 0.f);
       if (!(sums.x < bound && sums.y < bound && sums.z < bound && sums.w < bound)) {
         constexpr float kBelow = 1.f - 0x1p-10f;  // of no element above m
-        if (!(sums.x < kBelow && sums.y < kBelow && sums.z < kBelow && sums.w < kBelow)) {
+        // without a reference yet (a first tile of -inf and NaN alone) the sums say nothing
+        if (m == kNegInf || !(sums.x < kBelow && sums.y < kBelow && sums.z < kBelow && sums.w < kBelow)) {
           const float top = v.maximum();
           if (top > m || !((sums.x + sums.y) + (sums.z + sums.w) < INFINITY)) {  // a new reference; or NaN or +inf
             const float m2 = fmaxf(m, top);
