@@ -261,7 +261,8 @@ def pa_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, 
     _check(_lib.pa_rotary_frequencies(host, ctypes.byref(attn), int(rotary_dim), float(base),
                                       ROTARY_SCALINGS[scaling], float(factor), float(original_max_position),
                                       float(low_turns), float(high_turns)), "pa_rotary_frequencies")
-    return torch.tensor(list(host), dtype=torch.float32, device=device or "cuda"), float(attn.value)
+    freq = torch.tensor(list(host), dtype=torch.float32, device="cuda" if device is None else device)
+    return freq, float(attn.value)
 
 
 def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
