@@ -590,4 +590,4 @@ def pa_trace_read(kind: int, reset: bool = False):
 
 def workspace_tensor(nbytes: int, device=None) -> torch.Tensor:
     """A device byte buffer suitable as `workspace` (torch allocations are 256-byte aligned)."""
-    return torch.empty(int(nbytes), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(int(nbytes), dtype=torch.uint8, device="cuda" if device is None else device)

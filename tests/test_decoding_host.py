@@ -15,3 +15,11 @@ def test_frequencies_are_made_on_the_device_that_is_asked_for(pa, monkeypatch, a
     freq, attn = pa.pa_rotary_frequencies(8, device=asked)
     assert seen == [made_on] and type(seen[0]) is type(made_on)
     assert freq.shape == (4,) and attn == 1.0
+
+
+@pytest.mark.parametrize("asked,made_on", [(None, "cuda"), (0, 0), (1, 1), ("cpu", "cpu")])
+def test_workspaces_are_made_on_the_device_that_is_asked_for(pa, monkeypatch, asked, made_on):  # noqa: F811
+    seen, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: (seen.append(device), empty(n, dtype=dtype))[1])
+    assert pa.workspace_tensor(512, asked).numel() == 512
+    assert seen == [made_on] and type(seen[0]) is type(made_on)
