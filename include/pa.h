@@ -252,8 +252,10 @@ pa_status pa_rotary_frequencies(float* inv_freq, float* attn_factor, int32_t rot
  *   s = attn_factor sin theta, pair i < R/2 of every q and k head becomes
  *   (x c - y s, y c + x s).  Pairs are elements (i, i + R/2), or (2i, 2i + 1) where
  *   interleaved != 0; elements from R = rotary_dim on stay as they are, and so does v.
- *   theta is formed exactly (64-bit fixed point turns), so every int32 position is
- *   served, negative ones too; the rotation runs in fp32 and its result is rounded
+ *   theta is kept in turns, in fixed point: inv_freq[i] / 2 pi in fp64, whole turns of its product
+ *   with the position drop out exactly, and the rest is held to 2^-32 of a turn, so theta is off
+ *   by |theta| 2^-52 + 2^-28 rad at most (inv_freq >= 0), at every int32 position, negative ones
+ *   too; the rotation runs in fp32 and its result is rounded
  *   once: q to q_out, k to the cache (FP8 and NVFP4: quantised from fp32 by the rules of
  *   pa_reshape_and_cache, not from k rounded to src_dtype).
  *

@@ -11,13 +11,14 @@ __device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.w
 
 // The kernel behind this one in the stream, if launched by launch_early, may come up as soon as
 // all blocks of this one have.  For a call's own second kernel: between calls it gained nothing
-// and its waiting blocks stood in the way (long forks 25 -> 30 us).
+// and its waiting blocks stood in the way (long forks, captured, 25 -> 30 us).
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A launch that may begin when the kernel before it ends, without a gap for the end to be seen
-// by the host's queue (eager calls back to back: beam selection 12.4 -> 10.3 us and 22.5 -> 19.8,
-// the rotary write of 2,176 tokens 12.4 -> 10.1, fork, append,
-// copy and release of long forks 34 -> 27).  Clusters of `cluster` blocks along x.
+// by the host's queue.  Eager calls back to back on inputs that change from call to call, without
+// and with it: beam selection of one request 12.3 and 8.1 us, of 128 rows of 131,072 bf16 24.6 and
+// 19.4 (its join included), the rotary write of 2,176 tokens 15.5 and 13.1, fork, append, copy and
+// release of long forks 34.0 and 28.1.  Clusters of `cluster` blocks along x.
 template <typename P>
 cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem, int cluster, const P& p,
                          cudaStream_t stream) {

@@ -249,9 +249,11 @@ __device__ __forceinline__ float2 rotation_of(const float2* table, int pieces, i
 // position and rows, then the rotations) below; what counts is how many tokens are on their
 // way, so registers are held to 32 for eight blocks an SM (8,192 tokens of 64/8 heads, pairs
 // side by side: 52 us, 6.4 TB/s, against 61 us with five blocks and no spills; FP8 cache
-// 54 against 66 us).  256 threads: with 128, 2,176 tokens of 32/8 heads took 12.9 us instead of
-// 13.8, but 256 onto an e4m3 cache 5.0 instead of 4.0; with 512, 15.4 and 3.8, and the long
-// case 65.
+// 54 against 66 us).  256 threads, captured calls on changing inputs: with 128, 2,176 tokens of
+// 32/8 heads take 12.3 us instead of 13.2, but 256 onto an e4m3 cache 4.8 instead of 3.8; with
+// 512, 19.7 and 3.4, and the long case 91.  Onto an NVFP4 cache the groups of 16 go to a few
+// warps of a block, which the others await (2,176 tokens 28 us, 8,192 of 64/8 heads 103, whose
+// bytes take 7 and 46; 43% of the issue slots, the barrier the largest stall).
 template <int SRC, int CDT, bool kInterleaved>
 __global__ void __launch_bounds__(256, CDT == PA_NVFP4 ? 4 : 8) rotary_piece_kernel(const RotaryParams p) {
   using T = typename Elem<SRC>::T;
@@ -381,7 +383,9 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
   constexpr int kBytes = Elem<SRC>::bytes, kKv = kv_unit<SRC, CDT>();
   const int half = p.rotary_dim / 2;
   // Pieces where every row allows them: on 2,176 tokens of 32/8 heads of 128 bf16 the pieces
-  // take 13 us and the generic kernel, which forms a rotation for every head, 82 us.
+  // take 13 us and the generic kernel, which forms a rotation for every head, 82 us.  Rows that
+  // are no pieces: 2,176 tokens of 64/8 heads of 96, 24 elements turned, take 99 us (96 turned,
+  // in pieces: 15), of 32/32 heads of 80, 20 turned, 104.
   const bool pieces = (p.interleaved ? p.rotary_dim : half) % kKv == 0 &&
                       aligned16(p.key, p.key_stride, p.num_tokens, kBytes) &&
                       aligned16(p.value, p.value_stride, p.num_tokens, kBytes) &&

@@ -216,7 +216,15 @@ constexpr unsigned kSharedTail = 1u << 30, kLargeRow = 1u << 31;
 // One row a thread: one block up to kAppendThreads rows, a cluster of them above.  What a row
 // needs stays in its thread's registers.  The first block's warps look through the pool from
 // its lowest block on, until as many free ones are found as all rows need.  All of it is
-// latency, some six dependent trips to memory (256 rows of a pool of 17,000 blocks: 7.7 us).
+// latency, some six dependent trips to memory (256 rows that share tails, a pool of 17,000
+// blocks with free ones all over it: 7.7 us), as long as the pool's first kLook blocks have
+// enough free ones.  Each kLook blocks more that are looked through are one more trip behind
+// the others, about 1.1 us: 256 rows of one new block each, with their release, take 5.7 us
+// where every second block is free, whatever the pool's size, but 6.8, 23 and 142 us where only
+// the last twentieth of 16,384, 131,072 and 1,048,576 blocks is.  Above kAppendThreads rows:
+// 2,048 take 13 us, 8,192 20 us.  Where a row grows by more than kInline tokens, these blocks
+// alone write every slot behind a search for its row: a prompt of 131,072 tokens takes 73 us, 16
+// chunks of 512 among 128 decodes 14.
 template <bool kCluster>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const SequenceParams p) {
   __shared__ AppendShared sh;
@@ -423,7 +431,9 @@ cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
   // the look for a parent's children costs more than its atomics (by parents against by
   // children: 128 parents and 1,024 children of 131,072 tokens 8.3 against 13.4 us, one parent
   // 7.6 against 36; of 1,024 tokens in tables of 64 blocks 3.5 against 2.5, and 1,024 parents
-  // of 131,072 tokens with as many children 19 against 14).
+  // of 131,072 tokens with as many children 19 against 14).  Lengths are on the device, so the
+  // tables' width stands for them: 128 parents and 1,024 children of 1,024 tokens take 2.6 us in
+  // tables of 64 blocks, 3.3 in tables of 8,192.
   if (p.num_parents > 0 && rows / 2 >= p.num_parents && rows <= kForkMost &&
       (long long)rows * p.max_blocks_per_seq >= 1 << 19) {
     // parts of the children until the grid fills the device, of eight for each parent or more
@@ -439,7 +449,9 @@ cudaError_t launch_fork_blocks(const SequenceParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_release_blocks(const SequenceParams& p, cudaStream_t stream) {
-  // blocks a row: enough for its longest table, at kTableUnroll entries a thread
+  // blocks a row: enough for the longest row its table has room for, at kTableUnroll entries a
+  // thread.  Rows far shorter than that pay for blocks with nothing to do: 1,024 rows of 1,024
+  // tokens take 3 us in tables of 64 blocks and 13.5 in tables of 8,192.
   int cluster = 1;
   while (cluster < 8 && p.num_rows < (1 << 27) && cluster * kTableThreads * kTableUnroll < p.max_blocks_per_seq) cluster *= 2;
   return launch_early(release_kernel, dim3(p.num_rows * cluster), kTableThreads, 0, cluster, p, stream);
