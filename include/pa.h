@@ -18,7 +18,9 @@
  *   4. pa_rotary_and_cache   rotary positions of q and k, and the write of 1. in one pass;
  *   5. pa_beam_select        the best continuations of every sequence's beams;
  *   6. pa_fork_blocks, pa_append_blocks, pa_release_blocks   block tables, reference
- *                            counts and slots of sequences that branch, grow and end.
+ *                            counts and slots of sequences that branch, grow and end;
+ *   7. pa_positions_and_slots, pa_rotary_axes_and_cache   positions of text and media on
+ *                            several axes, with slots, and 4. on those axes.
  *
  * Sources, cited by key:
  *   [AGENTIC] "宣稱省下 106 倍成本：vLLM 怎麼把 Serving 系統校準給 Agentic Workload"
@@ -149,6 +151,7 @@ typedef enum pa_dtype {
 #define PA_ERRFLAG_PARENT 0x40u    /* pa_fork_blocks: a parent >= num_parents */
 #define PA_ERRFLAG_POOL 0x80u      /* pa_append_blocks: fewer free blocks than the call needs */
 #define PA_ERRFLAG_REF_COUNT 0x100u /* a block in use whose reference count is below 1 */
+#define PA_ERRFLAG_MEDIA 0x200u     /* pa_positions_and_slots: a medium out of order or range */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* pa_status_string(pa_status status);
@@ -287,6 +290,39 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
                               const float* k_scale, const float* v_scale, pa_stream_t stream);
 
 /*
+ * The axis of every pair of a rotation on several axes (HOST: writes host memory, needs no
+ * device).  Axis a turns sections[a] pairs; the sections' sum is rotary_dim / 2.
+ *   cycled == 0  the axes one after the other: the first sections[0] pairs turn on axis 0, ...
+ *   cycled != 0  the axes dealt round: pair i is axis i % num_axes' while i < num_axes x
+ *                sections[i % num_axes], else axis 0's; PA_ERR_INVALID_ARG where that does not
+ *                give every axis its section
+ */
+#define PA_MAX_ROTARY_AXES 4
+#define PA_MAX_ROTARY_AXES_DIM 512
+
+pa_status pa_rotary_pair_axes(uint8_t* pair_axis, int32_t rotary_dim, const int32_t* sections, int32_t num_axes,
+                              int32_t cycled);
+
+/*
+ * pa_rotary_axes_and_cache -- pa_rotary_and_cache with positions on several axes, as images and
+ * video have them (time, height, width): pair i turns by positions[pair_axis[i]][t] x inv_freq[i].
+ *
+ *   positions    int32 [num_axes][num_tokens] (pa_positions_and_slots writes them so)
+ *   pair_axis    HOST, [rotary_dim / 2]: pair i's axis, below num_axes (pa_rotary_pair_axes, or
+ *                any other); read during the call
+ *   num_axes     1 .. PA_MAX_ROTARY_AXES; rotary_dim <= PA_MAX_ROTARY_AXES_DIM
+ *   the rest as pa_rotary_and_cache, its numerics too.
+ */
+pa_status pa_rotary_axes_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                   void* v_cache, const int32_t* positions, const int64_t* slot_mapping,
+                                   const float* inv_freq, const uint8_t* pair_axis, int32_t num_axes,
+                                   int32_t num_tokens, int32_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_size, int32_t rotary_dim, int32_t block_size, int32_t interleaved,
+                                   float attn_factor, int64_t q_out_stride, int64_t q_stride, int64_t key_stride,
+                                   int64_t value_stride, pa_dtype src_dtype, pa_dtype cache_dtype,
+                                   const float* k_scale, const float* v_scale, pa_stream_t stream);
+
+/*
  * pa_beam_select -- beam search's step over beams and vocabulary.
  * A candidate is (beam w, token v) of a sequence; its score is
  *   beam_scores[w] + logits[w][v] - log sum_u exp(logits[w][u]),
@@ -397,6 +433,44 @@ pa_status pa_append_blocks(int32_t* block_tables, int32_t* seq_lens, const int32
 pa_status pa_release_blocks(const int32_t* block_tables, int32_t* seq_lens, const int32_t* keep_lens,
                             int32_t* ref_counts, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_blocks,
                             int32_t block_size, pa_stream_t stream);
+
+/*
+ * pa_positions_and_slots -- positions and cache slots of a step's new tokens, from request
+ * lengths, block tables and the media in the sequences.  [ARCH] Part 1, forward pass: input
+ * preparation builds positions and slot_mapping.  For block tables that stand already
+ * (pa_append_blocks hands out blocks and writes the same slots); positions are those that the
+ * rotary calls read.
+ *
+ *   Token i of a sequence (i counts all its tokens) is text, or belongs to a medium: a grid of
+ *   frames x rows x columns tokens, row by row, frame by frame.  A medium whose first token
+ *   comes at position b has its token (f, r, c) at (b + f x step, b + r, b + c), and the token
+ *   behind it comes at the position after the largest of those: b + max((frames - 1) x step + 1,
+ *   rows, columns).  Text is one position a token, the same on every axis; a sequence starts at 0.
+ *
+ *   positions       int32 [num_axes][total_q_tokens] (written), or NULL
+ *   slot_mapping    int64 [total_q_tokens] (written), or NULL: then block_tables may be NULL, and it
+ *                   and the sizes of blocks are not used
+ *   query_start_loc int32 [num_seqs + 1], as pa_varlen_attn; a request's rows are its sequence's
+ *                   last tokens
+ *   seq_lens        int32 [num_seqs], counting the new tokens
+ *   media_start     int32 [num_seqs + 1], or NULL (text only): sequence r's media are
+ *                   media[media_start[r]] .. media[media_start[r + 1] - 1]
+ *   media           int32 [num_media][5]: first token, frames, rows, columns, step.  In ascending
+ *                   order, none over another; frames, rows and columns >= 1, step >= 0, tokens and
+ *                   positions below 2^31.  Media behind the sequence's end may stand there already.
+ *   num_axes        1 or 3 (time, height, width); media need 3
+ * Whole numbers throughout.  Where query_start_loc does not run from 0 to total_q_tokens without
+ * decreasing (PA_ERRFLAG_QUERY), every token gets slot -1 and position 0, so that the calls that
+ * follow write nothing; so do the tokens of a request that is longer than its sequence
+ * (PA_ERRFLAG_QUERY), whose sequence is longer than its table (PA_ERRFLAG_SEQ_LEN), or one of whose
+ * media is malformed (PA_ERRFLAG_MEDIA).  A table entry outside [0, num_blocks) gives its tokens slot
+ * -1 and sets PA_ERRFLAG_BLOCK_TABLE.
+ */
+pa_status pa_positions_and_slots(int32_t* positions, int64_t* slot_mapping, const int32_t* query_start_loc,
+                                 const int32_t* seq_lens, const int32_t* block_tables, const int32_t* media_start,
+                                 const int32_t* media, int32_t num_seqs, int32_t total_q_tokens, int32_t num_axes,
+                                 int32_t num_media, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                 int32_t block_size, pa_stream_t stream);
 
 /*
  * Context tokens per split-K partition that pa_decode / pa_varlen_attn use when
@@ -648,7 +722,7 @@ pa_status pa_get_error_flags(uint32_t* flags, int32_t clear, pa_stream_t stream)
  * 8 = the span of the single-token-row and multi-token-row kernels of
  * pa_varlen_attn, which run concurrently on two streams, 9 = rotary_and_cache,
  * 10 = beam_select (its kernels together), 11 = fork_blocks, 12 = append_blocks,
- * 13 = release_blocks),
+ * 13 = release_blocks, 14 = positions_and_slots; pa_rotary_axes_and_cache counts as 9),
  * returns the launch count and the summed device milliseconds since the last
  * reset (reset != 0 clears every kind).
  * Tracing is off by default and costs nothing when off.  Not thread-safe.

@@ -1,6 +1,6 @@
 """fp64 reference definitions of the operators around attention in a decoding step
-(test infrastructure): rotary positions, beam selection, and the pages of sequences
-that branch, grow and end.
+(test infrastructure): rotary positions on one axis or several, positions and slots of
+sequences with media, beam selection, and the pages of sequences that branch, grow and end.
 
 Rotary positions and beam search are textbook definitions; the pages' state (one pool,
 reference counts, copy-on-write) is [AGENTIC] "統一分頁 + 共用池" and [LINEAGE] "Prefix
@@ -54,6 +54,58 @@ def rotate(x64, positions, inv_freq, interleaved: bool = False, attn_factor: flo
     y[..., a] = first * c - second * s
     y[..., b] = second * c + first * s
     return y
+
+
+def rotate_axes(x64, positions, inv_freq, pair_axis, interleaved: bool = False,
+                attn_factor: float = 1.0) -> np.ndarray:
+    """``rotate`` with positions [axes][tokens]: pair i turns by the position on axis pair_axis[i]."""
+    y = np.array(x64, dtype=np.float64)
+    freq = np.asarray(inv_freq, dtype=np.float32).astype(np.float64)
+    for i, axis in enumerate(pair_axis):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + len(freq))
+        theta = np.asarray(positions[axis], dtype=np.float64) * freq[i]
+        c, s = (np.cos(theta) * attn_factor)[:, None], (np.sin(theta) * attn_factor)[:, None]
+        y[..., a], y[..., b] = x64[..., a] * c - x64[..., b] * s, x64[..., b] * c + x64[..., a] * s
+    return y
+
+
+# --------------------------------------------------------------------------
+# Positions and slots
+# --------------------------------------------------------------------------
+
+def sequence_positions(num_tokens: int, media) -> np.ndarray:
+    """Positions [3][num_tokens] of a sequence's tokens, one after the other; ``media`` are
+    (first token, frames, rows, columns, step), ascending."""
+    out = np.zeros((3, num_tokens), dtype=np.int64)
+    starts = {int(m[0]): [int(v) for v in m] for m in media}
+    at = place = 0
+    while at < num_tokens:
+        if at not in starts:
+            out[:, at] = place
+            at += 1
+            place += 1
+            continue
+        _, frames, rows, cols, step = starts[at]
+        highest = place
+        for f in range(frames):
+            for r in range(rows):
+                for c in range(cols):
+                    if at < num_tokens:
+                        out[:, at] = place + f * step, place + r, place + c
+                    highest = max(highest, place + f * step, place + r, place + c)
+                    at += 1
+        place = highest + 1
+    return out
+
+
+def positions_and_slots(query_start_loc, seq_lens, block_tables, block_size: int, media):
+    """(positions [3][tokens], slots [tokens]) of a step's new tokens; ``media`` holds a list for every sequence."""
+    positions, slots = [], []
+    for i, n in enumerate(seq_lens):
+        n, new = int(n), int(query_start_loc[i + 1]) - int(query_start_loc[i])
+        positions.append(sequence_positions(n, media[i])[:, n - new:])
+        slots += [int(block_tables[i][t // block_size]) * block_size + t % block_size for t in range(n - new, n)]
+    return np.concatenate(positions, 1).astype(np.int32), np.array(slots, dtype=np.int64)
 
 
 # --------------------------------------------------------------------------

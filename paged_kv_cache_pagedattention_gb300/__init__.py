@@ -39,14 +39,15 @@ PA_ERRFLAG_BLOCK_TABLE, PA_ERRFLAG_SLOT, PA_ERRFLAG_SEQ_LEN, PA_ERRFLAG_QUERY, P
     0x1, 0x2, 0x4, 0x8, 0x10
 # diagnostic only: a declared shared block differed for some member (the output is unaffected)
 PA_ERRFLAG_SHARED_MISMATCH = 0x20
-PA_ERRFLAG_PARENT, PA_ERRFLAG_POOL, PA_ERRFLAG_REF_COUNT = 0x40, 0x80, 0x100
+PA_ERRFLAG_PARENT, PA_ERRFLAG_POOL, PA_ERRFLAG_REF_COUNT, PA_ERRFLAG_MEDIA = 0x40, 0x80, 0x100, 0x200
 PA_MAX_BEAM_CANDIDATES, PA_MAX_BEAMS, PA_MAX_VOCAB = 32, 1024, 1 << 30
+PA_MAX_ROTARY_AXES, PA_MAX_ROTARY_AXES_DIM = 4, 512
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 # Names of the kernel kinds reported by pa_trace_read.
 TRACE_KINDS = ("reshape_and_cache", "attention", "merge", "varlen_plan", "prefill_tiles", "shared_prefix",
                "shared_span", "copy_blocks", "varlen_span", "rotary_and_cache", "beam_select", "fork_blocks",
-               "append_blocks", "release_blocks")
+               "append_blocks", "release_blocks", "positions_and_slots")
 
 # Every symbol include/pa.h declares, with its ctypes signature.
 _P, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -62,6 +63,12 @@ SIGNATURES = {
     "pa_rotary_and_cache": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                                            _I32, _I32, _F, _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
                                            _P, _P, _P]),
+    "pa_rotary_pair_axes": (ctypes.c_int, [_P, _I32, ctypes.POINTER(_I32), _I32, _I32]),
+    "pa_rotary_axes_and_cache": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_char_p, _I32, _I32, _I32,
+                                                _I32, _I32, _I32, _I32, _I32, _I32, _F, _I64, _I64, _I64, _I64,
+                                                ctypes.c_int, ctypes.c_int, _P, _P, _P]),
+    "pa_positions_and_slots": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                              _P]),
     "pa_beam_select_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
     "pa_beam_select": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, ctypes.c_int, _P, _SZ, _P]),
     "pa_fork_blocks": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P]),
@@ -266,11 +273,13 @@ def pa_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, 
 
 
 def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq,
-                        interleaved=False, attn_factor=1.0, k_scale=None, v_scale=None, stream=None) -> None:
+                        interleaved=False, attn_factor=1.0, k_scale=None, v_scale=None, stream=None,
+                        pair_axis=None) -> None:
     """Rotate q [T][Hq][d] into q_out (which may be q) and key [T][Hkv][d] by positions (int32
     [T]), and write key and value into the paged caches at slot_mapping (int64 [T]; a negative
     slot skips the token).  inv_freq float32 [rotary_dim/2].  q, key and value may be slices of
-    one projection (any distance between tokens).  q and q_out None: keys only."""
+    one projection (any distance between tokens).  q and q_out None: keys only.  pair_axis: see
+    pa_rotary_axes_and_cache."""
     shape, dtype, dev = key.shape, key.dtype, key.get_device()
     if len(shape) != 3 or value.shape != shape or value.dtype is not dtype:
         raise ValueError("key/value must be [num_tokens][num_kv_heads][head_size] of one dtype")
@@ -298,8 +307,16 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
         if q_elem != 1 or q_out_elem != 1 or q_head != d or q_out_head != d:
             _check_heads(q, "q")
             _check_heads(q_out, "q_out")
-    if positions.dtype is not _int32 or positions.shape != (t,) or not positions.is_contiguous():
-        _bad(positions, (t,), "positions")
+    axes = 0
+    if pair_axis is not None:
+        if positions.dim() != 2:
+            raise ValueError("positions must be int32 [num_axes][num_tokens]")
+        axes = positions.shape[0]
+        if type(pair_axis) is not bytes or len(pair_axis) != inv_freq.numel():
+            raise ValueError("pair_axis must be bytes, one for each pair of inv_freq")
+    places = (t,) if pair_axis is None else (axes, t)
+    if positions.dtype is not _int32 or positions.shape != places or not positions.is_contiguous():
+        _bad(positions, places, "positions")
     if slot_mapping.dtype is not _int64 or slot_mapping.shape != (t,) or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 tensor [num_tokens]")
     if inv_freq.dtype is not _float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -318,7 +335,17 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
         raise ValueError("pa_rotary_and_cache: all tensors must be on one CUDA device")
     if dev < 0 or dev != _current_device():
         return _on_device(dev, pa_rotary_and_cache, q_out, q, key, value, k_cache, v_cache, positions, slot_mapping,
-                          inv_freq, interleaved, attn_factor, k_scale, v_scale, stream)
+                          inv_freq, interleaved, attn_factor, k_scale, v_scale, stream, pair_axis)
+    if pair_axis is not None:
+        st = _lib.pa_rotary_axes_and_cache(
+            q_out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), pair_axis, axes, t, nb, hq, hkv, d,
+            2 * inv_freq.numel(), bs, 1 if interleaved else 0, attn_factor, q_out_stride, q_stride, k_stride, v_stride,
+            dtype_code(key), code, k_scale_ptr, v_scale_ptr,
+            _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_rotary_axes_and_cache"))
+        if st != PA_OK:
+            raise PAError(st, "pa_rotary_axes_and_cache")
+        return
     st = _lib.pa_rotary_and_cache(
         q_out_ptr, q_ptr, key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), t, nb, hq, hkv, d, 2 * inv_freq.numel(),
@@ -326,6 +353,29 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
         k_scale_ptr, v_scale_ptr, _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_rotary_and_cache"))
     if st != PA_OK:
         raise PAError(st, "pa_rotary_and_cache")
+
+
+def pa_rotary_pair_axes(sections, cycled=False) -> bytes:
+    """The axis of every pair for pa_rotary_axes_and_cache: sections[a] pairs turn on axis a,
+    the axes one after the other, or dealt round (see pa.h)."""
+    sections = [int(n) for n in sections]
+    pairs = sum(sections)
+    if not 1 <= pairs <= PA_MAX_ROTARY_AXES_DIM // 2:
+        raise ValueError("sections must sum to the rotated pairs, at most 256")
+    out = (ctypes.c_uint8 * pairs)()
+    _check(_lib.pa_rotary_pair_axes(out, 2 * pairs, (_I32 * len(sections))(*sections), len(sections),
+                                    1 if cycled else 0), "pa_rotary_pair_axes")
+    return bytes(out)
+
+
+def pa_rotary_axes_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, pair_axis,
+                             interleaved=False, attn_factor=1.0, k_scale=None, v_scale=None, stream=None) -> None:
+    """pa_rotary_and_cache with positions on several axes (int32 [num_axes][T]): pair i turns by
+    the token's position on axis pair_axis[i] (bytes [rotary_dim/2]; pa_rotary_pair_axes)."""
+    if pair_axis is None:
+        raise ValueError("pair_axis must be bytes, one for each pair of inv_freq")
+    pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, interleaved,
+                        attn_factor, k_scale, v_scale, stream, pair_axis)
 
 
 def pa_beam_select_workspace_size(num_seqs, num_beams, vocab_size, num_candidates) -> int:
@@ -457,6 +507,64 @@ def pa_release_blocks(block_tables, seq_lens, ref_counts, block_size, keep_lens=
         _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_release_blocks"))
     if st != PA_OK:
         raise PAError(st, "pa_release_blocks")
+
+
+def pa_positions_and_slots(positions, slot_mapping, query_start_loc, seq_lens, block_tables, num_blocks, block_size,
+                           media_start=None, media=None, stream=None) -> None:
+    """Positions (int32 [T], or [3][T] for time, height and width; None: not wanted) and cache slots
+    (int64 [T]; None: not wanted, and block_tables may be None) of a step's tokens: query_start_loc
+    int32 [rows+1], seq_lens int32 [rows] with the new tokens, block_tables int32 [rows][width].
+    media int32 [M][5] (first token, frames, rows, columns, step) of the sequences, media_start
+    int32 [rows+1].  See pa.h."""
+    n, dev = seq_lens.numel(), seq_lens.get_device()
+    if seq_lens.dtype is not _int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        _bad(seq_lens, (n,), "seq_lens")
+    if query_start_loc.dtype is not _int32 or query_start_loc.shape != (n + 1,) or \
+            not query_start_loc.is_contiguous() or query_start_loc.get_device() != dev:
+        _bad(query_start_loc, (n + 1,), "query_start_loc")
+    total, axes, width, records = 0, 1, 0, 0
+    positions_ptr = slots_ptr = tables_ptr = start_ptr = media_ptr = None
+    if slot_mapping is not None:
+        if slot_mapping.dtype is not _int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
+                slot_mapping.get_device() != dev:
+            raise ValueError("slot_mapping must be a contiguous int64 tensor [total_q_tokens] on seq_lens' device")
+        if block_tables is None or block_tables.dim() != 2:
+            raise ValueError("slot_mapping needs block_tables [rows][max_blocks_per_seq]")
+        total, width = slot_mapping.numel(), block_tables.shape[1]
+        if block_tables.dtype is not _int32 or block_tables.shape[0] != n or not block_tables.is_contiguous() or \
+                block_tables.get_device() != dev:
+            _bad(block_tables, (n, width), "block_tables")
+        slots_ptr, tables_ptr = slot_mapping.data_ptr(), block_tables.data_ptr()
+    if positions is not None:
+        shape = positions.shape
+        if len(shape) not in (1, 2):
+            raise ValueError("positions must be int32 [total_q_tokens] or [3][total_q_tokens]")
+        axes = shape[0] if len(shape) == 2 else 1
+        if positions.dtype is not _int32 or not positions.is_contiguous() or positions.get_device() != dev or \
+                (slot_mapping is not None and shape[-1] != total):
+            _bad(positions, shape[:-1] + (total or shape[-1],), "positions")
+        total, positions_ptr = shape[-1], positions.data_ptr()
+    elif media is not None or media_start is not None:
+        axes = 3
+    if media is not None or media_start is not None:
+        if media is None or media_start is None or media.dim() != 2:
+            raise ValueError("media [M][5] and media_start [rows+1] go together")
+        records = media.shape[0]
+        if media.dtype is not _int32 or media.shape[1] != 5 or not media.is_contiguous() or media.get_device() != dev:
+            _bad(media, (records, 5), "media")
+        if media_start.dtype is not _int32 or media_start.shape != (n + 1,) or not media_start.is_contiguous() or \
+                media_start.get_device() != dev:
+            _bad(media_start, (n + 1,), "media_start")
+        start_ptr, media_ptr = media_start.data_ptr(), media.data_ptr()
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_positions_and_slots, positions, slot_mapping, query_start_loc, seq_lens,
+                          block_tables, num_blocks, block_size, media_start, media, stream)
+    st = _lib.pa_positions_and_slots(
+        positions_ptr, slots_ptr, query_start_loc.data_ptr(), seq_lens.data_ptr(), tables_ptr, start_ptr, media_ptr,
+        n, total, axes, records, width, num_blocks, block_size,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_positions_and_slots"))
+    if st != PA_OK:
+        raise PAError(st, "pa_positions_and_slots")
 
 
 def pa_default_partition_size(num_seqs, num_kv_heads, max_seq_len, block_size) -> int:

@@ -289,7 +289,7 @@ bool cache_maps(CUtensorMap* tk, CUtensorMap* tv, const void* k_cache, const voi
 
 // ------------------------------------------------------------------ tracing
 
-constexpr int kTraceKinds = 14;
+constexpr int kTraceKinds = 15;
 bool g_trace_on = false;
 struct TraceSlot {
   int kind;
@@ -511,6 +511,83 @@ bool rows_overlap(const void* a, int64_t a_width, const void* b, int64_t b_width
   return behind < a_width || behind + b_width > stride;
 }
 
+// pa_rotary_and_cache's checks and launch; pair_axis: nullptr for positions on one axis.
+pa_status rotary_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                           void* v_cache, const int32_t* positions, const int64_t* slot_mapping,
+                           const float* inv_freq, const uint8_t* pair_axis, int32_t num_tokens, int32_t num_blocks,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t rotary_dim,
+                           int32_t block_size, int32_t interleaved, float attn_factor, int64_t q_out_stride,
+                           int64_t q_stride, int64_t key_stride, int64_t value_stride, pa_dtype src_dtype,
+                           pa_dtype cache_dtype, const float* k_scale, const float* v_scale, pa_stream_t stream) {
+  const int scale_stride = scale_stride_of(cache_dtype);
+  cache_dtype = base_dtype(cache_dtype);
+  if (num_tokens < 0 || num_blocks < 1 || num_q_heads < 0 || num_kv_heads < 1 || head_size < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_size) return PA_ERR_INVALID_ARG;
+  if (!(attn_factor > 0.f) || !(attn_factor < INFINITY)) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !positions || !slot_mapping || !inv_freq) return PA_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && (!q || !q_out)) return PA_ERR_INVALID_ARG;
+  if (src_dtype != PA_F32 && src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  const bool cache_scaled = scaled_dtype(cache_dtype);
+  if (cache_dtype != src_dtype && !cache_scaled) return PA_ERR_UNSUPPORTED;
+  if (cache_scaled && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  const long long eb = dtype_bytes(src_dtype);
+  if ((head_size * eb) % 16) return PA_ERR_UNSUPPORTED;
+  if (cache_dtype == PA_NVFP4 ? !nvfp4_shape_ok(head_size, block_size) : (head_size * dtype_bytes(cache_dtype)) % 16)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t q_width = (int64_t)num_q_heads * head_size, kv_width = (int64_t)num_kv_heads * head_size;
+  if (q_width > INT32_MAX || kv_width > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;  // a token's row by 32-bit places
+  if (num_tokens > 1 && (key_stride < kv_width || value_stride < kv_width ||
+                         (num_q_heads > 0 && (q_stride < q_width || q_out_stride < q_width))))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && q == q_out && num_tokens > 1 && q_stride != q_out_stride) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key, eb) || !aligned(value, eb) ||
+      (num_q_heads > 0 && (!aligned(q, eb) || !aligned(q_out, eb))))
+    return PA_ERR_INVALID_ARG;
+  // a token's q_out over what another one still reads (rows of other distances are the caller's)
+  auto written_over = [&](const void* src, int64_t width, int64_t stride) {
+    return (num_tokens == 1 || stride == q_out_stride) &&
+           rows_overlap(q_out, q_width * eb, src, width * eb, num_tokens, stride * eb);
+  };
+  if (num_q_heads > 0 && ((q != q_out && written_over(q, q_width, q_stride)) ||
+                          written_over(key, kv_width, key_stride) || written_over(value, kv_width, value_stride)))
+    return PA_ERR_INVALID_ARG;
+  pa::RotaryParams p;
+  p.q_out = q_out;
+  p.q = q;
+  p.key = key;
+  p.value = value;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.inv_freq = inv_freq;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err = error_word();
+  p.q_out_stride = q_out_stride;
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.scale_stride = scale_stride;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.head_size = head_size;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.attn_factor = attn_factor;
+  p.several_axes = pair_axis != nullptr;
+  memset(p.pair_axis, 0, sizeof(p.pair_axis));
+  for (int i = 0; pair_axis && i < rotary_dim / 2; ++i) p.pair_axis[i / 16] |= (uint32_t)pair_axis[i] << (2 * (i % 16));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TraceScope t(9, s);
+  return cuda_status(pa::launch_rotary(p, src_dtype, cache_dtype, s));
+}
+
 }  // namespace
 
 namespace pa {
@@ -664,70 +741,104 @@ pa_status pa_rotary_and_cache(void* q_out, const void* q, const void* key, const
                               int32_t interleaved, float attn_factor, int64_t q_out_stride, int64_t q_stride,
                               int64_t key_stride, int64_t value_stride, pa_dtype src_dtype, pa_dtype cache_dtype,
                               const float* k_scale, const float* v_scale, pa_stream_t stream) {
-  const int scale_stride = scale_stride_of(cache_dtype);
-  cache_dtype = base_dtype(cache_dtype);
-  if (num_tokens < 0 || num_blocks < 1 || num_q_heads < 0 || num_kv_heads < 1 || head_size < 1 || block_size < 1)
+  return rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, nullptr,
+                          num_tokens, num_blocks, num_q_heads, num_kv_heads, head_size, rotary_dim, block_size,
+                          interleaved, attn_factor, q_out_stride, q_stride, key_stride, value_stride, src_dtype,
+                          cache_dtype, k_scale, v_scale, stream);
+}
+
+pa_status pa_rotary_pair_axes(uint8_t* pair_axis, int32_t rotary_dim, const int32_t* sections, int32_t num_axes,
+                              int32_t cycled) {
+  if (!pair_axis || !sections || rotary_dim < 2 || rotary_dim % 2 || num_axes < 1) return PA_ERR_INVALID_ARG;
+  if (num_axes > PA_MAX_ROTARY_AXES || rotary_dim > PA_MAX_ROTARY_AXES_DIM) return PA_ERR_UNSUPPORTED;
+  const int pairs = rotary_dim / 2;
+  long long sum = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (sections[a] < 0) return PA_ERR_INVALID_ARG;
+    sum += sections[a];
+  }
+  if (sum != pairs) return PA_ERR_INVALID_ARG;
+  uint8_t axis[PA_MAX_ROTARY_AXES_DIM / 2];
+  int count[PA_MAX_ROTARY_AXES] = {};
+  for (int i = 0, a = 0, end = sections[0]; i < pairs; ++i) {
+    if (cycled) {
+      a = i < (long long)num_axes * sections[i % num_axes] ? i % num_axes : 0;
+    } else {
+      while (i >= end) end += sections[++a];
+    }
+    axis[i] = static_cast<uint8_t>(a);
+    ++count[a];
+  }
+  for (int a = 0; a < num_axes; ++a)
+    if (count[a] != sections[a]) return PA_ERR_INVALID_ARG;
+  memcpy(pair_axis, axis, pairs);
+  return PA_OK;
+}
+
+pa_status pa_rotary_axes_and_cache(void* q_out, const void* q, const void* key, const void* value, void* k_cache,
+                                   void* v_cache, const int32_t* positions, const int64_t* slot_mapping,
+                                   const float* inv_freq, const uint8_t* pair_axis, int32_t num_axes,
+                                   int32_t num_tokens, int32_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_size, int32_t rotary_dim, int32_t block_size, int32_t interleaved,
+                                   float attn_factor, int64_t q_out_stride, int64_t q_stride, int64_t key_stride,
+                                   int64_t value_stride, pa_dtype src_dtype, pa_dtype cache_dtype,
+                                   const float* k_scale, const float* v_scale, pa_stream_t stream) {
+  if (!pair_axis || num_axes < 1 || rotary_dim < 2 || rotary_dim % 2) return PA_ERR_INVALID_ARG;
+  if (num_axes > PA_MAX_ROTARY_AXES || rotary_dim > PA_MAX_ROTARY_AXES_DIM) return PA_ERR_UNSUPPORTED;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (pair_axis[i] >= num_axes) return PA_ERR_INVALID_ARG;
+  return rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, pair_axis,
+                          num_tokens, num_blocks, num_q_heads, num_kv_heads, head_size, rotary_dim, block_size,
+                          interleaved, attn_factor, q_out_stride, q_stride, key_stride, value_stride, src_dtype,
+                          cache_dtype, k_scale, v_scale, stream);
+}
+
+pa_status pa_positions_and_slots(int32_t* positions, int64_t* slot_mapping, const int32_t* query_start_loc,
+                                 const int32_t* seq_lens, const int32_t* block_tables, const int32_t* media_start,
+                                 const int32_t* media, int32_t num_seqs, int32_t total_q_tokens, int32_t num_axes,
+                                 int32_t num_media, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                 int32_t block_size, pa_stream_t stream) {
+  if (num_seqs < 0 || total_q_tokens < 0 || num_media < 0) return PA_ERR_INVALID_ARG;
+  if (num_axes != 1 && num_axes != 3) return PA_ERR_UNSUPPORTED;
+  if (num_axes == 1 && (media_start || num_media > 0)) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return total_q_tokens == 0 ? PA_OK : PA_ERR_INVALID_ARG;
+  if (total_q_tokens == 0) return PA_OK;
+  if ((!positions && !slot_mapping) || !query_start_loc || !seq_lens) return PA_ERR_INVALID_ARG;
+  if (slot_mapping && (!block_tables || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1))
     return PA_ERR_INVALID_ARG;
-  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_size) return PA_ERR_INVALID_ARG;
-  if (!(attn_factor > 0.f) || !(attn_factor < INFINITY)) return PA_ERR_INVALID_ARG;
-  if (num_tokens == 0) return PA_OK;
-  if (!key || !value || !k_cache || !v_cache || !positions || !slot_mapping || !inv_freq) return PA_ERR_INVALID_ARG;
-  if (num_q_heads > 0 && (!q || !q_out)) return PA_ERR_INVALID_ARG;
-  if (src_dtype != PA_F32 && src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-  const bool cache_scaled = scaled_dtype(cache_dtype);
-  if (cache_dtype != src_dtype && !cache_scaled) return PA_ERR_UNSUPPORTED;
-  if (cache_scaled && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
-  const long long eb = dtype_bytes(src_dtype);
-  if ((head_size * eb) % 16) return PA_ERR_UNSUPPORTED;
-  if (cache_dtype == PA_NVFP4 ? !nvfp4_shape_ok(head_size, block_size) : (head_size * dtype_bytes(cache_dtype)) % 16)
-    return PA_ERR_UNSUPPORTED;
-  const int64_t q_width = (int64_t)num_q_heads * head_size, kv_width = (int64_t)num_kv_heads * head_size;
-  if (q_width > INT32_MAX || kv_width > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;  // a token's row by 32-bit places
-  if (num_tokens > 1 && (key_stride < kv_width || value_stride < kv_width ||
-                         (num_q_heads > 0 && (q_stride < q_width || q_out_stride < q_width))))
-    return PA_ERR_INVALID_ARG;
-  if (num_q_heads > 0 && q == q_out && num_tokens > 1 && q_stride != q_out_stride) return PA_ERR_INVALID_ARG;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(key, eb) || !aligned(value, eb) ||
-      (num_q_heads > 0 && (!aligned(q, eb) || !aligned(q_out, eb))))
-    return PA_ERR_INVALID_ARG;
-  // a token's q_out over what another one still reads (rows of other distances are the caller's)
-  auto written_over = [&](const void* src, int64_t width, int64_t stride) {
-    return (num_tokens == 1 || stride == q_out_stride) &&
-           rows_overlap(q_out, q_width * eb, src, width * eb, num_tokens, stride * eb);
-  };
-  if (num_q_heads > 0 && ((q != q_out && written_over(q, q_width, q_stride)) ||
-                          written_over(key, kv_width, key_stride) || written_over(value, kv_width, value_stride)))
-    return PA_ERR_INVALID_ARG;
-  pa::RotaryParams p;
-  p.q_out = q_out;
-  p.q = q;
-  p.key = key;
-  p.value = value;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
+  if (num_media > 0 && (!media_start || !media)) return PA_ERR_INVALID_ARG;
+  if (num_seqs > kMostPages || total_q_tokens > kMostPages) return PA_ERR_UNSUPPORTED;
+  // a token's results over what another one still reads
+  const size_t n = num_seqs, starts = (n + 1) * sizeof(int32_t);
+  const struct { const void* at; size_t size; } out[2] = {
+      {positions, positions ? (size_t)num_axes * total_q_tokens * sizeof(int32_t) : 0},
+      {slot_mapping, slot_mapping ? (size_t)total_q_tokens * sizeof(int64_t) : 0}};
+  for (const auto& o : out)
+    if (overlap(o.at, o.size, query_start_loc, starts) || overlap(o.at, o.size, seq_lens, n * sizeof(int32_t)) ||
+        overlap(o.at, o.size, block_tables, slot_mapping ? n * max_blocks_per_seq * sizeof(int32_t) : 0) ||
+        overlap(o.at, o.size, media_start, media_start ? starts : 0) ||
+        overlap(o.at, o.size, media, (size_t)num_media * 5 * sizeof(int32_t)))
+      return PA_ERR_INVALID_ARG;
+  if (overlap(out[0].at, out[0].size, out[1].at, out[1].size)) return PA_ERR_INVALID_ARG;
+  pa::PositionsParams p;
   p.positions = positions;
   p.slot_mapping = slot_mapping;
-  p.inv_freq = inv_freq;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
+  p.query_start_loc = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.media_start = media_start;
+  p.media = media;
   p.err = error_word();
-  p.q_out_stride = q_out_stride;
-  p.q_stride = q_stride;
-  p.key_stride = key_stride;
-  p.value_stride = value_stride;
-  p.scale_stride = scale_stride;
-  p.num_tokens = num_tokens;
-  p.num_q_heads = num_q_heads;
-  p.num_kv_heads = num_kv_heads;
-  p.head_size = head_size;
-  p.rotary_dim = rotary_dim;
-  p.interleaved = interleaved ? 1 : 0;
+  p.num_seqs = num_seqs;
+  p.total_tokens = total_q_tokens;
+  p.num_axes = num_axes;
+  p.num_media = num_media;
   p.num_blocks = num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
   p.block_size = block_size;
-  p.attn_factor = attn_factor;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  TraceScope t(9, s);
-  return cuda_status(pa::launch_rotary(p, src_dtype, cache_dtype, s));
+  TraceScope t(14, s);
+  return cuda_status(pa::launch_positions(p, s));
 }
 
 size_t pa_beam_select_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab_size,

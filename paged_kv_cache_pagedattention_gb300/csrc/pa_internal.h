@@ -95,6 +95,8 @@ struct CopyParams {
 
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 
+constexpr int kMaxRotaryPairs = PA_MAX_ROTARY_AXES_DIM / 2;  // of a rotation on several axes
+
 // Rotary positions with the cache write.  Strides are in elements, between tokens.
 struct RotaryParams {
   void* q_out;
@@ -103,7 +105,7 @@ struct RotaryParams {
   const void* value;
   void* k_cache;
   void* v_cache;
-  const int32_t* positions;
+  const int32_t* positions;  // [num_tokens], or on several axes [axes][num_tokens]
   const int64_t* slot_mapping;
   const float* inv_freq;  // [rotary_dim / 2]
   const float* k_scale;   // FP8 / NVFP4: scale of KV head h at k_scale[h * scale_stride]
@@ -120,9 +122,32 @@ struct RotaryParams {
   int num_blocks;
   int block_size;
   float attn_factor;
+  int several_axes;
+  uint32_t pair_axis[kMaxRotaryPairs / 16];  // several axes: two bits a pair, pair i in word i / 16
 };
 
 cudaError_t launch_rotary(const RotaryParams& p, int src_dtype, int cache_dtype, cudaStream_t stream);
+
+// Positions and slots of a step's tokens.
+struct PositionsParams {
+  int32_t* positions;              // [num_axes][total_tokens], or nullptr
+  int64_t* slot_mapping;           // [total_tokens], or nullptr
+  const int32_t* query_start_loc;  // [num_seqs + 1]
+  const int32_t* seq_lens;         // [num_seqs]
+  const int32_t* block_tables;     // [num_seqs][max_blocks_per_seq]; nullptr without slots
+  const int32_t* media_start;      // [num_seqs + 1], or nullptr: text only
+  const int32_t* media;            // [num_media][5]
+  unsigned* err;
+  int num_seqs;
+  int total_tokens;
+  int num_axes;
+  int num_media;
+  int num_blocks;
+  int max_blocks_per_seq;
+  int block_size;
+};
+
+cudaError_t launch_positions(const PositionsParams& p, cudaStream_t stream);
 
 struct BeamParams {
   const void* logits;        // [num_seqs * num_beams][vocab_size], rows row_stride elements apart

@@ -3,6 +3,7 @@
 //
 //   angle of pair i at position p: p * f_i, f_i = inv_freq[i]; c, s = attn_factor * (cos, sin)
 //   (x, y) -> (x c - y s, y c + x s), pairs (i, i + R/2) or (2i, 2i + 1), i < R/2
+//   on several axes p is the token's position on pair i's axis
 //
 // The angle is kept as a fraction of a turn in 64-bit fixed point: f_i / 2 pi is rounded
 // once (fp64, 53 bits), and p times it modulo 2^64 drops whole turns exactly, so far
@@ -43,9 +44,26 @@ __device__ __forceinline__ float2 rotation(int pos, unsigned long long turn, flo
   return make_float2(c * m, s * m);
 }
 
+// Where a token stands: its position, or on several axes the token itself.
+template <bool kAxes>
+struct Place {
+  long long t;
+  int pos;
+  __device__ __forceinline__ Place(const RotaryParams& p, long long token) : t(token), pos(0) {
+    if constexpr (!kAxes) pos = p.positions[t];
+  }
+  // its position for pair i
+  __device__ __forceinline__ int of(const RotaryParams& p, int i) const {
+    if constexpr (!kAxes) return pos;
+    const unsigned axis = p.pair_axis[i >> 4] >> (2 * (i & 15)) & 3u;
+    return p.positions[(long long)axis * p.num_tokens + t];
+  }
+};
+
 // Element j of a row after rotation, its partner read from the row.
-template <int SRC>
-__device__ __forceinline__ float rotated_at(const RotaryParams& p, const typename Elem<SRC>::T* row, int j, int pos) {
+template <int SRC, bool kAxes>
+__device__ __forceinline__ float rotated_at(const RotaryParams& p, const typename Elem<SRC>::T* row, int j,
+                                            const Place<kAxes>& at) {
   const float x = Elem<SRC>::load(row + j);
   if (j >= p.rotary_dim) return x;
   const int half = p.rotary_dim / 2;
@@ -60,7 +78,7 @@ __device__ __forceinline__ float rotated_at(const RotaryParams& p, const typenam
     i = first ? j : j - half;
     partner = first ? j + half : j - half;
   }
-  const float2 cs = rotation(pos, turn_fraction(p.inv_freq[i]), p.attn_factor);
+  const float2 cs = rotation(at.of(p, i), turn_fraction(p.inv_freq[i]), p.attn_factor);
   const float y = Elem<SRC>::load(row + partner);
   return first ? x * cs.x - y * cs.y : x * cs.x + y * cs.y;
 }
@@ -69,7 +87,7 @@ __device__ __forceinline__ float rotated_at(const RotaryParams& p, const typenam
 // eight elements behind the rotated ones) of a q row, or one group of a k or v row that
 // makes 16 bytes of cache (8 bytes of code and a block scale in NVFP4).  q is handled by
 // whole pairs, so it may be rotated in place.
-template <int SRC, int CDT>
+template <int SRC, int CDT, bool kAxes>
 __global__ void __launch_bounds__(256) rotary_generic_kernel(const RotaryParams p) {
   using SE = Elem<SRC>;
   using T = typename SE::T;
@@ -95,7 +113,7 @@ __global__ void __launch_bounds__(256) rotary_generic_kernel(const RotaryParams 
       flag_error(p.err, PA_ERRFLAG_SLOT);
       continue;
     }
-    const int pos = p.positions[t];
+    const Place<kAxes> at(p, t);
     if (rem < q_units) {
       const int h = static_cast<int>(rem / q_row), c = static_cast<int>(rem % q_row);
       const T* src = static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * d;
@@ -103,7 +121,7 @@ __global__ void __launch_bounds__(256) rotary_generic_kernel(const RotaryParams 
       if (c < pair_units) {
         for (int i = 4 * c; i < min(half, 4 * c + 4); ++i) {
           const int a = p.interleaved ? 2 * i : i, b = p.interleaved ? 2 * i + 1 : i + half;
-          const float2 cs = rotation(pos, turn_fraction(p.inv_freq[i]), p.attn_factor);
+          const float2 cs = rotation(at.of(p, i), turn_fraction(p.inv_freq[i]), p.attn_factor);
           const float x = SE::load(src + a), y = SE::load(src + b);
           dst[a] = SE::from_float(x * cs.x - y * cs.y);
           dst[b] = SE::from_float(y * cs.x + x * cs.y);
@@ -128,11 +146,11 @@ __global__ void __launch_bounds__(256) rotary_generic_kernel(const RotaryParams 
       T* dst = static_cast<T*>(cache) + (tile * p.block_size + off) * d + j0;
 #pragma unroll
       for (int i = 0; i < kGroup; ++i)
-        dst[i] = is_v || j0 + i >= p.rotary_dim ? src[j0 + i] : SE::from_float(rotated_at<SRC>(p, src, j0 + i, pos));
+        dst[i] = is_v || j0 + i >= p.rotary_dim ? src[j0 + i] : SE::from_float(rotated_at<SRC, kAxes>(p, src, j0 + i, at));
     } else {
       float x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = is_v ? SE::load(src + j0 + i) : rotated_at<SRC>(p, src, j0 + i, pos);
+      for (int i = 0; i < 16; ++i) x[i] = is_v ? SE::load(src + j0 + i) : rotated_at<SRC, kAxes>(p, src, j0 + i, at);
       const float scale = (is_v ? p.v_scale : p.k_scale)[h * p.scale_stride];
       if constexpr (CDT == PA_NVFP4) {
         uint2 codes;
@@ -254,7 +272,7 @@ __device__ __forceinline__ float2 rotation_of(const float2* table, int pieces, i
 // 512, 19.7 and 3.4, and the long case 91.  Onto an NVFP4 cache the groups of 16 go to a few
 // warps of a block, which the others await (2,176 tokens 28 us, 8,192 of 64/8 heads 103, whose
 // bytes take 7 and 46; 43% of the issue slots, the barrier the largest stall).
-template <int SRC, int CDT, bool kInterleaved>
+template <int SRC, int CDT, bool kInterleaved, bool kAxes>
 __global__ void __launch_bounds__(256, CDT == PA_NVFP4 ? 4 : 8) rotary_piece_kernel(const RotaryParams p) {
   using T = typename Elem<SRC>::T;
   constexpr int kQ = Piece<SRC>::n, kKv = kv_unit<SRC, CDT>();
@@ -299,9 +317,10 @@ __global__ void __launch_bounds__(256, CDT == PA_NVFP4 ? 4 : 8) rotary_piece_ker
   load_plain(plain_first);
 
   const long long slot = p.slot_mapping[t];
-  const int pos = p.positions[t];
+  const Place<kAxes> at(p, t);
   for (int i = threadIdx.x; i < half; i += 256)
-    table[i % kPairs * pieces + i / kPairs] = rotation(pos, turn_fraction(p.inv_freq[i]), p.attn_factor);
+    table[i % kPairs * pieces + i / kPairs] =
+        rotation(at.of(p, i), turn_fraction(p.inv_freq[i]), p.attn_factor);
   if (slot < 0 || slot >= (long long)p.num_blocks * p.block_size) {
     if (slot >= 0 && threadIdx.x == 0) flag_error(p.err, PA_ERRFLAG_SLOT);
     return;
@@ -378,7 +397,7 @@ bool aligned16(const void* ptr, long long stride, int num_tokens, int bytes) {
   return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (num_tokens == 1 || stride * bytes % 16 == 0);
 }
 
-template <int SRC, int CDT>
+template <int SRC, int CDT, bool kAxes>
 cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
   constexpr int kBytes = Elem<SRC>::bytes, kKv = kv_unit<SRC, CDT>();
   const int half = p.rotary_dim / 2;
@@ -394,33 +413,40 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
                       half * sizeof(float2) <= 48 * 1024;
   if (pieces) {
     const size_t smem = half * sizeof(float2);
-    return launch_early(p.interleaved ? rotary_piece_kernel<SRC, CDT, true> : rotary_piece_kernel<SRC, CDT, false>,
+    return launch_early(p.interleaved ? rotary_piece_kernel<SRC, CDT, true, kAxes>
+                                      : rotary_piece_kernel<SRC, CDT, false, kAxes>,
                         dim3(p.num_tokens), 256, smem, 1, p, stream);
   }
   const long long per_token = (long long)p.num_q_heads * ((half + 3) / 4 + (p.head_size - p.rotary_dim + 7) / 8) +
                               2ll * (p.head_size / (SRC == CDT ? kKv : 16)) * p.num_kv_heads;
   const long long blocks = (per_token * p.num_tokens + 255) / 256;
-  return launch_early(rotary_generic_kernel<SRC, CDT>, dim3(static_cast<unsigned>(blocks < 152 * 64 ? blocks : 152 * 64)),
+  return launch_early(rotary_generic_kernel<SRC, CDT, kAxes>, dim3(static_cast<unsigned>(blocks < 152 * 64 ? blocks : 152 * 64)),
                       256, 0, 1, p, stream);
 }
 
-template <int SRC>
+template <int SRC, bool kAxes>
 cudaError_t launch_source(const RotaryParams& p, int cache_dtype, cudaStream_t stream) {
   switch (cache_dtype) {
-    case PA_FP8_E4M3: return launch<SRC, PA_FP8_E4M3>(p, stream);
-    case PA_FP8_E5M2: return launch<SRC, PA_FP8_E5M2>(p, stream);
-    case PA_NVFP4: return launch<SRC, PA_NVFP4>(p, stream);
-    default: return launch<SRC, SRC>(p, stream);
+    case PA_FP8_E4M3: return launch<SRC, PA_FP8_E4M3, kAxes>(p, stream);
+    case PA_FP8_E5M2: return launch<SRC, PA_FP8_E5M2, kAxes>(p, stream);
+    case PA_NVFP4: return launch<SRC, PA_NVFP4, kAxes>(p, stream);
+    default: return launch<SRC, SRC, kAxes>(p, stream);
   }
+}
+
+template <int SRC>
+cudaError_t launch_axes(const RotaryParams& p, int cache_dtype, cudaStream_t stream) {
+  return p.several_axes ? launch_source<SRC, true>(p, cache_dtype, stream)
+                        : launch_source<SRC, false>(p, cache_dtype, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryParams& p, int src_dtype, int cache_dtype, cudaStream_t stream) {
   switch (src_dtype) {
-    case PA_F32: return launch_source<PA_F32>(p, cache_dtype, stream);
-    case PA_F16: return launch_source<PA_F16>(p, cache_dtype, stream);
-    case PA_BF16: return launch_source<PA_BF16>(p, cache_dtype, stream);
+    case PA_F32: return launch_axes<PA_F32>(p, cache_dtype, stream);
+    case PA_F16: return launch_axes<PA_F16>(p, cache_dtype, stream);
+    case PA_BF16: return launch_axes<PA_BF16>(p, cache_dtype, stream);
     default: return cudaErrorInvalidValue;
   }
 }
