@@ -21,6 +21,8 @@
  *                            counts and slots of sequences that branch, grow and end;
  *   7. pa_positions_and_slots, pa_rotary_axes_and_cache   positions of text and media on
  *                            several axes, with slots, and 4. on those axes.
+ * And beside 2. and 3.:
+ *   8. pa_diff_decode, pa_diff_varlen_attn   differential attention on the same caches.
  *
  * Sources, cited by key:
  *   [AGENTIC] "宣稱省下 106 倍成本：vLLM 怎麼把 Serving 系統校準給 Agentic Workload"
@@ -703,6 +705,61 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
                                   pa_stream_t stream);
 
 /*
+ * Differential attention on the paged cache: each head is the difference of two softmax maps
+ * over one value row, which takes away what both maps attend to.
+ *
+ *   out[r][h] = A_1 - lambda[r][h] A_2,  A_j = softmax(scale q[r][2h + j] K_j^T) V
+ *
+ * Heads are counted in the caches' own way, so that every call that writes a cache serves these
+ * too: num_q_heads and num_kv_heads count the query rows and the cached rows, both even.  Query
+ * head 2h + j is map j of head h < num_q_heads / 2; KV group g = h / (num_q_heads / num_kv_heads)
+ * has map j's keys in KV head 2g + j, and its value rows of 2 x head_size elements in KV heads 2g
+ * (the first half) and 2g + 1.
+ *
+ *   out            [rows][num_q_heads / 2][2 x head_size], q_dtype (written); rows are num_seqs, or
+ *                  total_q_tokens
+ *   q              [rows][num_q_heads][head_size], q_dtype
+ *   lambda         float; row r, head h at lambda[r * lambda_row_stride + h * lambda_head_stride]
+ *                  (strides >= 0; 0 where rows or heads share one)
+ *   norm_weight    float [2 x head_size], or NULL.  Where it is given, each head of the difference
+ *                  becomes o / sqrt(mean(o^2) + norm_eps) x norm_weight (a model's constant factor
+ *                  belongs into the weight); norm_eps > 0
+ *   window         sliding window, as pa_decode_windowed and pa_varlen_attn_windowed (0: none)
+ *   the rest, partitions, masks and errors as pa_decode and pa_varlen_attn.  out and q are 16-byte
+ *   aligned; out must not overlap what is read (PA_ERR_INVALID_ARG).
+ * Maps, difference and norm are fp32, rounded once (the tensor-core kernels round the maps' weights
+ * to 16 bits for their product with V, as pa_decode does).  A map that attends nothing (all of a
+ * row's entries out of range) is 0.  bf16 and f16 with head_size 64 or 128, and FP8 caches with
+ * head_size 128, run on the tensor cores where block_size is 16, 32 or 64; the rest in fp32.
+ */
+size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_size, int32_t max_seq_len, int32_t block_size,
+                                     int32_t partition_size);
+pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_size, int32_t block_size, float scale, const float* lambda,
+                         int64_t lambda_row_stride, int64_t lambda_head_stride, const float* norm_weight,
+                         float norm_eps, int32_t window, pa_dtype q_dtype, pa_dtype kv_dtype, const float* k_scale,
+                         const float* v_scale, int32_t partition_size, void* workspace, size_t workspace_bytes,
+                         pa_stream_t stream);
+
+/* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together. */
+size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                                     int32_t max_seq_len, int32_t block_size, int32_t partition_size);
+pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              int32_t num_blocks, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_seqs,
+                              int32_t total_q_tokens, int32_t max_query_len, int32_t max_seq_len,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                              float scale, const float* lambda, int64_t lambda_row_stride,
+                              int64_t lambda_head_stride, const float* norm_weight, float norm_eps, int32_t window,
+                              int32_t causal, pa_dtype q_dtype, pa_dtype kv_dtype, const float* k_scale,
+                              const float* v_scale, int32_t partition_size, void* workspace,
+                              size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Read the device error word of the current device (host pointer `flags`),
  * after synchronising `stream`.  clear != 0 resets it to zero.  Returns
  * PA_ERR_BOUNDS if any error bit other than TIMEOUT is set, PA_ERR_TIMEOUT if
@@ -722,7 +779,8 @@ pa_status pa_get_error_flags(uint32_t* flags, int32_t clear, pa_stream_t stream)
  * 8 = the span of the single-token-row and multi-token-row kernels of
  * pa_varlen_attn, which run concurrently on two streams, 9 = rotary_and_cache,
  * 10 = beam_select (its kernels together), 11 = fork_blocks, 12 = append_blocks,
- * 13 = release_blocks, 14 = positions_and_slots; pa_rotary_axes_and_cache counts as 9),
+ * 13 = release_blocks, 14 = positions_and_slots, 15 = diff_attention (single-token rows, and every row of the
+ * generic kernel), 16 = diff_merge, 17 = diff_prefill_tiles; pa_rotary_axes_and_cache counts as 9),
  * returns the launch count and the summed device milliseconds since the last
  * reset (reset != 0 clears every kind).
  * Tracing is off by default and costs nothing when off.  Not thread-safe.

@@ -25,7 +25,7 @@ Sources cited by key in the docstrings of this package:
 
 Parity status: every public function here is pinned by a ``-m "not gpu"`` test
 in ``tests/test_oracle_pins.py`` (``decoding_step.py``: ``tests/test_decoding_oracle.py``,
-positions and several axes ``tests/test_axes_host.py``) against values the pages print, closed forms,
+positions and several axes ``tests/test_axes_host.py``; ``differential.py``: ``tests/test_diff_host.py``) against values the pages print, closed forms,
 invariants, an independent library routine or brute force.  No function is
 "parity unpinned".
 """
@@ -77,4 +77,9 @@ from .decoding_step import (  # noqa: F401
     rotate,
     rotate_axes,
     sequence_positions,
+)
+from .differential import (  # noqa: F401
+    diff_map,
+    diff_norm,
+    diff_varlen,
 )

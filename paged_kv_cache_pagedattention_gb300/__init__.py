@@ -47,7 +47,8 @@ ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 # Names of the kernel kinds reported by pa_trace_read.
 TRACE_KINDS = ("reshape_and_cache", "attention", "merge", "varlen_plan", "prefill_tiles", "shared_prefix",
                "shared_span", "copy_blocks", "varlen_span", "rotary_and_cache", "beam_select", "fork_blocks",
-               "append_blocks", "release_blocks", "positions_and_slots")
+               "append_blocks", "release_blocks", "positions_and_slots", "diff_attention", "diff_merge",
+               "diff_prefill_tiles")
 
 # Every symbol include/pa.h declares, with its ctypes signature.
 _P, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -94,6 +95,13 @@ SIGNATURES = {
     "pa_varlen_attn_windowed": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
                                                _I32, _I32, _I32, _I32, _F, _I32, _I32, ctypes.c_int, ctypes.c_int,
                                                _P, _P, _I32, _P, _SZ, _P]),
+    "pa_diff_decode_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "pa_diff_decode": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _F, _P,
+                                      _I64, _I64, _P, _F, _I32, ctypes.c_int, ctypes.c_int, _P, _P, _I32, _P, _SZ, _P]),
+    "pa_diff_varlen_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "pa_diff_varlen_attn": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                           _I32, _I32, _F, _P, _I64, _I64, _P, _F, _I32, _I32, ctypes.c_int,
+                                           ctypes.c_int, _P, _P, _I32, _P, _SZ, _P]),
     "pa_get_error_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32, _P]),
     "pa_trace_enable": (ctypes.c_int, [_I32]),
     "pa_trace_read": (ctypes.c_int, [_I32, ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_double), _I32]),
@@ -673,6 +681,117 @@ def pa_varlen_attn(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_
                                _ptr(v_scale), int(partition_size), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream)),
            "pa_varlen_attn")
+
+
+def pa_diff_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size,
+                                  partition_size=0) -> int:
+    return _lib.pa_diff_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len,
+                                              block_size, partition_size)
+
+
+def pa_diff_varlen_workspace_size(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads, head_size,
+                                  max_seq_len, block_size, partition_size=0) -> int:
+    return _lib.pa_diff_varlen_workspace_size(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads,
+                                              head_size, max_seq_len, block_size, partition_size)
+
+
+def _diff_args(where, out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight, k_scale,
+               v_scale):
+    """Checks of a differential call's tensors; (rows, num_q_heads, geometry, lambda's strides, device)."""
+    if q.dim() != 3:
+        raise ValueError(f"{where}: q must be [rows][num_q_heads][head_size]")
+    t, hq, d = q.shape
+    nb, hkv, bs, head = cache_geometry(k_cache, v_cache, d)
+    if head != d or hq % 2 or hkv % 2 or out.shape != (t, hq // 2, 2 * d) or out.dtype is not q.dtype:
+        raise ValueError(f"{where}: q must be [rows][num_q_heads][head_size] and out [rows][num_q_heads/2]"
+                         "[2*head_size] of one dtype, with even numbers of heads and the caches' head size")
+    b, dev = seq_lens.numel(), q.get_device()
+    if seq_lens.dtype is not _int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        _bad(seq_lens, (b,), "seq_lens")
+    if block_tables.dtype is not _int32 or block_tables.dim() != 2 or block_tables.shape[0] != b or \
+            not block_tables.is_contiguous():
+        raise ValueError(f"{where}: block_tables must be a contiguous int32 tensor [num_seqs][max_blocks_per_seq]")
+    if lambda_.dtype is not _float32 or lambda_.dim() > 2:
+        raise ValueError(f"{where}: lambda must be float32: a number, [heads] or [rows][heads]")
+    shape, strides = (1, 1) + lambda_.shape, (0, 0) + lambda_.stride()
+    if shape[-1] not in (1, hq // 2) or shape[-2] not in (1, t):
+        raise ValueError(f"{where}: lambda must be a number, [heads] or [rows][heads]")
+    row_stride = strides[-2] if shape[-2] > 1 else 0
+    head_stride = strides[-1] if shape[-1] > 1 else 0
+    others = [out, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace]
+    if norm_weight is not None:
+        if norm_weight.dtype is not _float32 or norm_weight.shape != (2 * d,) or not norm_weight.is_contiguous():
+            raise ValueError(f"{where}: norm_weight must be a contiguous float32 tensor [2*head_size]")
+        others.append(norm_weight)
+    for scale in (k_scale, v_scale):
+        if scale is not None:
+            if scale.dtype is not _float32 or scale.numel() not in (1, hkv) or not scale.is_contiguous():
+                raise ValueError(f"{where}: scales: float32, one per tensor or one per KV head")
+            others.append(scale)
+    if k_scale is not None and (v_scale is None or v_scale.numel() != k_scale.numel()):
+        raise ValueError(f"{where}: scales: float32, both one per tensor or both one per KV head")
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and
+            workspace.is_contiguous()):
+        raise ValueError(f"{where}: q, out, the caches and the workspace must be contiguous")
+    for x in others:
+        if x.get_device() != dev:
+            raise ValueError(f"{where}: all tensors must be on one CUDA device")
+    return t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def pa_diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, scale, lambda_, workspace,
+                   norm_weight=None, norm_eps=1e-5, k_scale=None, v_scale=None, partition_size=0, stream=None,
+                   window=0) -> None:
+    """Differential attention, one query a sequence: out [B][Hq/2][2d] = softmax(q[2h] K_1) V -
+    lambda softmax(q[2h+1] K_2) V of q [B][Hq][d] on caches whose KV heads 2g, 2g+1 hold group g's
+    two keys and its value's halves.  lambda_ float32: a number, [Hq/2] or [B][Hq/2] (any strides);
+    norm_weight float32 [2d]: root-mean-square norm of every head.  See pa.h."""
+    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev = _diff_args(
+        "pa_diff_decode", out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight, k_scale,
+        v_scale)
+    if t != b:
+        raise ValueError("pa_diff_decode: one row of q a sequence")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_diff_decode, out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, scale,
+                          lambda_, workspace, norm_weight, norm_eps, k_scale, v_scale, partition_size, stream, window)
+    st = _lib.pa_diff_decode(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), b, max_seq_len, hq, hkv, d, bs, scale, lambda_.data_ptr(),
+        row_stride, head_stride, _opt(norm_weight), norm_eps, window, dtype_code(q), kv_code(k_cache, k_scale),
+        _opt(k_scale), _opt(v_scale), partition_size, workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_diff_decode"))
+    if st != PA_OK:
+        raise PAError(st, "pa_diff_decode")
+
+
+def pa_diff_varlen_attn(out, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens, max_query_len, max_seq_len,
+                        scale, lambda_, workspace, norm_weight=None, norm_eps=1e-5, causal=True, k_scale=None,
+                        v_scale=None, partition_size=0, stream=None, window=0) -> None:
+    """Differential attention of a flattened varlen batch (pa_diff_decode's heads, lambda and norm;
+    q [T][Hq][d], query_start_loc int32 [B+1]).  See pa.h."""
+    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev = _diff_args(
+        "pa_diff_varlen_attn", out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight,
+        k_scale, v_scale)
+    if query_start_loc.dtype is not _int32 or query_start_loc.shape != (b + 1,) or \
+            not query_start_loc.is_contiguous() or query_start_loc.get_device() != dev:
+        _bad(query_start_loc, (b + 1,), "query_start_loc")
+    if dev < 0 or dev != _current_device():
+        return _on_device(dev, pa_diff_varlen_attn, out, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens,
+                          max_query_len, max_seq_len, scale, lambda_, workspace, norm_weight, norm_eps, causal,
+                          k_scale, v_scale, partition_size, stream, window)
+    st = _lib.pa_diff_varlen_attn(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(),
+        block_tables.shape[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), b, t, max_query_len, max_seq_len, hq,
+        hkv, d, bs, scale, lambda_.data_ptr(), row_stride, head_stride, _opt(norm_weight), norm_eps, window,
+        1 if causal else 0, dtype_code(q), kv_code(k_cache, k_scale), _opt(k_scale), _opt(v_scale), partition_size,
+        workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_diff_varlen_attn"))
+    if st != PA_OK:
+        raise PAError(st, "pa_diff_varlen_attn")
 
 
 def pa_get_error_flags(clear: bool = True, stream=None) -> int:

@@ -168,14 +168,13 @@ struct VarlenLayout {
 };
 
 VarlenLayout varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
-                           int requested) {
+                           int requested, int tile_tokens) {
   VarlenLayout L;
   L.part = resolve_partition(requested, num_seqs, hkv, max_seq_len, bs);
   L.part_pf = requested > 0 ? L.part : prefill_partition(L.part);
   L.parts = ceil_div(max_seq_len, L.part);
   L.parts_pf = ceil_div(max_seq_len, L.part_pf);
-  const int group = hq / (hkv > 0 ? hkv : 1);
-  L.max_work = (ceil_div(total_q, pa::prefill_tile_tokens(group)) + num_seqs) * L.parts_pf;
+  L.max_work = (ceil_div(total_q, tile_tokens) + num_seqs) * L.parts_pf;
   const size_t rows = (size_t)num_seqs * (size_t)L.parts + (size_t)total_q * (size_t)L.parts_pf;
   L.off_off = 256;
   L.work_off = L.off_off + align256((size_t)num_seqs * sizeof(int32_t));
@@ -289,7 +288,7 @@ bool cache_maps(CUtensorMap* tk, CUtensorMap* tv, const void* k_cache, const voi
 
 // ------------------------------------------------------------------ tracing
 
-constexpr int kTraceKinds = 15;
+constexpr int kTraceKinds = 18;
 bool g_trace_on = false;
 struct TraceSlot {
   int kind;
@@ -509,6 +508,46 @@ bool rows_overlap(const void* a, int64_t a_width, const void* b, int64_t b_width
   const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
   const int64_t behind = (apart % stride + stride) % stride;  // b's row behind the start of a's
   return behind < a_width || behind + b_width > stride;
+}
+
+// What the differential calls check beyond check_attention_args; `rows` of q and out.
+pa_status check_diff_args(const void* out, const void* q, const void* k_cache, const void* v_cache,
+                          int32_t num_blocks, int32_t rows, int32_t num_q_heads, int32_t num_kv_heads,
+                          int32_t head_size, int32_t block_size, float scale, const float* lambda,
+                          int64_t lambda_row_stride, int64_t lambda_head_stride, const float* norm_weight,
+                          float norm_eps, pa_dtype q_dtype, pa_dtype kv_dtype) {
+  if (!(scale > 0.f) || !(scale < INFINITY)) return PA_ERR_INVALID_ARG;
+  if (num_q_heads % 2 || num_kv_heads % 2) return PA_ERR_INVALID_ARG;
+  if (!lambda || lambda_row_stride < 0 || lambda_head_stride < 0) return PA_ERR_INVALID_ARG;
+  if (norm_weight && (!(norm_eps > 0.f) || !(norm_eps < INFINITY))) return PA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(lambda, 4) || !aligned(norm_weight, 4)) return PA_ERR_INVALID_ARG;
+  const int64_t most = INT64_MAX / 8;
+  if (lambda_row_stride > most / rows || lambda_head_stride > most / num_q_heads) return PA_ERR_UNSUPPORTED;
+  // a row's output over what another one still reads
+  const size_t row_bytes = (size_t)rows * num_q_heads * head_size * dtype_bytes(q_dtype);
+  const size_t cache = (size_t)num_blocks * num_kv_heads * tile_bytes(kv_dtype, block_size, head_size);
+  const size_t lambdas = ((rows - 1) * lambda_row_stride + (num_q_heads / 2 - 1) * lambda_head_stride + 1) * 4;
+  if (overlap(out, row_bytes, q, row_bytes) || overlap(out, row_bytes, k_cache, cache) ||
+      overlap(out, row_bytes, v_cache, cache) || overlap(out, row_bytes, lambda, lambdas) ||
+      overlap(out, row_bytes, norm_weight, norm_weight ? (size_t)2 * head_size * 4 : 0))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+pa::DiffParams diff_params(const AttnParams& a, const float* lambda, int64_t lambda_row_stride,
+                           int64_t lambda_head_stride, const float* norm_weight, float norm_eps, int scale_stride,
+                           int window) {
+  pa::DiffParams p;
+  p.a = a;
+  p.a.scale_stride = scale_stride;
+  p.a.window = window;
+  p.lambda = lambda;
+  p.lambda_row_stride = lambda_row_stride;
+  p.lambda_head_stride = lambda_head_stride;
+  p.norm_weight = norm_weight;
+  p.norm_eps = norm_eps;
+  p.multi_partials = 0;
+  return p;
 }
 
 // pa_rotary_and_cache's checks and launch; pair_axis: nullptr for positions on one axis.
@@ -1138,7 +1177,7 @@ size_t pa_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_
       max_seq_len < 1 || block_size < 1)
     return 256;
   return varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size,
-                       partition_size)
+                       partition_size, pa::prefill_tile_tokens(num_q_heads / num_kv_heads))
       .total;
 }
 
@@ -1174,8 +1213,9 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
                                       q_dtype, kv_dtype, k_scale, v_scale, partition_size, workspace);
   if (st != PA_OK) return st;
   if (!(scale > 0.f) || !(scale < INFINITY)) return PA_ERR_INVALID_ARG;
+  const int tile_tokens = pa::prefill_tile_tokens(num_q_heads / num_kv_heads);
   const VarlenLayout L = varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size,
-                                       max_seq_len, block_size, partition_size);
+                                       max_seq_len, block_size, partition_size, tile_tokens);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
   AttnParams p = base_params(out, q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq, seq_lens,
                              num_seqs, max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale,
@@ -1211,7 +1251,7 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
   cudaError_t e;
   {
     TraceScope t(3, s);
-    e = pa::launch_varlen_plan(p, part_off, work, work_count, static_cast<int>(L.max_work), s);
+    e = pa::launch_varlen_plan(p, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
   const bool fast_decode = pa::decode_mma_supported(q_dtype, kv_dtype, head_size, block_size, p.group);
@@ -1281,6 +1321,157 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
   if (L.parts > 1 || L.parts_pf > 1) {
     TraceScope t(2, s);
     e = pa::launch_merge(p, q_dtype, s);
+  }
+  return cuda_status(e);
+}
+
+size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_size, int32_t max_seq_len, int32_t block_size,
+                                     int32_t partition_size) {
+  if (num_seqs < 1 || num_q_heads < 1 || head_size < 1 || max_seq_len < 1 || block_size < 1) return 256;
+  return decode_layout(num_seqs, num_q_heads, 2 * head_size, max_seq_len, block_size, num_kv_heads / 2, partition_size)
+      .total;
+}
+
+pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_size, int32_t block_size, float scale, const float* lambda,
+                         int64_t lambda_row_stride, int64_t lambda_head_stride, const float* norm_weight,
+                         float norm_eps, int32_t window, pa_dtype q_dtype, pa_dtype kv_dtype, const float* k_scale,
+                         const float* v_scale, int32_t partition_size, void* workspace, size_t workspace_bytes,
+                         pa_stream_t stream) {
+  const int scale_stride = scale_stride_of(kv_dtype);
+  kv_dtype = base_dtype(kv_dtype);
+  if (num_seqs < 0 || window < 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  pa_status st = check_attention_args(out, q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq,
+                                      seq_lens, max_seq_len, num_q_heads, num_kv_heads, head_size, block_size,
+                                      q_dtype, kv_dtype, k_scale, v_scale, partition_size, workspace);
+  if (st == PA_OK)
+    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, num_seqs, num_q_heads, num_kv_heads, head_size,
+                         block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
+                         q_dtype, kv_dtype);
+  if (st != PA_OK) return st;
+  const DecodeLayout L = decode_layout(num_seqs, num_q_heads, 2 * head_size, max_seq_len, block_size,
+                                       num_kv_heads / 2, partition_size);
+  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (overlap(out, (size_t)num_seqs * num_q_heads * head_size * dtype_bytes(q_dtype), workspace, L.total))
+    return PA_ERR_INVALID_ARG;
+  pa::DiffParams p = diff_params(
+      base_params(out, q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                  max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale, k_scale, v_scale),
+      lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps, scale_stride, window);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.a.num_rows = num_seqs;
+  p.a.max_query_len = 1;
+  p.a.part = p.a.part_pf = p.a.part_shared = L.part;
+  p.a.max_partitions = static_cast<int>(L.parts);
+  p.a.ws_ml = reinterpret_cast<float2*>(ws + L.ml_off);
+  p.a.ws_acc = reinterpret_cast<float*>(ws + L.acc_off);
+  const int grid_z = window_partitions(L.parts, window, 1, block_size, L.part);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  {
+    TraceScope t(15, s);
+    e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_z, -1, s);
+  }
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  if (L.parts > 1) {
+    TraceScope t(16, s);
+    e = pa::launch_diff_merge(p, q_dtype, s);
+  }
+  return cuda_status(e);
+}
+
+size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                                     int32_t max_seq_len, int32_t block_size, int32_t partition_size) {
+  (void)max_query_len;
+  if (num_seqs < 1 || total_q_tokens < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_size < 1 ||
+      max_seq_len < 1 || block_size < 1)
+    return 256;
+  return varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size, max_seq_len,
+                       block_size, partition_size, 1)
+      .total;
+}
+
+pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              int32_t num_blocks, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_seqs,
+                              int32_t total_q_tokens, int32_t max_query_len, int32_t max_seq_len,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                              float scale, const float* lambda, int64_t lambda_row_stride,
+                              int64_t lambda_head_stride, const float* norm_weight, float norm_eps, int32_t window,
+                              int32_t causal, pa_dtype q_dtype, pa_dtype kv_dtype, const float* k_scale,
+                              const float* v_scale, int32_t partition_size, void* workspace,
+                              size_t workspace_bytes, pa_stream_t stream) {
+  const int scale_stride = scale_stride_of(kv_dtype);
+  kv_dtype = base_dtype(kv_dtype);
+  if (num_seqs < 0 || total_q_tokens < 0 || window < 0) return PA_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_q_tokens == 0) return PA_OK;
+  if (!query_start_loc || max_query_len < 1) return PA_ERR_INVALID_ARG;
+  pa_status st = check_attention_args(out, q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq,
+                                      seq_lens, max_seq_len, num_q_heads, num_kv_heads, head_size, block_size,
+                                      q_dtype, kv_dtype, k_scale, v_scale, partition_size, workspace);
+  if (st == PA_OK)
+    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, total_q_tokens, num_q_heads, num_kv_heads, head_size,
+                         block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
+                         q_dtype, kv_dtype);
+  if (st != PA_OK) return st;
+  const int tile_tokens = 1;
+  const VarlenLayout L = varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size,
+                                       max_seq_len, block_size, partition_size, tile_tokens);
+  if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (overlap(out, (size_t)total_q_tokens * num_q_heads * head_size * dtype_bytes(q_dtype), workspace, L.total))
+    return PA_ERR_INVALID_ARG;
+  pa::DiffParams p = diff_params(
+      base_params(out, q, k_cache, v_cache, num_blocks, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                  max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale, k_scale, v_scale),
+      lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps, scale_stride, window);
+  // prefill tiles are claimed by index over (work item, KV head group)
+  if (L.max_work * p.a.num_kv_heads * p.a.num_head_groups > (1LL << 30)) return PA_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttnParams& a = p.a;
+  a.query_start_loc = query_start_loc;
+  a.num_rows = total_q_tokens;
+  a.max_query_len = max_query_len;
+  a.part = L.part;
+  a.part_pf = L.part_pf;
+  a.part_shared = L.part;
+  a.max_partitions = static_cast<int>(L.parts);
+  a.causal = causal ? 1 : 0;
+  const int grid_dec = window_partitions(L.parts, window, 1, block_size, L.part);
+  const int grid_all = window_partitions(L.parts, window, max_query_len, block_size, L.part);
+  const int grid_pf = window_partitions(L.parts_pf, window, max_query_len, block_size, L.part_pf);
+  int32_t* work_count = reinterpret_cast<int32_t*>(ws);
+  a.plan_ok = reinterpret_cast<int32_t*>(ws + 4);
+  a.work_claim = reinterpret_cast<int32_t*>(ws + 8);
+  a.work_full = reinterpret_cast<int32_t*>(ws + 12);
+  int32_t* part_off = reinterpret_cast<int32_t*>(ws + L.off_off);
+  int4* work = reinterpret_cast<int4*>(ws + L.work_off);
+  a.part_off = part_off;
+  a.work = work;
+  a.work_count = work_count;
+  a.ws_ml = reinterpret_cast<float2*>(ws + L.ml_off);
+  a.ws_acc = reinterpret_cast<float*>(ws + L.acc_off);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  {
+    TraceScope t(3, s);
+    e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
+  }
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  (void)grid_dec;
+  {
+    TraceScope t(15, s);
+    e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
+  }
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  if (L.parts > 1 || L.parts_pf > 1) {
+    TraceScope t(16, s);
+    e = pa::launch_diff_merge(p, q_dtype, s);
   }
   return cuda_status(e);
 }

@@ -10,6 +10,7 @@
 // Sources: [AGENTIC] "Online softmax 到底在幹嘛" (weighted sum / weight sum per part,
 // local maxima brought to the global maximum before adding); [LINEAGE]
 // "PagedAttention" (K/V read through the block table).
+#include "kv_rows.cuh"
 #include "pa_common.cuh"
 
 namespace pa {
@@ -18,40 +19,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGenericMaxPerLane = 8;  // head_size <= 256
-
-// A token row of a cache tile (= physical block x Hkv + KV head): the address of its
-// first element (NVFP4: of its code row) and, for NVFP4, of its block-scale row.
-struct KvRow {
-  const uint8_t* row;
-  const uint8_t* scales;
-};
-
-template <int KVDT>
-__device__ __forceinline__ KvRow kv_row(const void* cache, long long tile, int bs, int d, int off) {
-  const uint8_t* base = static_cast<const uint8_t*>(cache);
-  if constexpr (is_nvfp4<KVDT>()) {
-    const uint8_t* t = base + tile * nvfp4_tile_bytes(bs, d);
-    return {t + off * (d / 2), t + bs * (d / 2) + off * (d / 16)};
-  } else {
-    return {base + ((tile * bs + off) * d) * Elem<KVDT>::bytes, nullptr};
-  }
-}
-
-// Stored value (without the fp32 scale) of element dd of a token row.
-template <int KVDT>
-__device__ __forceinline__ float kv_elem(const KvRow& r, int dd) {
-  if constexpr (is_nvfp4<KVDT>()) {
-    const uint32_t byte = r.row[dd >> 1];
-    const __half2_raw c = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-    __half_raw v;
-    v.x = (dd & 1) ? c.y : c.x;
-    const __half_raw b = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(r.scales[dd >> 4]), __NV_E4M3);
-    return __half2float(__half(v)) * __half2float(__half(b));
-  } else {
-    using KE = Elem<KVDT>;
-    return KE::load(reinterpret_cast<const typename KE::T*>(r.row) + dd);
-  }
-}
 
 template <int QDT, int KVDT>
 __global__ void __launch_bounds__(128, 1)
@@ -198,18 +165,6 @@ __global__ void __launch_bounds__(128, 1)
 // partial states with an online combine; then each lane owns four output
 // dimensions and streams the partials with 16-byte loads, eight in flight.
 constexpr int kMergeThreads = 128;
-
-__device__ __forceinline__ void combine_ml(float& m, float& l, float m2, float l2) {
-  if (l2 <= 0.f) return;
-  if (l <= 0.f) {
-    m = m2;
-    l = l2;
-    return;
-  }
-  const float nm = fmaxf(m, m2);
-  l = l * exp2f(m - nm) + l2 * exp2f(m2 - nm);
-  m = nm;
-}
 
 template <int QDT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const AttnParams p) {
@@ -640,10 +595,9 @@ cudaError_t launch_merge(const AttnParams& p, int q_dtype, cudaStream_t stream) 
 }
 
 cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work,
-                               int32_t* work_count, int max_work, cudaStream_t stream) {
+                               int32_t* work_count, int max_work, int tile_tokens, cudaStream_t stream) {
   varlen_plan_kernel<<<1, 1024, 0, stream>>>(p, part_off, work, work_count,
-                                             const_cast<int32_t*>(p.plan_ok), max_work,
-                                             prefill_tile_tokens(p.group));
+                                             const_cast<int32_t*>(p.plan_ok), max_work, tile_tokens);
   return cudaGetLastError();
 }
 

@@ -212,7 +212,7 @@ cudaError_t launch_attn_generic(const AttnParams& p, int q_dtype, int kv_dtype, 
                                 int only_multi_token, cudaStream_t stream);
 cudaError_t launch_merge(const AttnParams& p, int q_dtype, cudaStream_t stream);
 cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work,
-                               int32_t* work_count, int max_work, cudaStream_t stream);
+                               int32_t* work_count, int max_work, int tile_tokens, cudaStream_t stream);
 
 bool decode_mma_supported(int q_dtype, int kv_dtype, int head_size, int block_size, int group);
 cudaError_t launch_decode_mma(const AttnParams& p, int q_dtype, int kv_dtype, int grid_z,
@@ -226,6 +226,23 @@ cudaError_t launch_shared_prefix(const AttnParams& p, int q_dtype, int kv_dtype,
 cudaError_t launch_shared_prefix_tiles(const AttnParams& p, int q_dtype, int grid_z,
                                        const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
                                        cudaStream_t stream);
+
+// Differential attention.  Query head 2h + j is map j of head h, KV head 2g + j holds map j's keys
+// of KV group g, and KV heads 2g, 2g + 1 hold the halves of the group's value row.  In `a` the heads
+// are counted so (num_q_heads and num_kv_heads even); its partial states are those of the maps,
+// [partial rows][num_q_heads] with rows of 2 head_size, and out is [rows][num_q_heads / 2][2 head_size].
+struct DiffParams {
+  AttnParams a;
+  const float* lambda;  // of row r, head h: lambda[r * lambda_row_stride + h * lambda_head_stride]
+  long long lambda_row_stride, lambda_head_stride;
+  const float* norm_weight;  // [2 head_size], or nullptr: no norm
+  float norm_eps;
+  int multi_partials;  // rows of multi-token requests leave partial states whatever their number
+};
+
+cudaError_t launch_diff_generic(const DiffParams& p, int q_dtype, int kv_dtype, int grid_z, int only_multi_token,
+                                cudaStream_t stream);
+cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, cudaStream_t stream);
 
 // tcgen05 prefill tiles (TMEM accumulators); tmap_k has one-piece boxes, tmap_v
 // whole (block, head) tiles.  A persistent grid of at most max_ctas CTAs (one per SM)
