@@ -254,9 +254,10 @@ EncodeTiledFn encode_fn() {
 // a whole (block, head) tile, {128 bytes, block_size, pieces, 1}; in shared memory
 // it lands piece-major ([piece][token][128 bytes]) with the 128-byte swizzle.
 // With `one_piece` the box is a single piece, {128 bytes, block_size, 1, 1}, so
-// the copies of consecutive blocks can be placed side by side per piece.
+// the copies of consecutive blocks can be placed side by side per piece.  `rows` tokens a box
+// (0: a whole block's).
 bool encode_cache_map(CUtensorMap* m, const void* base, int kv_dtype, int num_blocks, int hkv, int bs, int d,
-                      bool one_piece = false) {
+                      bool one_piece = false, int rows = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const int eb = dtype_bytes(kv_dtype);
@@ -265,7 +266,7 @@ bool encode_cache_map(CUtensorMap* m, const void* base, int kv_dtype, int num_bl
   const int pieces = row_bytes / 128;
   cuuint64_t dims[4] = {(cuuint64_t)(128 / eb), (cuuint64_t)hkv * bs, (cuuint64_t)pieces, (cuuint64_t)num_blocks};
   cuuint64_t strides[3] = {(cuuint64_t)row_bytes, 128, (cuuint64_t)hkv * bs * row_bytes};
-  cuuint32_t box[4] = {(cuuint32_t)(128 / eb), (cuuint32_t)bs, one_piece ? 1u : (cuuint32_t)pieces, 1};
+  cuuint32_t box[4] = {(cuuint32_t)(128 / eb), (cuuint32_t)(rows > 0 ? rows : bs), one_piece ? 1u : (cuuint32_t)pieces, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUtensorMapDataType t = eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
   return fn(m, t, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -532,6 +533,12 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
       overlap(out, row_bytes, norm_weight, norm_weight ? (size_t)2 * head_size * 4 : 0))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
+}
+
+bool diff_decode_maps(CUtensorMap* tk, CUtensorMap* tv, const AttnParams& a, int kv_dtype) {
+  const int rows = pa::diff_decode_unit(kv_dtype, a.head_size, a.block_size);
+  return encode_cache_map(tk, a.k_cache, kv_dtype, a.num_blocks, a.num_kv_heads, a.block_size, a.head_size, false, rows) &&
+         encode_cache_map(tv, a.v_cache, kv_dtype, a.num_blocks, a.num_kv_heads, a.block_size, a.head_size, false, rows);
 }
 
 pa::DiffParams diff_params(const AttnParams& a, const float* lambda, int64_t lambda_row_stride,
@@ -1372,7 +1379,12 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
   const int grid_z = window_partitions(L.parts, window, 1, block_size, L.part);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  {
+  if (pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size)) {
+    CUtensorMap tk, tv;
+    if (!diff_decode_maps(&tk, &tv, p.a, kv_dtype)) return PA_ERR_CUDA;
+    TraceScope t(15, s);
+    e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_z, &tk, &tv, s);
+  } else {
     TraceScope t(15, s);
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_z, -1, s);
   }
@@ -1463,8 +1475,17 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  (void)grid_dec;
-  {
+  if (pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size)) {
+    CUtensorMap tk, tv;
+    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
+    if (max_query_len > 1) {
+      TraceScope t(15, s);
+      e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_pf, 1, s);
+      if (e != cudaSuccess) return PA_ERR_CUDA;
+    }
+    TraceScope t(15, s);
+    e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s);
+  } else {
     TraceScope t(15, s);
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
   }

@@ -244,6 +244,12 @@ cudaError_t launch_diff_generic(const DiffParams& p, int q_dtype, int kv_dtype, 
                                 cudaStream_t stream);
 cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, cudaStream_t stream);
 
+// Single-token rows on tensor cores; the maps' boxes are diff_decode_unit tokens of one head.
+bool diff_decode_supported(int q_dtype, int kv_dtype, int head_size, int block_size);
+int diff_decode_unit(int kv_dtype, int head_size, int block_size);
+cudaError_t launch_diff_decode(const DiffParams& p, int q_dtype, int kv_dtype, int grid_z, const CUtensorMap* tmap_k,
+                               const CUtensorMap* tmap_v, cudaStream_t stream);
+
 // tcgen05 prefill tiles (TMEM accumulators); tmap_k has one-piece boxes, tmap_v
 // whole (block, head) tiles.  A persistent grid of at most max_ctas CTAs (one per SM)
 // claims (work item, KV head group) tiles through p.work_claim; several launches may
