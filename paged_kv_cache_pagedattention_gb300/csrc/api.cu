@@ -1404,7 +1404,7 @@ size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, i
       max_seq_len < 1 || block_size < 1)
     return 256;
   return varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size, max_seq_len,
-                       block_size, partition_size, 1)
+                       block_size, partition_size, pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size))
       .total;
 }
 
@@ -1432,7 +1432,7 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
                          block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
-  const int tile_tokens = 1;
+  const int tile_tokens = pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size);
   const VarlenLayout L = varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size,
                                        max_seq_len, block_size, partition_size, tile_tokens);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
@@ -1475,22 +1475,33 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  if (pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size)) {
-    CUtensorMap tk, tv;
-    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
-    if (max_query_len > 1) {
-      TraceScope t(15, s);
-      e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_pf, 1, s);
-      if (e != cudaSuccess) return PA_ERR_CUDA;
-    }
-    TraceScope t(15, s);
-    e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s);
-  } else {
+  const bool multi = max_query_len > 1;
+  const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
+  const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
+  p.multi_partials = fast_prefill;
+  if (!fast_decode) {
     TraceScope t(15, s);
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  } else {
+    CUtensorMap tk, tv;
+    if (fast_prefill) {
+      if (!encode_cache_map(&tk, k_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, true) ||
+          !encode_cache_map(&tv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size))
+        return PA_ERR_CUDA;
+      TraceScope t(17, s);
+      e = pa::launch_diff_prefill(p, q_dtype, kv_dtype, static_cast<int>(L.max_work), sm_count(), &tk, &tv, s);
+    } else if (multi) {
+      TraceScope t(15, s);
+      e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_pf, 1, s);
+    }
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
+    TraceScope t(15, s);
+    e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
   }
-  if (e != cudaSuccess) return PA_ERR_CUDA;
-  if (L.parts > 1 || L.parts_pf > 1) {
+  if (L.parts > 1 || L.parts_pf > 1 || p.multi_partials) {
     TraceScope t(16, s);
     e = pa::launch_diff_merge(p, q_dtype, s);
   }
