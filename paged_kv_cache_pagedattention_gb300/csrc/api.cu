@@ -553,7 +553,6 @@ pa::DiffParams diff_params(const AttnParams& a, const float* lambda, int64_t lam
   p.lambda_head_stride = lambda_head_stride;
   p.norm_weight = norm_weight;
   p.norm_eps = norm_eps;
-  p.multi_partials = 0;
   return p;
 }
 
@@ -1478,7 +1477,6 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
   const bool multi = max_query_len > 1;
   const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
   const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
-  p.multi_partials = fast_prefill;
   if (!fast_decode) {
     TraceScope t(15, s);
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
@@ -1501,7 +1499,7 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
-  if (L.parts > 1 || L.parts_pf > 1 || p.multi_partials) {
+  if (L.parts > 1 || L.parts_pf > 1) {
     TraceScope t(16, s);
     e = pa::launch_diff_merge(p, q_dtype, s);
   }

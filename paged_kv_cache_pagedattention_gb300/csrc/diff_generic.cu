@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(128) diff_generic_kernel(const DiffParams p, i
       }
     }
   }
-  if (ri.parts_row == 1 && !(p.multi_partials && ri.q_len > 1)) {
+  if (ri.parts_row == 1) {
     const float w0 = diff_weight(l[0]), w1 = diff_weight(l[1]) * diff_lambda(p, row, head);
 #pragma unroll
     for (int k = 0; k < kDiffPairs; ++k) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
   const RowInfo ri = row_info(a, row);
   if (!ri.ok) return;
   const int np = ri.parts_row;
-  if (np <= 1 && !(p.multi_partials && ri.q_len > 1)) return;  // written by the attention kernel
+  if (np <= 1) return;  // written by the attention kernel
   const long long base = row_partial_base(a, ri, row);
   const int hq = a.num_q_heads;
   const float2* ml = a.ws_ml + base * hq + 2 * head;

@@ -1,19 +1,29 @@
 // Differential attention of multi-token rows on the 5th-generation tensor cores.
 //
-// A persistent grid, one CTA per SM; a CTA works on one map of a tile: a work item of the varlen
-// plan (request, first query row, partition of the keys) for one (KV group, group of <= 8 heads).
-// A tile's rows are (token, head) pairs, token-major (row = token * GP + head, GP = the head group
-// padded to a power of two), 128 to a row tile; row r lives in TMEM lane r.  The value row is twice
-// as wide as a key, so a map's accumulators take 2 head_size columns: one row tile with head_size
-// 128, two with 64.  Keys stream in chunks of 64 tokens (whole paged blocks).  Per chunk i:
-//   S(i)  = Q_j K_j(i)^T    M = 128 rows, N = 64 keys, K = head_size         -> TMEM (2 buffers)
+// A persistent grid, one CTA per SM; a CTA claims tiles: a work item of the varlen plan (request,
+// first query row, partition of the keys) for one (KV group, group of <= 8 heads).  A tile's rows
+// are (token, head) pairs, token-major (row = token * GP + head, GP = the head group padded to a
+// power of two), 128 to a row tile; row r lives in TMEM lane r.  The value row is twice as wide as
+// a key, so a map's accumulators take 2 head_size columns: one row tile with head_size 128, two
+// with 64.  Keys stream in chunks of 64 tokens (whole paged blocks), first under map 1, then under
+// map 2, as one run of chunks.  Per chunk i, map j:
+//   S(i)  = Q_j K_j(i)^T    M = 128 rows, N = 64 keys, K = head_size         -> TMEM
 //   P(i)  = softmax numerators of S(i), 16-bit, over S(i)                    -> TMEM
 //   O    += P(i) [V_1 V_2](i)   M = 128, N = 2 head_size, K = 64 keys        -> TMEM
-// Warps: four for the softmax of a row tile (a row a thread), two TMA producers (K; V), one issuer
-// of MMAs a row tile, and for FP8 caches six that widen codes to f16.
+// At the end of map 1 its rows A_1 = O / l go to their place in the workspace (fp32); at the end of
+// map 2 the same threads take A_1 - lambda A_2, its norm, and write the result.  Rows whose keys lie
+// in several partitions leave both maps' partial states instead.
+// Warps: eight for the softmax, two TMA producers (K; V), one issuer of MMAs a row tile; for FP8
+// caches one producer and six that widen codes to f16.
+//
+// What bounds it is the softmax: a warp needs some 1,600 cycles from S(i) to P(i) by itself, the
+// products of a chunk 768.  With one row tile, two warps of each scheduler therefore take its
+// chunks in turn (four S buffers), and hand the running maximum of a row from one to the other
+// through shared memory; with two row tiles each has its own four warps (two S buffers each).
 #include <algorithm>
 
 #include "diff.cuh"
+#include "launch.cuh"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -21,41 +31,48 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRows = 128;   // rows of a row tile = TMEM lanes
-constexpr int kChunk = 64;   // keys of a chunk
-constexpr int kSBufs = 2;    // S / P buffers of a row tile, 64 TMEM columns each
-constexpr int kOCol = kSBufs * 64;
-constexpr int kConvThreads = 192;
+constexpr int kRows = 128;      // rows of a row tile = TMEM lanes
+constexpr int kChunk = 64;      // keys of a chunk
+constexpr int kSoftWarps = 8;   // two warpgroups of softmax warps
 constexpr int kValidRing = 16;
 
 template <int HEAD, int BS, bool F8>
 struct DiffTc {
   static constexpr int kTiles = HEAD == 128 ? 1 : 2;
-  static constexpr int kTileCols = HEAD == 128 ? 512 : 256;  // kOCol + 2 HEAD used
+  static constexpr bool kTurns = kTiles == 1;                // the two warpgroups take chunks in turn
+  static constexpr int kSBufs = kTurns ? 4 : 2;              // S / P buffers of a row tile, 64 TMEM columns each
+  static constexpr int kOCol = kSBufs * 64;
   static constexpr int kWide = 2 * HEAD;
+  static constexpr int kTileCols = kOCol + kWide;
+  static constexpr int kCols = kTurns ? kWide / 2 : kWide;   // columns of O a thread finishes
   static constexpr int kPieces = HEAD / 64;                  // 128-byte pieces of a 16-bit key
   static constexpr int kBlocks = kChunk / BS;
   static constexpr int kPiece = kChunk * 128;
   static constexpr int kKBytes = kPieces * kPiece;           // keys of a chunk
   static constexpr int kVBytes = 2 * kKBytes;                // values of a chunk
-  static constexpr int kStageBytes = kKBytes + kVBytes;
-  static constexpr int kStages = F8 ? 3 : HEAD == 128 ? 4 : 7;
+  static constexpr int kKStages = F8 ? 2 : HEAD == 128 ? 3 : 6;
+  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 3 : 6;
   static constexpr int kQPiece = kRows * 128;
-  static constexpr int kQTile = kPieces * kQPiece;
-  // FP8: codes land in a staging ring, [K | V_1 | V_2][block][token][head_size bytes]
+  static constexpr int kQTile = kPieces * kQPiece;           // of one map
+  static constexpr int kKOff = kTiles * 2 * kQTile;
+  static constexpr int kVOff = kKOff + kKStages * kKBytes;
+  // FP8: codes land in staging rings, K [block][token][head_size bytes], V [half][block][token][..]
   static constexpr int kStg = F8 ? 2 : 0;
   static constexpr int kStgBlock = BS * HEAD;
   static constexpr int kStgTensor = kBlocks * kStgBlock;
-  static constexpr int kStgOff = kTiles * kQTile + kStages * kStageBytes;
-  static constexpr int kBarOff = kStgOff + kStg * 3 * kStgTensor;
-  static constexpr int kNumBars = 2 * kStages + 3 * kSBufs * kTiles + 1 + 2 * kStg;
+  static constexpr int kStgKOff = kVOff + kVStages * kVBytes;
+  static constexpr int kStgVOff = kStgKOff + kStg * kStgTensor;
+  static constexpr int kBarOff = kStgVOff + kStg * 2 * kStgTensor;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 2 + kSoftWarps + 1 + 4 * kStg;
   static constexpr int kSmem = 1024 + kBarOff + 8 * kNumBars + 16;
-  static constexpr int kProducer = 4 * kTiles, kMma = kProducer + 2, kConv = kMma + kTiles;
-  static constexpr int kThreads = (kConv + (F8 ? kConvThreads / 32 : 0)) * 32;
+  static constexpr int kProducers = F8 ? 1 : 2;              // FP8: 16 warps leave 128 registers a thread
+  static constexpr int kProducer = kSoftWarps, kMma = kProducer + kProducers, kConvK = kMma + kTiles, kConvV = kConvK + 2;
+  static constexpr int kThreads = (F8 ? kConvV + 4 : kConvK) * 32;
   static_assert(kBlocks * BS == kChunk, "block size must divide the chunk");
-  static_assert(kOCol + kWide <= kTileCols && kTiles * kTileCols <= 512, "TMEM columns");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kTiles * kTileCols == 512, "TMEM columns");
+  static_assert(kSmem + 5 * 1024 <= 227 * 1024, "shared memory, with the static arrays");
   static_assert(!F8 || HEAD == 128, "FP8 rows are one 128-byte piece");
+  static_assert(kSBufs + kKStages + kStg < kValidRing, "a chunk's word outlives its stages");
 };
 
 // Byte offset, inside a chunk's V, of key `key`'s row in piece `pc` (the pieces of both halves).
@@ -63,6 +80,36 @@ template <int HEAD, int BS>
 __device__ __forceinline__ uint32_t v_row_off(int key, int pc) {
   return (uint32_t)((key / BS) * (HEAD / 32) * BS * 128 + pc * BS * 128 + (key % BS) * 128);
 }
+
+// A row of 128 codes widened to f16: two pieces of 128 bytes, piece_stride apart.
+template <int KVDT>
+__device__ __forceinline__ void widen_row(const uint8_t* srow, uint8_t* drow, int piece_stride, int sw) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint4 codes = *reinterpret_cast<const uint4*>(srow + ((q ^ sw) << 4));
+    const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) fp8x4_to_f16x2x2<KVDT>(cw[e], h[2 * e], h[2 * e + 1]);
+    uint8_t* row = drow + (q >> 2) * piece_stride;
+    const int cc = (2 * q) & 7;
+    *reinterpret_cast<uint4*>(row + ((cc ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(row + (((cc + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+// 32 elements of an output row, 16-byte aligned.
+template <int QDT>
+__device__ __forceinline__ void store_row(typename Elem<QDT>::T* out, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(out + 8 * q) =
+        make_uint4(pack2<QDT>(v[8 * q], v[8 * q + 1]), pack2<QDT>(v[8 * q + 2], v[8 * q + 3]),
+                   pack2<QDT>(v[8 * q + 4], v[8 * q + 5]), pack2<QDT>(v[8 * q + 6], v[8 * q + 7]));
+}
+
+// All 256 softmax threads.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct DiffPrefillArgs {
   DiffParams p;
@@ -76,80 +123,101 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   constexpr int ODT = kCvt ? PA_F16 : QDT;
   using G = DiffTc<HEAD, BS, kCvt>;
   using QE = Elem<QDT>;
-  constexpr int ST = G::kStages, NB = G::kBlocks, NT = G::kTiles;
+  constexpr int KST = G::kKStages, VST = G::kVStages, SG = G::kStg;
+  constexpr int NB = G::kBlocks, NT = G::kTiles, SB = G::kSBufs;
+  constexpr bool kTurns = G::kTurns;
   const AttnParams& p = args.p.a;
-
-  if (plan_rejected(p)) return;
-  const int nwork = *p.work_count;
-  const int nfull = *p.work_full;
-  const int num_groups = (p.group + 7) / 8;
-  const int ny = p.num_kv_heads * num_groups;  // (KV group, head group, map)
-  const int total = nwork * ny;
-  const int total_full = nfull * ny;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sKV = sQ + NT * G::kQTile;
-  uint8_t* sStg = smem + G::kStgOff;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kBarOff);
-  uint64_t* empty = full + ST;
-  // Row tile t, buffer b (chunk i: b = i % 2, phase i / 2): S(i) is in TMEM, P(i) is, PV(i) is done
-  uint64_t* s_full = empty + ST;
-  uint64_t* p_full = s_full + NT * kSBufs;
-  uint64_t* o_done = p_full + NT * kSBufs;
-  uint64_t* mma_fin = o_done + NT * kSBufs;
-  uint64_t* stg_full = mma_fin + 1;
-  uint64_t* stg_empty = stg_full + G::kStg;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stg_empty + G::kStg);
+  uint8_t* sQ = smem;                       // [row tile][map][piece][row][128 bytes]
+  uint8_t* sK = smem + G::kKOff;            // [stage][piece][key][128 bytes]
+  uint8_t* sV = smem + G::kVOff;            // [stage][block][piece of both halves][token][128 bytes]
+  uint8_t* sStgK = smem + G::kStgKOff;
+  uint8_t* sStgV = smem + G::kStgVOff;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + G::kBarOff);
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  // Row tile t, buffer b: S(i) is in TMEM (and its chunk's s_valid known), P(i) is, PV(i) is done
+  uint64_t* s_full = v_empty + VST;
+  uint64_t* p_full = s_full + NT * SB;
+  uint64_t* o_done = p_full + NT * SB;
+  uint64_t* o_free = o_done + NT * SB;      // a map's O has been read
+  uint64_t* v_zeroed = o_free + NT;         // map j's last values have their end zeroed (two row tiles)
+  uint64_t* m_post = v_zeroed + 2;          // softmax warp w has posted its rows' maxima
+  uint64_t* mma_fin = m_post + kSoftWarps;
+  uint64_t* stgk_full = mma_fin + 1;
+  uint64_t* stgk_empty = stgk_full + SG;
+  uint64_t* stgv_full = stgk_empty + SG;
+  uint64_t* stgv_empty = stgv_full + SG;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stgv_empty + SG);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ int s_next, s_abort;
-  // bit b: block b of a chunk can be read; chunks are at most ST + kStg apart
-  __shared__ int s_valid[kValidRing];
-  static_assert(ST + G::kStg < kValidRing, "a chunk's word outlives its stage");
-  constexpr int RS = kCvt ? G::kStg : ST;  // the copies' ring
-  uint64_t* rfull = kCvt ? stg_full : full;
-  uint64_t* rempty = kCvt ? stg_empty : empty;
+  __shared__ int s_valid[kValidRing];       // bit b: block b of the chunk can be read
+  __shared__ int s_fail[2];                 // a softmax warp gave up in map j
+  __shared__ float s_m[2][kRows], s_l[2][2][kRows], s_sq[2][kRows];
+  __shared__ int8_t s_shift[2][NT * kRows];  // FP8 caches: map j's row times 2^shift fits f16
 
   if (tid == 0) {
     tma_prefetch_desc(&args.tk);
     tma_prefetch_desc(&args.tv);
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(full + i, kCvt ? kConvThreads : 2);
-      mbar_init(empty + i, NT);
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(k_full + i, kCvt ? 64 : 1);
+      mbar_init(k_empty + i, NT);
     }
-    for (int i = 0; i < G::kStg; ++i) {
-      mbar_init(stg_full + i, 2);
-      mbar_init(stg_empty + i, kConvThreads);
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(v_full + i, kCvt ? 128 : 1);
+      mbar_init(v_empty + i, NT);
     }
-    for (int i = 0; i < NT * kSBufs; ++i) {
-      mbar_init(s_full + i, 1);
+    for (int i = 0; i < SG; ++i) {
+      mbar_init(stgk_full + i, 1);
+      mbar_init(stgk_empty + i, 64);
+      mbar_init(stgv_full + i, 1);
+      mbar_init(stgv_empty + i, 128);
+    }
+    for (int i = 0; i < NT * SB; ++i) {
+      mbar_init(s_full + i, 2);
       mbar_init(p_full + i, kRows);
       mbar_init(o_done + i, 1);
     }
+    for (int i = 0; i < NT; ++i) mbar_init(o_free + i, kTurns ? 2 * kRows : kRows);
+    mbar_init(v_zeroed, kRows);
+    mbar_init(v_zeroed + 1, kRows);
+    for (int i = 0; i < kSoftWarps; ++i) mbar_init(m_post + i, 1);
     mbar_init(mma_fin, NT);
     fence_mbar_init();
-    s_next = atomicAdd(p.work_claim, 1);
-    s_abort = 0;
+    s_abort = s_fail[0] = s_fail[1] = 0;
   }
-  __syncthreads();
-  int L = s_next;
-  if (L >= total) return;
   if (warp == G::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  int gch = 0;               // ring chunks of earlier tiles
-  int tch[NT] = {};          // a row tile's chunks of earlier tiles
-  int g_issued = 0;
-  for (;;) {
+  previous_done();
+  const int num_groups = (p.group + 7) / 8;
+  const int ny = p.num_kv_heads / 2 * num_groups;
+  const bool rejected = plan_rejected(p);
+  const int nwork = rejected ? 0 : *p.work_count;
+  const int nfull = rejected ? 0 : *p.work_full;
+  const int total = nwork * ny, total_full = nfull * ny;
+  if (tid == 0) s_next = rejected ? 0 : atomicAdd(p.work_claim, 1);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int L = s_next;
+  int gch = 0;       // ring chunks of earlier tiles: a chunk's place in the K and V rings
+  int tch[NT] = {};  // a row tile's chunks of earlier tiles
+  int maps_done = 0; // maps of earlier tiles: o_free's phases
+  int tails = 0;     // earlier tiles with a tail chunk: v_zeroed's
+  int k_issued = 0, v_issued = 0;
+  while (L < total) {
     const int lc = L < total_full ? L : L - total_full;
     const int nc = L < total_full ? nfull : nwork - nfull;
-    // (item, map) pairs run fastest but for the group, so that both maps of a tile are in flight together
-    const int x = (L < total_full ? 0 : nfull) + (lc >> 1) % nc, y = (lc >> 1) / nc, map = lc & 1;
+    const int x = (L < total_full ? 0 : nfull) + lc % nc, y = lc / nc;
     const int4 item = p.work[x];
     const int r = item.x, row0 = item.y, z = item.z;
     const int g = y / num_groups, hg = y % num_groups, kvh = 2 * g;
@@ -175,7 +243,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
       const int k1t = min(k0 + part, p.causal ? pos0 + t * tile_tokens + nt : seq_len);
       return k1t > klo ? (k1t - klo + kChunk - 1) / kChunk : 0;
     };
-    int nch_t[NT];
+    int nch_t[NT];  // a row tile's chunks under one map
 #pragma unroll
     for (int t = 0; t < NT; ++t) nch_t[t] = tile_chunks(t);
     const int k1 = min(k0 + part, p.causal ? pos0 + ntok : seq_len);
@@ -187,383 +255,444 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     const bool tail_chunk = nch > 0 && klo + nch * kChunk > kv_loaded_end;
     const int zero_tile = nch_t[NT - 1] == nch ? NT - 1 : 0;
 
-    const int row_tok = tid / gp, row_head = tid % gp;
-    const bool row_valid = tid < NT * kRows && row_tok < ntok && row_head < nh;
+    // Softmax warpgroup w, thread = row.  One row tile: w loads map w's queries; two: w's own rows, both maps
+    const int wg = warp >> 2, row = tid % kRows;
+    const int tile_row = kTurns ? row : wg * kRows + row;
+    const int row_tok = tile_row / gp, row_head = tile_row % gp;
+    const bool row_valid = warp < kSoftWarps && row_tok < ntok && row_head < nh;
     const int row_pos = pos0 + row_tok;
-    const int q_head = 2 * (h0 + row_head) + map;
-    int q_shift = 0;  // FP8 caches: the row times 2^q_shift fits f16
-    if (tid < NT * kRows) {
-      const uint4* src = row_valid ? reinterpret_cast<const uint4*>(
-                                         static_cast<const typename QE::T*>(p.q) +
-                                         ((long long)(row0 + row_tok) * p.num_q_heads + q_head) * HEAD)
-                                   : nullptr;
-      uint8_t* dst = sQ + (tid / kRows) * G::kQTile;
-      if constexpr (!kCvt) {
+    if (warp < kSoftWarps) {
+#pragma unroll 1
+      for (int mp = kTurns ? wg : 0; mp < (kTurns ? wg + 1 : 2); ++mp) {
+        const uint4* src = row_valid ? reinterpret_cast<const uint4*>(
+                                           static_cast<const typename QE::T*>(p.q) +
+                                           ((long long)(row0 + row_tok) * p.num_q_heads + 2 * (h0 + row_head) + mp) * HEAD)
+                                     : nullptr;
+        uint8_t* dst = sQ + ((kTurns ? 0 : wg) * 2 + mp) * G::kQTile;
+        if constexpr (!kCvt) {
 #pragma unroll
-        for (int c = 0; c < HEAD / 8; ++c) {
-          const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(tid % kRows, c & 7)) = v;
-        }
-      } else {
-        float amax = 0.f;
-        for (int c = 0; c < HEAD / 8 && src; ++c) {
-          const uint4 v = src[c];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2<QDT>(w[e]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          for (int c = 0; c < HEAD / 8; ++c) {
+            const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(row, c & 7)) = v;
           }
-        }
-        int ex = 0;
-        frexpf(amax, &ex);
-        q_shift = max(-100, min(100, 15 - ex));
+        } else {
+          float amax = 0.f;
+          for (int c = 0; c < HEAD / 8 && src; ++c) {
+            const uint4 v = src[c];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2<QDT>(w[e]);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          int ex = 0;
+          frexpf(amax, &ex);
+          const int shift = max(-100, min(100, 15 - ex));
+          s_shift[mp][tile_row] = static_cast<int8_t>(shift);
 #pragma unroll 4
-        for (int c = 0; c < HEAD / 8; ++c) {
-          const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
+          for (int c = 0; c < HEAD / 8; ++c) {
+            const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2<QDT>(w[e]);
-            h[e] = pack2<PA_F16>(ldexpf(f.x, q_shift), ldexpf(f.y, q_shift));
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2<QDT>(w[e]);
+              h[e] = pack2<PA_F16>(ldexpf(f.x, shift), ldexpf(f.y, shift));
+            }
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(row, c & 7)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
           }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(tid % kRows, c & 7)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
+      fence_proxy_async();
     }
-    fence_proxy_async();
     tc_fence_before();
-    __syncthreads();  // the Q rows are in place; every role of the previous tile is done
+    __syncthreads();  // the queries are in place; every role of the previous tile is done
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const int32_t* table = p.block_tables + (long long)r * p.max_blocks_per_seq;
 
-    if (warp == G::kProducer || warp == G::kProducer + 1) {
+    if (warp >= G::kProducer && warp < G::kMma) {
       // ------------------------------------------------------------ TMA producers
-      const bool is_v = warp != G::kProducer;
+      const bool does_k = warp == G::kProducer, does_v = kCvt || warp != G::kProducer;
       const int kb_end = (k1 + BS - 1) / BS;
       auto load_window = [&](int w) {
         const int kb = kb_first + 32 * w + lane;
         return kb < kb_end ? table[kb] : -1;
       };
-      int cur_w = 0;
-      int win = load_window(0);
-      int win_next = load_window(1);
-      for (int i = 0; i < nch; ++i) {
-        const int gi = gch + i, s = gi % RS;
-        if (gi >= RS && !__all_sync(0xffffffffu, mbar_wait_bounded(rempty + s, ((gi / RS) - 1) & 1))) {
-          if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
-          s_abort = 1;
-          break;
-        }
-        const int w = (i * NB) >> 5;  // NB divides 32: a chunk's blocks share a window
-        if (w != cur_w) {
-          win = win_next;
-          win_next = load_window(w + 1);
-          cur_w = w;
-        }
-        // A block out of range, and the chunk's end behind the last one, is copied from behind the
-        // cache's last block: zeros.  Scores of the former are masked by its bit.
-        int phys[NB];
-        int valid = 0;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int e = __shfl_sync(0xffffffffu, win, (i * NB + b) & 31);
-          const bool in_range = kb_first + i * NB + b < kb_end;
-          const bool ok_b = e >= 0 && e < p.num_blocks;
-          if (in_range && !ok_b && lane == 0 && !is_v) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
-          phys[b] = in_range && ok_b ? e : p.num_blocks;
-          valid |= (ok_b || !in_range) << b;
-        }
-        if (elect_one()) {
-          if (!is_v) s_valid[gi % kValidRing] = valid;
-          if constexpr (kCvt) {
-            uint8_t* sg = sStg + s * 3 * G::kStgTensor;
-            mbar_arrive_expect_tx(rfull + s, G::kStgTensor * (is_v ? 2 : 1));
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              if (is_v) {
-                for (int h = 0; h < 2; ++h)
-                  tma_load_4d(sg + (1 + h) * G::kStgTensor + b * G::kStgBlock, &args.tv, 0, (kvh + h) * BS, 0, phys[b],
-                              rfull + s);
-              } else {
-                tma_load_4d(sg + b * G::kStgBlock, &args.tk, 0, (kvh + map) * BS, 0, phys[b], rfull + s);
-              }
-            }
-          } else {
-            uint8_t* sk = sKV + s * G::kStageBytes;
-            mbar_arrive_expect_tx(full + s, is_v ? G::kVBytes : G::kKBytes);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              if (is_v) {
-                uint8_t* sv = sk + G::kKBytes + v_row_off<HEAD, BS>(b * BS, 0);
-                for (int h = 0; h < 2; ++h)
-                  tma_load_4d(sv + h * G::kPieces * BS * 128, &args.tv, 0, (kvh + h) * BS, 0, phys[b], full + s);
-              } else {
-#pragma unroll
-                for (int pc = 0; pc < G::kPieces; ++pc)
-                  tma_load_4d(sk + pc * G::kPiece + b * BS * 128, &args.tk, 0, (kvh + map) * BS, pc, phys[b], full + s);
-              }
-            }
-          }
-        }
-        __syncwarp();
-        g_issued = gi + 1;
-      }
-    } else if (kCvt && warp >= G::kConv) {
-      // ------------------------------------------------------------ FP8 converters: a row a thread
-      if constexpr (kCvt) {
-        const int ct = tid - G::kConv * 32;
-        const int tensor = ct / kChunk, key = ct % kChunk;  // K, V_1, V_2
-        const int blk = key / BS, tok = key % BS, sw = key & 7;
-        for (int i = 0; i < nch; ++i) {
-          const int gi = gch + i, s = gi % ST, ss = gi % G::kStg;
-          bool ok = mbar_wait_bounded(stg_full + ss, (gi / G::kStg) & 1);
-          if (gi >= ST) ok = ok && mbar_wait_bounded(empty + s, ((gi / ST) - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
-            s_abort = 1;
-            break;
-          }
-          const uint8_t* srow = sStg + (ss * 3 + tensor) * G::kStgTensor + blk * G::kStgBlock + tok * 128;
-          uint8_t* sk = sKV + s * G::kStageBytes;
-          uint8_t* drow = tensor == 0 ? sk + key * 128
-                                      : sk + G::kKBytes + v_row_off<HEAD, BS>(key, (tensor - 1) * G::kPieces);
-          const int piece_stride = tensor == 0 ? G::kPiece : BS * 128;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 codes = *reinterpret_cast<const uint4*>(srow + ((q ^ sw) << 4));
-            const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) fp8x4_to_f16x2x2<KVDT>(cw[e], h[2 * e], h[2 * e + 1]);
-            uint8_t* row = drow + (q >> 2) * piece_stride;
-            const int cc = (2 * q) & 7;
-            *reinterpret_cast<uint4*>(row + ((cc ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + (((cc + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
-          fence_proxy_async();
-          mbar_arrive(stg_empty + ss);
-          mbar_arrive(full + s);
-        }
-      }
-    } else if (warp >= G::kMma && warp < G::kConv) {
-      // ------------------------------------------------------------ MMA issuers, one warp a row tile
-      const int t = NT == 1 ? 0 : warp - G::kMma;
-      const int my_nch = NT == 1 ? nch_t[0] : t == 0 ? nch_t[0] : nch_t[NT - 1];
-      const int tc = NT == 1 ? tch[0] : t == 0 ? tch[0] : tch[NT - 1];
-      const uint32_t fmt = ODT == PA_BF16 ? 1u : 0u;
-      const uint32_t id_s = umma_idesc(kRows, kChunk, fmt, 0);
-      const uint32_t id_o = umma_idesc(kRows, G::kWide, fmt, 1);
-      const uint64_t qd = umma_desc(smem_u32(sQ) + t * G::kQTile, 16, 1024);
-      const uint64_t kd0 = umma_desc(smem_u32(sKV), 16, 1024);
-      const uint64_t vd0 = umma_desc(smem_u32(sKV) + G::kKBytes, BS * 128, 1024);
-      const uint32_t tT = tmem + t * G::kTileCols;
-      uint64_t* my_p_full = p_full + t * kSBufs;
-      auto issue_s = [&](int j) {
-        const uint64_t kd = kd0 + (uint64_t)((((gch + j) % ST) * G::kStageBytes) >> 4);
-        const uint32_t d = tT + ((tc + j) % kSBufs) * 64;
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < HEAD / 16; ++ks) {
-            const uint32_t qo = ((ks >> 2) * G::kQPiece + (ks & 3) * 32) >> 4;
-            const uint32_t ko = ((ks >> 2) * G::kPiece + (ks & 3) * 32) >> 4;
-            umma(d, qd + qo, kd + ko, id_s, ks > 0 ? 1u : 0u);
-          }
-          umma_commit(s_full + t * kSBufs + (tc + j) % kSBufs);
-        }
-        __syncwarp();
-      };
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-      };
       bool ok = true;
-      for (int j = 0; ok && j < kSBufs && j < my_nch; ++j) {
-        ok = wait_all(full + (gch + j) % ST, ((gch + j) / ST) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_s(j);
-      }
-      for (int i = 0; ok && i < nch; ++i) {
-        const int gi = gch + i, ci = tc + i;
-        if (i >= my_nch) {
-          // a chunk that this row tile does not read: its stage is released once it has landed
-          if (!(ok = wait_all(full + gi % ST, (gi / ST) & 1))) break;
-          if (elect_one()) mbar_arrive(empty + gi % ST);
-          __syncwarp();
-          continue;
-        }
-        // the last chunk's V is read only after the row tile that zeroes its end has written P
-        if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile) {
-          const int cz = (zero_tile == 0 ? tch[0] : tch[NT - 1]) + i;
-          if (!(ok = wait_all(p_full + zero_tile * kSBufs + cz % kSBufs, (cz / kSBufs) & 1))) break;
-        }
-        if (!(ok = wait_all(my_p_full + ci % kSBufs, (ci / kSBufs) & 1))) break;
-        tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(((gi % ST) * G::kStageBytes) >> 4);
-        const uint32_t pt = tT + (ci % kSBufs) * 64;
-        if (elect_one()) {
+      // stage gi of a ring is free: its last reader is done
+      auto free_stage = [&](uint64_t* empty, int stages, int gi) {
+        return gi < stages || __all_sync(0xffffffffu, mbar_wait_bounded(empty + gi % stages, ((gi / stages) - 1) & 1));
+      };
+      for (int mp = 0; ok && mp < 2; ++mp) {
+        int cur_w = 0;
+        int win = load_window(0);
+        int win_next = load_window(1);
+        for (int i = 0; i < nch; ++i) {
+          const int gi = gch + mp * nch + i;
+          const int w = (i * NB) >> 5;  // NB divides 32: a chunk's blocks share a window
+          if (w != cur_w) {
+            win = win_next;
+            win_next = load_window(w + 1);
+            cur_w = w;
+          }
+          // A block out of range, and the chunk's end behind the last one, is copied from behind the
+          // cache's last block: zeros.  Scores of the former are masked by its bit.
+          int phys[NB];
+          int valid = 0;
 #pragma unroll
-          for (int ks = 0; ks < kChunk / 16; ++ks)
-            umma_tmem_a(tT + kOCol, pt + ks * 8, vd + (uint64_t)(v_row_off<HEAD, BS>(16 * ks, 0) >> 4), id_o,
-                        (i > 0 || ks > 0) ? 1u : 0u);
-          umma_commit(o_done + t * kSBufs + ci % kSBufs);
-          umma_commit(empty + gi % ST);
-        }
-        __syncwarp();
-        const int j = i + kSBufs;
-        if (j < my_nch) {
-          if (!(ok = wait_all(full + (gch + j) % ST, ((gch + j) / ST) & 1))) break;
-          tc_fence_after();
-          issue_s(j);
+          for (int b = 0; b < NB; ++b) {
+            const int e = __shfl_sync(0xffffffffu, win, (i * NB + b) & 31);
+            const bool in_range = kb_first + i * NB + b < kb_end;
+            const bool ok_b = e >= 0 && e < p.num_blocks;
+            if (in_range && !ok_b && lane == 0 && does_k) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
+            phys[b] = in_range && ok_b ? e : p.num_blocks;
+            valid |= (ok_b || !in_range) << b;
+          }
+          if (does_k) {
+            constexpr int RS = kCvt ? SG : KST;
+            uint64_t* full = (kCvt ? stgk_full : k_full) + gi % RS;
+            if (!(ok = free_stage(kCvt ? stgk_empty : k_empty, RS, gi))) break;
+            if (elect_one()) {
+              s_valid[gi % kValidRing] = valid;
+              mbar_arrive_expect_tx(full, kCvt ? G::kStgTensor : G::kKBytes);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                if constexpr (kCvt) {
+                  tma_load_4d(sStgK + gi % RS * G::kStgTensor + b * G::kStgBlock, &args.tk, 0, (kvh + mp) * BS, 0, phys[b],
+                              full);
+                } else {
+#pragma unroll
+                  for (int pc = 0; pc < G::kPieces; ++pc)
+                    tma_load_4d(sK + gi % RS * G::kKBytes + pc * G::kPiece + b * BS * 128, &args.tk, 0, (kvh + mp) * BS, pc,
+                                phys[b], full);
+                }
+              }
+            }
+            __syncwarp();
+            k_issued = gi + 1;
+          }
+          if (does_v) {
+            constexpr int RS = kCvt ? SG : VST;
+            uint64_t* full = (kCvt ? stgv_full : v_full) + gi % RS;
+            if (!(ok = free_stage(kCvt ? stgv_empty : v_empty, RS, gi))) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(full, kCvt ? 2 * G::kStgTensor : G::kVBytes);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint8_t* d = kCvt ? sStgV + (gi % RS * 2 + h) * G::kStgTensor + b * G::kStgBlock
+                                    : sV + gi % RS * G::kVBytes + v_row_off<HEAD, BS>(b * BS, h * G::kPieces);
+                  tma_load_4d(d, &args.tv, 0, (kvh + h) * BS, 0, phys[b], full);
+                }
+              }
+            }
+            __syncwarp();
+            v_issued = gi + 1;
+          }
         }
       }
       if (!ok) {
         if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
         s_abort = 1;
       }
-    } else if (warp < 4 * NT) {
+    } else if (kCvt && warp >= G::kConvK) {
+      // ------------------------------------------------------------ FP8 converters: a row a thread
+      if constexpr (kCvt) {
+        const bool is_v = warp >= G::kConvV;
+        const int ct = tid - (is_v ? G::kConvV : G::kConvK) * 32;
+        const int half = ct / kChunk, key = ct % kChunk, blk = key / BS, tok = key % BS;
+        uint64_t* sf = is_v ? stgv_full : stgk_full;
+        uint64_t* se = is_v ? stgv_empty : stgk_empty;
+        uint64_t* df = is_v ? v_full : k_full;
+        uint64_t* de = is_v ? v_empty : k_empty;
+        const int DST = is_v ? VST : KST;
+        for (int i = 0; i < 2 * nch; ++i) {
+          const int gi = gch + i, s = gi % DST, ss = gi % SG;
+          bool ok = mbar_wait_bounded(sf + ss, (gi / SG) & 1);
+          if (gi >= DST) ok = ok && mbar_wait_bounded(de + s, ((gi / DST) - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
+            s_abort = 1;
+            break;
+          }
+          if (is_v)
+            widen_row<KVDT>(sStgV + (ss * 2 + half) * G::kStgTensor + blk * G::kStgBlock + tok * 128,
+                            sV + s * G::kVBytes + v_row_off<HEAD, BS>(key, half * G::kPieces), BS * 128, key & 7);
+          else
+            widen_row<KVDT>(sStgK + ss * G::kStgTensor + blk * G::kStgBlock + tok * 128, sK + s * G::kKBytes + key * 128,
+                            G::kPiece, key & 7);
+          fence_proxy_async();
+          mbar_arrive(se + ss);
+          mbar_arrive(df + s);
+        }
+      }
+    } else if (warp >= G::kMma && warp < G::kConvK) {
+      // ------------------------------------------------------------ MMA issuers, one warp a row tile
+      // As soon as P(i) is written PV(i), then S(i + SB) into the buffer that PV(i) frees: a thread's
+      // MMAs run in the order of their issue.
+      const int t = NT == 1 ? 0 : warp - G::kMma;
+      const int my_nch = t == 0 ? nch_t[0] : nch_t[NT - 1];
+      const int tc = t == 0 ? tch[0] : tch[NT - 1];
+      const uint32_t fmt = ODT == PA_BF16 ? 1u : 0u;
+      const uint32_t id_s = umma_idesc(kRows, kChunk, fmt, 0);
+      const uint32_t id_o = umma_idesc(kRows, G::kWide, fmt, 1);
+      const uint64_t qd0 = umma_desc(smem_u32(sQ) + t * 2 * G::kQTile, 16, 1024);
+      const uint64_t kd0 = umma_desc(smem_u32(sK), 16, 1024);
+      const uint64_t vd0 = umma_desc(smem_u32(sV), BS * 128, 1024);
+      const uint32_t tT = tmem + t * G::kTileCols;
+      uint64_t* my_s_full = s_full + t * SB;
+      uint64_t* my_p_full = p_full + t * SB;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+      };
+      // the row tile's j-th chunk (of both maps): S(j) behind its keys; false where a wait gave up
+      auto issue_s = [&](int j) {
+        const int mp = j >= my_nch, gi = gch + (mp ? nch + j - my_nch : j);
+        if (!wait_all(k_full + gi % KST, (gi / KST) & 1)) return false;
+        tc_fence_after();
+        const uint64_t qd = qd0 + (uint64_t)(mp * G::kQTile >> 4);
+        const uint64_t kd = kd0 + (uint64_t)((gi % KST) * G::kKBytes >> 4);
+        const int buf = (tc + j) % SB;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < HEAD / 16; ++ks) {
+            const uint32_t qo = ((ks >> 2) * G::kQPiece + (ks & 3) * 32) >> 4;
+            const uint32_t ko = ((ks >> 2) * G::kPiece + (ks & 3) * 32) >> 4;
+            umma(tT + buf * 64, qd + qo, kd + ko, id_s, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(my_s_full + buf);
+          umma_commit(k_empty + gi % KST);
+          mbar_arrive(my_s_full + buf);  // passes on what k_full brought: the chunk's s_valid
+        }
+        __syncwarp();
+        return true;
+      };
+      // chunks of the rings that this row tile does not read are released once they have landed
+      auto skip = [&](uint64_t* full, uint64_t* empty, int stages, int gi) {
+        if (!wait_all(full + gi % stages, (gi / stages) & 1)) return false;
+        if (elect_one()) mbar_arrive(empty + gi % stages);
+        __syncwarp();
+        return true;
+      };
+      bool ok = true;
+      // S runs SB chunks ahead; keys behind a map's last chunk are skipped on the way
+      auto advance = [&](int j) {
+        ok = ok && issue_s(j);
+        if (NT > 1 && (j == my_nch - 1 || j == 2 * my_nch - 1))
+          for (int i = my_nch; ok && i < nch; ++i)
+            ok = skip(k_full, k_empty, KST, gch + (j >= my_nch ? nch : 0) + i);
+      };
+      if (NT > 1 && my_nch == 0)
+        for (int i = 0; ok && i < 2 * nch; ++i)
+          ok = skip(k_full, k_empty, KST, gch + i) && skip(v_full, v_empty, VST, gch + i);
+      for (int j = 0; ok && j < SB && j < 2 * my_nch; ++j) advance(j);
+      for (int j = 0; ok && j < 2 * my_nch; ++j) {
+        const int mp = j >= my_nch, i = mp ? j - my_nch : j;
+        const int gi = gch + mp * nch + i, ci = tc + j, buf = ci % SB;
+        // the last chunk's V is read only after the row tile that zeroes its end has written P
+        if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile &&
+            !(ok = wait_all(v_zeroed + mp, tails & 1)))
+          break;
+        if (!(ok = wait_all(my_p_full + buf, (ci / SB) & 1))) break;
+        if (!(ok = wait_all(v_full + gi % VST, (gi / VST) & 1))) break;
+        // a map's first product overwrites O, which the map before it must have been read from
+        if (i == 0 && (maps_done + mp) > 0 && !(ok = wait_all(o_free + t, (maps_done + mp - 1) & 1))) break;
+        tc_fence_after();
+        const uint64_t vd = vd0 + (uint64_t)((gi % VST) * G::kVBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < kChunk / 16; ++ks)
+            umma_tmem_a(tT + G::kOCol, tT + buf * 64 + ks * 8, vd + (uint64_t)(v_row_off<HEAD, BS>(16 * ks, 0) >> 4),
+                        id_o, (i > 0 || ks > 0) ? 1u : 0u);
+          umma_commit(o_done + t * SB + buf);
+          umma_commit(v_empty + gi % VST);
+        }
+        __syncwarp();
+        if (NT > 1 && i == my_nch - 1)
+          for (int q = my_nch; ok && q < nch; ++q) ok = skip(v_full, v_empty, VST, gch + mp * nch + q);
+        if (ok && j + SB < 2 * my_nch) advance(j + SB);
+      }
+      if (!ok) {
+        if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
+        s_abort = 1;
+      }
+    } else if (warp < kSoftWarps) {
       // ------------------------------------------------------------ softmax: a row a thread
-      const int t = NT == 1 ? 0 : warp >> 2;
-      const int my_nch = NT == 1 ? nch_t[0] : t == 0 ? nch_t[0] : nch_t[NT - 1];
-      const int tc = NT == 1 ? tch[0] : t == 0 ? tch[0] : tch[NT - 1];
+      const int t = kTurns ? 0 : wg;
+      const int my_nch = t == 0 ? nch_t[0] : nch_t[NT - 1];
+      const int tc = t == 0 ? tch[0] : tch[NT - 1];
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t tT = tmem + t * G::kTileCols;
-      const uint32_t tO = tT + kOCol;
-      uint64_t* my_s_full = s_full + t * kSBufs;
-      uint64_t* my_p_full = p_full + t * kSBufs;
-      uint64_t* my_o_done = o_done + t * kSBufs;
-      const float c = kCvt ? ldexpf(p.scale * kLog2e * p.k_scale[(kvh + map) * p.scale_stride], -q_shift)
-                           : p.scale * kLog2e;
+      const uint32_t tO = tT + G::kOCol + (kTurns ? wg * G::kCols : 0);  // this thread's columns of O
+      uint64_t* my_s_full = s_full + t * SB;
+      uint64_t* my_p_full = p_full + t * SB;
+      uint64_t* my_o_done = o_done + t * SB;
       const int row_limit = p.causal ? min(k1, row_pos + 1) : k1;
       const int row_lo = p.window > 0 ? max(0, row_pos - p.window + 1) : 0;
-      float m = -INFINITY, l = 0.f;
+      const int kv_len = p.causal ? row_pos + 1 : seq_len;
+      const int parts_row = (kv_len - origin + part - 1) / part;
+      const bool write = row_valid && z < parts_row;
+      const bool direct = parts_row == 1;
+      const int head = h0 + row_head;
+      const long long pi = (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req + z;
+      const int col0 = kTurns ? wg * G::kCols : 0;
       bool fail = false;
-      for (int i = 0; i < my_nch; ++i) {
-        const int base = klo + i * kChunk;
-        const int ci = tc + i, gi = gch + i;
-        const uint32_t tS = tT + (ci % kSBufs) * 64;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(my_s_full + ci % kSBufs, (ci / kSBufs) & 1))) {
-          fail = true;
-          break;
-        }
-        tc_fence_after();
-        uint32_t sr[kChunk];
-        tmem_ld32(tS + lane_base, sr);
-        tmem_ld32(tS + 32 + lane_base, sr + 32);
-        tmem_wait_ld();
-        float sc[kChunk];
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) sc[j] = __uint_as_float(sr[j]);
-        const int rem = row_limit - base, lo_rem = row_lo - base;
-        if (rem < kChunk || lo_rem > 0) {
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j)
-            if (j >= rem || j < lo_rem) sc[j] = -INFINITY;
-        }
-        // the chunk has long landed: its word is there to be read
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + gi % ST, (gi / ST) & 1))) {
-          fail = true;
-          break;
-        }
-        const int valid = s_valid[gi % kValidRing];
-        if (valid != (1 << NB) - 1) {
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j)
-            if (!(valid >> (j / BS) & 1)) sc[j] = -INFINITY;
-        }
-        float mq[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float v = max3(sc[8 * q], sc[8 * q + 1], sc[8 * q + 2]);
-          v = max3(v, sc[8 * q + 3], sc[8 * q + 4]);
-          v = max3(v, sc[8 * q + 5], sc[8 * q + 6]);
-          mq[q] = fmaxf(v, sc[8 * q + 7]);
-        }
-        const float mx = max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7])) * c;
-        const bool need = mx > m + kRescaleSlack;
-        float al = 1.f;
-        if (need) {
-          const float nm = fmaxf(m, mx);
-          al = ex2_approx(m - nm);
-          m = nm;
-          l *= al;
-        }
-        const float u = m == -INFINITY ? 0.f : m;
-        const uint64_t c2 = f2_pack(c, c), nu2 = f2_pack(-u, -u);
-        uint32_t pk[kChunk / 2];
-        uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int j = 0; j < kChunk / 2; ++j) {
-          const float2 v = f2_unpack(f2_fma(f2_pack(sc[2 * j], sc[2 * j + 1]), c2, nu2));
-          const float e0 = ex2_approx(v.x), e1 = ex2_approx(v.y);
-          acc2[j & 3] = f2_add(acc2[j & 3], f2_pack(e0, e1));
-          pk[j] = pack2<ODT>(e0, e1);
-        }
-        const float2 lsum = f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])));
-        l += lsum.x + lsum.y;
-        // O is rescaled only once PV(i - 1) has completed
-        if (__any_sync(0xffffffffu, need) && i > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + (ci - 1) % kSBufs, ((ci - 1) / kSBufs) & 1))) {
+#pragma unroll 1
+      for (int mp = 0; !fail && mp < 2; ++mp) {
+        const float c = kCvt ? ldexpf(p.scale * kLog2e * p.k_scale[(kvh + mp) * p.scale_stride], -s_shift[mp][tile_row])
+                             : p.scale * kLog2e;
+        float m = -INFINITY, l = 0.f;  // m: the row's maximum when this thread last saw it
+#pragma unroll 1
+        for (int i = 0; i < my_nch; ++i) {
+          const int ci = tc + mp * my_nch + i, buf = ci % SB;
+          if (kTurns && (ci & 1) != wg) continue;
+          const int gi = gch + mp * nch + i;
+          const int base = klo + i * kChunk;
+          const uint32_t tS = tT + buf * 64;
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(my_s_full + buf, (ci / SB) & 1))) {
             fail = true;
             break;
           }
           tc_fence_after();
-#pragma unroll 1
-          for (int cb = 0; cb < G::kWide; cb += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + cb + lane_base, o);
-            tmem_wait_ld();
+          uint32_t sr[kChunk];
+          tmem_ld32(tS + lane_base, sr);
+          tmem_ld32(tS + 32 + lane_base, sr + 32);
+          const int valid = s_valid[gi % kValidRing];
+          tmem_wait_ld();
+          float sc[kChunk];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-            tmem_st32(tO + cb + lane_base, o);
-          }
-        }
-        tmem_st32(tS + lane_base, pk);  // P(i) over the first half of S(i)'s columns
-        // V rows past the loaded keys may hold any bits: zeroed, to keep 0 * V finite
-        if (tail_chunk && t == zero_tile && i == nch - 1) {
-          const int vrem = kv_loaded_end - base;
-          for (int q = tid % kRows; q < 2 * G::kPieces * kChunk; q += kRows) {
-            const int key = q % kChunk;
-            if (key < vrem) continue;
-            uint4* d = reinterpret_cast<uint4*>(sKV + (gi % ST) * G::kStageBytes + G::kKBytes +
-                                                v_row_off<HEAD, BS>(key, q / kChunk));
+          for (int j = 0; j < kChunk; ++j) sc[j] = __uint_as_float(sr[j]);
+          const int rem = row_limit - base, lo_rem = row_lo - base;
+          if (rem < kChunk || lo_rem > 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < kChunk; ++j)
+              if (j >= rem || j < lo_rem) sc[j] = -INFINITY;
           }
-          fence_proxy_async();
-        }
-        tmem_wait_st();
-        // PV(i - 2) is observed, so that no phase of o_done is ever two behind
-        if (i >= kSBufs &&
-            !__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + ci % kSBufs, ((ci - kSBufs) / kSBufs) & 1))) {
-          fail = true;
-          break;
-        }
-        tc_fence_before();
-        mbar_arrive(my_p_full + ci % kSBufs);
-      }
-      if (!fail && my_nch > 0) {
-        const int cl = tc + my_nch - 1;
-        fail = !__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + cl % kSBufs, (cl / kSBufs) & 1));
-        tc_fence_after();
-      }
-      if (fail) {
-        if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
-        s_abort = 1;
-      } else {
-        // ---- epilogue: the row's partial state (unnormalised O, maximum in log2 units, sum)
-        const int kv_len = p.causal ? row_pos + 1 : seq_len;
-        const int parts_row = (kv_len - origin + part - 1) / part;
-        const bool write = row_valid && z < parts_row;
-        const long long pi = (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req + z;
-        const long long at = pi * p.num_q_heads + q_head;
-        float* w_row = p.ws_acc + at * G::kWide;
+          if (valid != (1 << NB) - 1) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j)
+              if (!(valid >> (j / BS) & 1)) sc[j] = -INFINITY;
+          }
+          float mq[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float v = max3(sc[8 * q], sc[8 * q + 1], sc[8 * q + 2]);
+            v = max3(v, sc[8 * q + 3], sc[8 * q + 4]);
+            v = max3(v, sc[8 * q + 5], sc[8 * q + 6]);
+            mq[q] = fmaxf(v, sc[8 * q + 7]);
+          }
+          const float mx = max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7])) * c;
+          float m_prev = m;  // the row's maximum before this chunk
+          if constexpr (kTurns) {
+            // the other warpgroup's warp of the same rows posted it with the chunk before
+            if (ci > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(m_post + (warp ^ 4), ((ci - 1) >> 1) & 1))) {
+              fail = true;
+              break;
+            }
+            m_prev = i > 0 ? s_m[wg ^ 1][row] : -INFINITY;
+          }
+          const bool need = mx > m_prev + kRescaleSlack;
+          const float nm = need ? fmaxf(m_prev, mx) : m_prev;
+          if constexpr (kTurns) {
+            s_m[wg][row] = nm;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m_post + warp);
+          }
+          if (nm != m) {
+            l *= ex2_approx(m - nm);  // 0 while this thread's sum is
+            m = nm;
+          }
+          const float u = m == -INFINITY ? 0.f : m;
+          const uint64_t c2 = f2_pack(c, c), nu2 = f2_pack(-u, -u);
+          uint32_t pk[kChunk / 2];
+          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int j = 0; j < kChunk / 2; ++j) {
+            const float2 v = f2_unpack(f2_fma(f2_pack(sc[2 * j], sc[2 * j + 1]), c2, nu2));
+            const float e0 = ex2_approx(v.x), e1 = ex2_approx(v.y);
+            acc2[j & 3] = f2_add(acc2[j & 3], f2_pack(e0, e1));
+            pk[j] = pack2<ODT>(e0, e1);
+          }
+          const float2 lsum = f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])));
+          l += lsum.x + lsum.y;
+          tmem_st32(tS + lane_base, pk);  // P(i) over the first half of S(i)'s columns
+          // O is rescaled only once PV(i - 1) has completed
+          if (__any_sync(0xffffffffu, need) && i > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + (ci - 1) % SB, ((ci - 1) / SB) & 1))) {
+              fail = true;
+              break;
+            }
+            tc_fence_after();
+            const float al = need ? ex2_approx(m_prev - nm) : 1.f;
 #pragma unroll 1
-        for (int cb = 0; cb < G::kWide; cb += 32) {
-          const float vs = kCvt ? p.v_scale[(kvh + cb / HEAD) * p.scale_stride] : 1.f;
+            for (int cb = 0; cb < G::kWide; cb += 32) {
+              uint32_t o[32];
+              tmem_ld32(tT + G::kOCol + cb + lane_base, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+              tmem_st32(tT + G::kOCol + cb + lane_base, o);
+            }
+          }
+          // V rows past the sequence may hold any bits: zeroed, to keep 0 * V finite
+          if (tail_chunk && t == zero_tile && i == nch - 1) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_full + gi % VST, (gi / VST) & 1))) {
+              fail = true;
+              break;
+            }
+            const int vrem = kv_loaded_end - base;
+            for (int q = row; q < 2 * G::kPieces * kChunk; q += kRows) {
+              const int key = q % kChunk;
+              if (key < vrem) continue;
+              uint4* d = reinterpret_cast<uint4*>(sV + (gi % VST) * G::kVBytes + v_row_off<HEAD, BS>(key, q / kChunk));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) d[e] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+            if (NT > 1) mbar_arrive(v_zeroed + mp);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(my_p_full + buf);
+        }
+        // ---- the map's end: O is complete, the row's maximum and sum are joined
+        const int cl = tc + (mp + 1) * my_nch - 1;  // the map's last chunk
+        if (!fail && my_nch > 0) {
+          bool got = mbar_wait_bounded(my_o_done + cl % SB, (cl / SB) & 1);
+          if (kTurns && (cl & 1) != wg) got = got && mbar_wait_bounded(m_post + (warp ^ 4), (cl >> 1) & 1);
+          fail = !__all_sync(0xffffffffu, got);
+          tc_fence_after();
+        }
+        if constexpr (kTurns) {
+          if (!fail && my_nch > 0) {
+            const float last = s_m[cl & 1][row];
+            if (last != m) {
+              l *= ex2_approx(m - last);
+              m = last;
+            }
+          }
+          s_l[mp][wg][row] = l;
+          if (fail) s_fail[mp] = 1;
+          softmax_sync();
+          fail = s_fail[mp] != 0;  // all or none go on: there is another such meeting below
+          l = s_l[mp][0][row] + s_l[mp][1][row];
+        }
+        if (fail) break;
+        const long long at = pi * p.num_q_heads + 2 * head + mp;
+        float* ws = p.ws_acc + at * G::kWide + col0;
+        float weight = diff_weight(l);
+        if (mp == 1 && write && direct) weight *= -diff_lambda(args.p, qs + t0 + row_tok, head);
+        float sq = 0.f;
+        typename QE::T* out = static_cast<typename QE::T*>(p.out) +
+                              ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
+        const bool norm = mp == 1 && args.p.norm_weight != nullptr;
+#pragma unroll 1
+        for (int cb = 0; cb < G::kCols; cb += 32) {
+          const float vs = kCvt ? p.v_scale[(kvh + (col0 + cb) / HEAD) * p.scale_stride] : 1.f;
+          const float f = direct ? vs * weight : vs;
           uint32_t o[32];
           if (my_nch > 0) {
             tmem_ld32(tO + cb + lane_base, o);
@@ -572,42 +701,101 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0u;
           }
-          if (!write) continue;
+          float v[32];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(w_row + cb + 4 * q) =
-                make_float4(__uint_as_float(o[4 * q]) * vs, __uint_as_float(o[4 * q + 1]) * vs,
-                            __uint_as_float(o[4 * q + 2]) * vs, __uint_as_float(o[4 * q + 3]) * vs);
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
+          if (mp == 1 && direct && write) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 a = *reinterpret_cast<const float4*>(ws - G::kWide + cb + 4 * q);  // map 1's
+              v[4 * q] += a.x;
+              v[4 * q + 1] += a.y;
+              v[4 * q + 2] += a.z;
+              v[4 * q + 3] += a.w;
+            }
+          }
+          if (norm) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              sq = fmaf(v[j], v[j], sq);
+              o[j] = __float_as_uint(v[j]);
+            }
+            tmem_st32(tO + cb + lane_base, o);  // kept for the second look
+          }
+          if (!write) continue;
+          if (mp == 0 || !direct) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(ws + cb + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          } else if (!norm) {
+            store_row<QDT>(out + cb, v);
+          }
         }
-        if (write) p.ws_ml[at] = make_float2(m, l);
+        if (write && !direct && (!kTurns || wg == 0)) p.ws_ml[at] = make_float2(m, l);
+        if (norm) {
+          if constexpr (kTurns) {
+            s_sq[wg][row] = sq;
+            softmax_sync();
+            sq = s_sq[0][row] + s_sq[1][row];
+          }
+          const float rn = rsqrtf(sq / G::kWide + args.p.norm_eps);
+          tmem_wait_st();
+#pragma unroll 1
+          for (int cb = 0; cb < G::kCols; cb += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + cb + lane_base, o);
+            tmem_wait_ld();
+            if (!write || !direct) continue;
+            float v[32];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float* w = args.p.norm_weight + col0 + cb + 4 * q;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(o[4 * q + e]) * (rn * w[e]);
+            }
+            store_row<QDT>(out + cb, v);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(o_free + t);
+      }
+      if (fail) {
+        if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
+        s_abort = 1;
       }
     }
 
-    gch += nch;
+    gch += 2 * nch;
+    maps_done += 2;
+    tails += tail_chunk;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) tch[t] += nch_t[t];
+    for (int t = 0; t < NT; ++t) tch[t] += 2 * nch_t[t];
     if (tid == 0) s_next = atomicAdd(p.work_claim, 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     L = s_next;
-    if (L >= total || s_abort) break;
+    if (s_abort) break;
   }
 
   // ---- every MMA completes and every copy lands before TMEM is released and the CTA leaves
-  if (warp >= G::kMma && warp < G::kConv) {
+  if (warp >= G::kMma && warp < G::kConvK) {
     if (elect_one()) umma_commit(mma_fin);
     __syncwarp();
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(mma_fin, 0)) && lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
-  } else if ((warp == G::kProducer || warp == G::kProducer + 1) && lane == 0) {
-    for (int j = max(0, g_issued - RS); j < g_issued; ++j)
-      if (!mbar_wait_bounded(rfull + j % RS, (j / RS) & 1)) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
+  } else if (warp >= G::kProducer && warp < G::kMma && lane == 0) {
+    constexpr int KR = kCvt ? SG : KST, VR = kCvt ? SG : VST;
+    bool ok = true;
+    for (int j = max(0, k_issued - KR); j < k_issued; ++j)
+      ok = mbar_wait_bounded((kCvt ? stgk_full : k_full) + j % KR, (j / KR) & 1) && ok;
+    for (int j = max(0, v_issued - VR); j < v_issued; ++j)
+      ok = mbar_wait_bounded((kCvt ? stgv_full : v_full) + j % VR, (j / VR) & 1) && ok;
+    if (!ok) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == G::kMma) {
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
@@ -619,14 +807,13 @@ cudaError_t launch_t(const DiffParams& p, int num_items, int max_ctas, const CUt
   constexpr auto kern = diff_prefill_kernel<QDT, KVDT, HEAD, BS>;
   const cudaError_t e = set_smem<kern>(G::kSmem);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)num_items * p.a.num_kv_heads * ((p.a.group + 7) / 8);
+  const long long tiles = (long long)num_items * (p.a.num_kv_heads / 2) * ((p.a.group + 7) / 8);
   const int grid = static_cast<int>(std::min<long long>(tiles, std::max(1, max_ctas)));
   DiffPrefillArgs args;
   args.p = p;
   args.tk = *tk;
   args.tv = *tv;
-  kern<<<grid, G::kThreads, G::kSmem, stream>>>(args);
-  return cudaGetLastError();
+  return launch_early<DiffPrefillArgs>(kern, dim3(grid), G::kThreads, G::kSmem, 1, args, stream);
 }
 
 template <int QDT, int KVDT, int HEAD>
