@@ -168,10 +168,10 @@ struct VarlenLayout {
 };
 
 VarlenLayout varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
-                           int requested, int tile_tokens) {
+                           int requested, int tile_tokens, int part_pf = 0) {
   VarlenLayout L;
   L.part = resolve_partition(requested, num_seqs, hkv, max_seq_len, bs);
-  L.part_pf = requested > 0 ? L.part : prefill_partition(L.part);
+  L.part_pf = requested > 0 ? L.part : part_pf > 0 ? part_pf : prefill_partition(L.part);
   L.parts = ceil_div(max_seq_len, L.part);
   L.parts_pf = ceil_div(max_seq_len, L.part_pf);
   L.max_work = (ceil_div(total_q, tile_tokens) + num_seqs) * L.parts_pf;
@@ -533,6 +533,19 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
       overlap(out, row_bytes, norm_weight, norm_weight ? (size_t)2 * head_size * 4 : 0))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
+}
+
+// Chunks of new tokens: partitions so long that the row tiles' states are few, but where there are
+// fewer tiles than SMs the context is split until there are some two items an SM (a chunk of 37
+// tokens on 1,000: 47 us with one partition, 23 with 17).
+VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
+                                int requested) {
+  const int tile_tokens = pa::diff_prefill_tile_tokens(hq / hkv, d);
+  const long long tiles = ceil_div(total_q, tile_tokens) * (std::max(2, hkv) / 2) * std::max(1LL, ceil_div(hq / hkv, 8));
+  const long long parts = std::max(1LL, ceil_div(2 * sm_count(), tiles));
+  const int least = round_up(64, bs);
+  const int part = std::min(round_up(16384, least), round_up(std::max(least, static_cast<int>(ceil_div(max_seq_len, parts))), least));
+  return varlen_layout(num_seqs, total_q, hq, hkv / 2, 2 * d, max_seq_len, bs, requested, tile_tokens, part);
 }
 
 bool diff_decode_maps(CUtensorMap* tk, CUtensorMap* tv, const AttnParams& a, int kv_dtype) {
@@ -1388,9 +1401,9 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_z, -1, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  if (L.parts > 1) {
+  if (grid_z > 1) {
     TraceScope t(16, s);
-    e = pa::launch_diff_merge(p, q_dtype, s);
+    e = pa::launch_diff_merge(p, q_dtype, 1, grid_z, s);
   }
   return cuda_status(e);
 }
@@ -1402,8 +1415,8 @@ size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, i
   if (num_seqs < 1 || total_q_tokens < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_size < 1 ||
       max_seq_len < 1 || block_size < 1)
     return 256;
-  return varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size, max_seq_len,
-                       block_size, partition_size, pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size))
+  return diff_varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size,
+                            partition_size)
       .total;
 }
 
@@ -1432,8 +1445,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
   const int tile_tokens = pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size);
-  const VarlenLayout L = varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads / 2, 2 * head_size,
-                                       max_seq_len, block_size, partition_size, tile_tokens);
+  const VarlenLayout L = diff_varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len,
+                                            block_size, partition_size);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
   if (overlap(out, (size_t)total_q_tokens * num_q_heads * head_size * dtype_bytes(q_dtype), workspace, L.total))
     return PA_ERR_INVALID_ARG;
@@ -1474,7 +1487,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  const bool multi = max_query_len > 1;
+  // One request of several tokens: no single-token rows.
+  const bool multi = max_query_len > 1, single = num_seqs > 1 || total_q_tokens == 1;
   const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
   const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
   if (!fast_decode) {
@@ -1482,26 +1496,55 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
   } else {
-    CUtensorMap tk, tv;
+    // Single-token rows (bound by memory) beside the tiles (bound by the tensor cores), as in
+    // pa_varlen_attn: the tiles hold two thirds of the SMs first, and all of them once the rows end.
+    CUtensorMap tk, tv, pk, pv;
+    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
+    if (fast_prefill &&
+        (!encode_cache_map(&pk, k_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, true) ||
+         !encode_cache_map(&pv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size)))
+      return PA_ERR_CUDA;
+    std::unique_lock<std::mutex> lock(g_side_mutex, std::defer_lock);
+    SideStream* side = nullptr;
+    if (multi && single) {
+      lock.lock();
+      side = side_stream();
+    }
+    cudaStream_t s2 = s;
+    if (side && cudaEventRecord(side->fork, s) == cudaSuccess &&
+        cudaStreamWaitEvent(side->stream, side->fork, 0) == cudaSuccess)
+      s2 = side->stream;
+    const int sms = sm_count(), items = static_cast<int>(L.max_work);
+    const bool split = fast_prefill && s2 != s;
     if (fast_prefill) {
-      if (!encode_cache_map(&tk, k_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, true) ||
-          !encode_cache_map(&tv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size))
-        return PA_ERR_CUDA;
       TraceScope t(17, s);
-      e = pa::launch_diff_prefill(p, q_dtype, kv_dtype, static_cast<int>(L.max_work), sm_count(), &tk, &tv, s);
+      const int ctas = split ? std::max(1, sms * kPrefillShareNum / kPrefillShareDen) : sms;
+      e = pa::launch_diff_prefill(p, q_dtype, kv_dtype, items, ctas, &pk, &pv, s);
     } else if (multi) {
       TraceScope t(15, s);
       e = pa::launch_diff_generic(p, q_dtype, kv_dtype, grid_pf, 1, s);
     }
-    if (e != cudaSuccess) return PA_ERR_CUDA;
-    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
-    TraceScope t(15, s);
-    e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s);
+    if (e == cudaSuccess && single) {
+      TraceScope t(15, s2);
+      e = pa::launch_diff_decode(p, q_dtype, kv_dtype, grid_dec, &tk, &tv, s2);
+    }
+    if (e == cudaSuccess && split) {  // the tiles still unclaimed
+      TraceScope t(17, s2);
+      e = pa::launch_diff_prefill(p, q_dtype, kv_dtype, items, sms, &pk, &pv, s2);
+    }
+    if (s2 != s) {  // join, even after a failed launch, so that the caller's stream stays ordered
+      if (cudaEventRecord(side->join, s2) != cudaSuccess || cudaStreamWaitEvent(s, side->join, 0) != cudaSuccess)
+        e = cudaErrorUnknown;
+    }
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
-  if (L.parts > 1 || L.parts_pf > 1) {
+  if (grid_dec > 1 && single) {
     TraceScope t(16, s);
-    e = pa::launch_diff_merge(p, q_dtype, s);
+    e = pa::launch_diff_merge(p, q_dtype, 1, grid_dec, s);
+  }
+  if (e == cudaSuccess && grid_pf > 1 && multi) {
+    TraceScope t(16, s);
+    e = pa::launch_diff_merge(p, q_dtype, 0, grid_pf, s);
   }
   return cuda_status(e);
 }

@@ -428,12 +428,20 @@ __device__ RequestPlan plan_request(const AttnParams& p, int r, int tile_tokens)
     rp.origin = window_origin(p, rp.seq_len, rp.q_len);
     rp.parts = ceil_div_dev(rp.seq_len - rp.origin, rp.part);
     if (rp.q_len > 1) {
-      for (int t0 = 0; t0 < rp.q_len; t0 += tile_tokens) {
-        const int np = tile_partitions(p, rp, t0, tile_tokens);
-        if (np > 0) {
-          rp.full_tiles += np - 1;
-          rp.last_tiles += 1;
-        }
+      // Row tiles reach further from one to the next, so the sum over tiles of the whole partitions
+      // before a tile's last one is also the sum over partitions of the tiles that reach past them.
+      const int tiles = ceil_div_dev(rp.q_len, tile_tokens);
+      const int base = rp.seq_len - rp.q_len - rp.origin;
+      if (!p.causal) {
+        rp.full_tiles = tiles * (rp.parts - 1);
+        rp.last_tiles = tiles;
+      } else if (tiles <= rp.parts) {
+        for (int t0 = 0; t0 < rp.q_len; t0 += tile_tokens) rp.full_tiles += tile_partitions(p, rp, t0, tile_tokens) - 1;
+        rp.last_tiles = tiles;
+      } else {
+        for (int z = 1; z < rp.parts; ++z)  // tiles whose keys reach past z partitions
+          rp.full_tiles += tiles - max(0, z * rp.part - base) / tile_tokens;
+        rp.last_tiles = tiles;
       }
     }
   }
@@ -452,7 +460,8 @@ __global__ void __launch_bounds__(1024)
                        int32_t* plan_ok, int max_work, int tile_tokens) {
   __shared__ int warp_tot[3][32];
   __shared__ int carry[3];
-  __shared__ int bad, full_total;
+  __shared__ int bad, full_total, num_listed;
+  __shared__ int3 listed[1024];  // requests of a batch with tiles: (request, first whole tile's place, first last tile's)
   const int tid = threadIdx.x;
   const int lane = tid & 31, wid = tid >> 5, nw = blockDim.x >> 5;
   if (tid == 0) {
@@ -510,22 +519,31 @@ __global__ void __launch_bounds__(1024)
     __syncthreads();
     int ex[3];
     for (int k = 0; k < 3; ++k) ex[k] = carry[k] + (wid ? warp_tot[k][wid - 1] : 0) + sc[k] - v[k];
+    if (tid == 0) num_listed = 0;
+    __syncthreads();
     if (r < p.num_seqs) {
       part_off[r] = ex[0];
-      if (rp.full_tiles + rp.last_tiles) {
-        int kf = ex[1], kl = full_total + ex[2];
-        const int row0 = p.query_start_loc[r];
-        // partition-major: the row tiles that read one partition are listed (and so
-        // claimed) one after another, and read its K/V from L2 while it is there
-        const int last_t0 = (rp.q_len - 1) / tile_tokens * tile_tokens;
-        const int np_max = tile_partitions(p, rp, last_t0, tile_tokens);  // the most any row tile has
-        for (int z = 0; z < np_max; ++z) {
-          for (int t0 = 0; t0 < rp.q_len; t0 += tile_tokens) {
-            const int np = tile_partitions(p, rp, t0, tile_tokens);
-            if (z >= np) continue;
-            const int k = z + 1 < np ? kf++ : kl++;
-            if (k < max_work) work[k] = make_int4(r, row0 + t0, z, 0);
-          }
+      if (rp.full_tiles + rp.last_tiles) listed[atomicAdd(&num_listed, 1)] = make_int3(r, ex[1], full_total + ex[2]);
+    }
+    __syncthreads();
+    // a warp writes a request's tiles, partition-major: the row tiles that read one partition are
+    // listed (and so claimed) one after another, and read its K/V from L2 while it is there
+    for (int q = wid; q < num_listed; q += nw) {
+      const int lr = listed[q].x;
+      int kf = listed[q].y, kl = listed[q].z;
+      const RequestPlan lp = plan_request(p, lr, tile_tokens);
+      const int row0 = p.query_start_loc[lr], tiles = ceil_div_dev(lp.q_len, tile_tokens);
+      const int np_max = tile_partitions(p, lp, (tiles - 1) * tile_tokens, tile_tokens);  // the most any row tile has
+      for (int z = 0; z < np_max; ++z) {
+        for (int tb = 0; tb < tiles; tb += 32) {
+          const int t0 = (tb + lane) * tile_tokens;
+          const int np = tb + lane < tiles ? tile_partitions(p, lp, t0, tile_tokens) : 0;
+          const unsigned whole = __ballot_sync(0xffffffffu, z + 1 < np), last = __ballot_sync(0xffffffffu, z + 1 == np);
+          const unsigned below = (1u << lane) - 1;
+          const int k = z + 1 < np ? kf + __popc(whole & below) : kl + __popc(last & below);
+          if (z < np && k < max_work) work[k] = make_int4(lr, row0 + t0, z, 0);
+          kf += __popc(whole);
+          kl += __popc(last);
         }
       }
     }

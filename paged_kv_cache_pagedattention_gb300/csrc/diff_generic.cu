@@ -160,20 +160,32 @@ __global__ void __launch_bounds__(128) diff_generic_kernel(const DiffParams p, i
   }
 }
 
+struct DiffMergeArgs {
+  DiffParams p;
+  int single;  // of a flattened batch: the single-token rows, an item a request; else the others, an item a row
+};
+
 // Rows with partial states: kWarps warps a head share its partitions.  Lane i sums elements
 // 64 k + 2 i and the next of both maps, every partition weighted by 2^(m_j - M) of its map.
 template <int QDT, int kWarps, int N>
-__global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_kernel(const DiffParams p) {
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_kernel(const DiffMergeArgs args) {
+  const DiffParams& p = args.p;
   const AttnParams& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = a.num_q_heads / 2, width = 2 * a.head_size;
   const long long item = kWarps == 1 ? (long long)blockIdx.x * 4 + warp : blockIdx.x;
   const int part = kWarps == 1 ? 0 : warp;  // this warp's place among its head's
   previous_done();
-  if (item >= (long long)a.num_rows * heads || plan_rejected(a)) return;
-  const int row = static_cast<int>(item / heads), head = static_cast<int>(item % heads);
+  if (item >= (long long)(args.single ? a.num_seqs : a.num_rows) * heads || plan_rejected(a)) return;
+  int row = static_cast<int>(item / heads);
+  const int head = static_cast<int>(item % heads);
+  if (args.single && a.query_start_loc) {
+    const int q0 = a.query_start_loc[row];
+    if (a.query_start_loc[row + 1] - q0 != 1) return;
+    row = q0;
+  }
   const RowInfo ri = row_info(a, row);
-  if (!ri.ok) return;
+  if (!ri.ok || (ri.q_len > 1) == (args.single != 0)) return;
   const int np = ri.parts_row;
   if (np <= 1) return;  // written by the attention kernel
   const long long base = row_partial_base(a, ri, row);
@@ -253,19 +265,25 @@ cudaError_t launch_generic_t(const DiffParams& p, int grid_z, int only_multi, cu
   return cudaGetLastError();
 }
 
+// Single-token rows may have many partitions: eight warps a head then.  Rows of chunks have few, and there are many of them.
 template <int QDT, int N>
-cudaError_t launch_merge_t(const DiffParams& p, cudaStream_t s) {
-  const long long items = (long long)p.a.num_rows * (p.a.num_q_heads / 2);
-  if (p.a.max_partitions > 16)
-    return launch_early(diff_merge_kernel<QDT, 8, N>, dim3(static_cast<unsigned>(items)), 256, 0, 1, p, s);
-  return launch_early(diff_merge_kernel<QDT, 1, N>, dim3(static_cast<unsigned>((items + 3) / 4)), 128, 0, 1, p, s);
+cudaError_t launch_merge_t(const DiffParams& p, int single, int partitions, cudaStream_t s) {
+  DiffMergeArgs args;
+  args.p = p;
+  args.single = single;
+  const long long items = (long long)(single ? p.a.num_seqs : p.a.num_rows) * (p.a.num_q_heads / 2);
+  if (partitions > 16)
+    return launch_early<DiffMergeArgs>(diff_merge_kernel<QDT, 8, N>, dim3(static_cast<unsigned>(items)), 256, 0, 1, args,
+                                       s);
+  return launch_early<DiffMergeArgs>(diff_merge_kernel<QDT, 1, N>, dim3(static_cast<unsigned>((items + 3) / 4)), 128, 0,
+                                     1, args, s);
 }
 
 template <int QDT>
-cudaError_t launch_merge_width(const DiffParams& p, cudaStream_t s) {
-  if (p.a.head_size <= 64) return launch_merge_t<QDT, 2>(p, s);
-  if (p.a.head_size <= 128) return launch_merge_t<QDT, 4>(p, s);
-  return launch_merge_t<QDT, 8>(p, s);
+cudaError_t launch_merge_width(const DiffParams& p, int single, int partitions, cudaStream_t s) {
+  if (p.a.head_size <= 64) return launch_merge_t<QDT, 2>(p, single, partitions, s);
+  if (p.a.head_size <= 128) return launch_merge_t<QDT, 4>(p, single, partitions, s);
+  return launch_merge_t<QDT, 8>(p, single, partitions, s);
 }
 
 }  // namespace
@@ -290,10 +308,10 @@ cudaError_t launch_diff_generic(const DiffParams& p, int q_dtype, int kv_dtype, 
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, cudaStream_t stream) {
-  if (q_dtype == PA_F32) return launch_merge_width<PA_F32>(p, stream);
-  if (q_dtype == PA_F16) return launch_merge_width<PA_F16>(p, stream);
-  if (q_dtype == PA_BF16) return launch_merge_width<PA_BF16>(p, stream);
+cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, int single, int partitions, cudaStream_t stream) {
+  if (q_dtype == PA_F32) return launch_merge_width<PA_F32>(p, single, partitions, stream);
+  if (q_dtype == PA_F16) return launch_merge_width<PA_F16>(p, single, partitions, stream);
+  if (q_dtype == PA_BF16) return launch_merge_width<PA_BF16>(p, single, partitions, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -40,8 +40,9 @@ template <int HEAD, int BS, bool F8>
 struct DiffTc {
   static constexpr int kTiles = HEAD == 128 ? 1 : 2;
   static constexpr bool kTurns = kTiles == 1;                // the two warpgroups take chunks in turn
-  static constexpr int kSBufs = kTurns ? 4 : 2;              // S / P buffers of a row tile, 64 TMEM columns each
-  static constexpr int kOCol = kSBufs * 64;
+  static constexpr int kSBufs = kTurns ? 3 : 2;              // S / P buffers of a row tile, 64 TMEM columns each
+  static constexpr int kQCol = kSBufs * 64;                  // one row tile: the map's queries, 64 columns
+  static constexpr int kOCol = kQCol + (kTurns ? 64 : 0);
   static constexpr int kWide = 2 * HEAD;
   static constexpr int kTileCols = kOCol + kWide;
   static constexpr int kCols = kTurns ? kWide / 2 : kWide;   // columns of O a thread finishes
@@ -50,20 +51,21 @@ struct DiffTc {
   static constexpr int kPiece = kChunk * 128;
   static constexpr int kKBytes = kPieces * kPiece;           // keys of a chunk
   static constexpr int kVBytes = 2 * kKBytes;                // values of a chunk
-  static constexpr int kKStages = F8 ? 2 : HEAD == 128 ? 3 : 6;
-  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 3 : 6;
+  static constexpr int kKStages = F8 ? 3 : HEAD == 128 ? 4 : 5;
+  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 3 : 5;
   static constexpr int kQPiece = kRows * 128;
   static constexpr int kQTile = kPieces * kQPiece;           // of one map
-  static constexpr int kKOff = kTiles * 2 * kQTile;
+  static constexpr int kKOff = kTurns ? 0 : kTiles * 2 * kQTile;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
   // FP8: codes land in staging rings, K [block][token][head_size bytes], V [half][block][token][..]
-  static constexpr int kStg = F8 ? 2 : 0;
+  static constexpr int kStg = F8 ? 3 : 0;
   static constexpr int kStgBlock = BS * HEAD;
   static constexpr int kStgTensor = kBlocks * kStgBlock;
   static constexpr int kStgKOff = kVOff + kVStages * kVBytes;
   static constexpr int kStgVOff = kStgKOff + kStg * kStgTensor;
-  static constexpr int kBarOff = kStgVOff + kStg * 2 * kStgTensor;
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 2 + kSoftWarps + 1 + 4 * kStg;
+  static constexpr int kTurnOff = kStgVOff + kStg * 2 * kStgTensor;  // 4 KB a softmax warp
+  static constexpr int kBarOff = kTurnOff + kSoftWarps * 4096;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 3 + kSoftWarps + 1 + 4 * kStg;
   static constexpr int kSmem = 1024 + kBarOff + 8 * kNumBars + 16;
   static constexpr int kProducers = F8 ? 1 : 2;              // FP8: 16 warps leave 128 registers a thread
   static constexpr int kProducer = kSoftWarps, kMma = kProducer + kProducers, kConvK = kMma + kTiles, kConvV = kConvK + 2;
@@ -98,14 +100,99 @@ __device__ __forceinline__ void widen_row(const uint8_t* srow, uint8_t* drow, in
   }
 }
 
-// 32 elements of an output row, 16-byte aligned.
+// A warp's 32 rows x 32 columns between "a row a thread" and memory, where rows are far apart: turned
+// through 4 KB of shared memory, so that memory is touched in whole lines.  `at` is the thread's row
+// in memory (its first column), `live` whether it is touched.
+__device__ __forceinline__ void rows_to_memory(uint8_t* turn, float* at, bool live, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  float4* t = reinterpret_cast<float4*>(turn);
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    t[lane * 8 + (q ^ (lane & 7))] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 3), q = lane & 7;
+    float* dst = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
+    if (dst) reinterpret_cast<float4*>(dst)[q] = t[row * 8 + (q ^ (row & 7))];
+  }
+}
+
+__device__ __forceinline__ void rows_from_memory(uint8_t* turn, const float* at, bool live, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  float4* t = reinterpret_cast<float4*>(turn);
+  float4 x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 3);
+    const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
+    x[k] = src ? reinterpret_cast<const float4*>(src)[lane & 7] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 3), q = lane & 7;
+    t[row * 8 + (q ^ (row & 7))] = x[k];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 y = t[lane * 8 + (q ^ (lane & 7))];
+    v[4 * q] = y.x;
+    v[4 * q + 1] = y.y;
+    v[4 * q + 2] = y.z;
+    v[4 * q + 3] = y.w;
+  }
+}
+
+// The same, rounded to 16-bit output elements.
 template <int QDT>
-__device__ __forceinline__ void store_row(typename Elem<QDT>::T* out, const float (&v)[32]) {
+__device__ __forceinline__ void rows_to_output(uint8_t* turn, typename Elem<QDT>::T* at, bool live, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  uint4* t = reinterpret_cast<uint4*>(turn);
+  __syncwarp();
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(out + 8 * q) =
+    t[lane * 4 + (q ^ ((lane >> 1) & 3))] =
         make_uint4(pack2<QDT>(v[8 * q], v[8 * q + 1]), pack2<QDT>(v[8 * q + 2], v[8 * q + 3]),
                    pack2<QDT>(v[8 * q + 4], v[8 * q + 5]), pack2<QDT>(v[8 * q + 6], v[8 * q + 7]));
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = 8 * k + (lane >> 2), q = lane & 3;
+    uint4* dst = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
+    if (dst) dst[q] = t[row * 4 + (q ^ ((row >> 1) & 3))];
+  }
+}
+
+// A query row as 16-bit words: as it is, or for FP8 caches times 2^shift, so that f16 holds it.
+template <int QDT, bool kCvt, int HEAD>
+__device__ __forceinline__ int load_query_row(const uint4* src, uint32_t (&w)[HEAD / 2]) {
+#pragma unroll
+  for (int c = 0; c < HEAD / 8; ++c) {
+    const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
+    w[4 * c] = v.x;
+    w[4 * c + 1] = v.y;
+    w[4 * c + 2] = v.z;
+    w[4 * c + 3] = v.w;
+  }
+  if constexpr (!kCvt) return 0;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < HEAD / 2; ++i) {
+    const float2 f = unpack2<QDT>(w[i]);
+    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  int ex = 0;
+  frexpf(top, &ex);
+  const int shift = max(-100, min(100, 15 - ex));
+#pragma unroll
+  for (int i = 0; i < HEAD / 2; ++i) {
+    const float2 f = unpack2<QDT>(w[i]);
+    w[i] = pack2<PA_F16>(ldexpf(f.x, shift), ldexpf(f.y, shift));
+  }
+  return shift;
 }
 
 // All 256 softmax threads.
@@ -145,7 +232,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   uint64_t* o_done = p_full + NT * SB;
   uint64_t* o_free = o_done + NT * SB;      // a map's O has been read
   uint64_t* v_zeroed = o_free + NT;         // map j's last values have their end zeroed (two row tiles)
-  uint64_t* m_post = v_zeroed + 2;          // softmax warp w has posted its rows' maxima
+  uint64_t* q_full = v_zeroed + 2;          // map 2's queries are in TMEM (one row tile)
+  uint64_t* m_post = q_full + 1;            // softmax warp w has posted its rows' maxima
   uint64_t* mma_fin = m_post + kSoftWarps;
   uint64_t* stgk_full = mma_fin + 1;
   uint64_t* stgk_empty = stgk_full + SG;
@@ -185,6 +273,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     for (int i = 0; i < NT; ++i) mbar_init(o_free + i, kTurns ? 2 * kRows : kRows);
     mbar_init(v_zeroed, kRows);
     mbar_init(v_zeroed + 1, kRows);
+    mbar_init(q_full, kRows);
     for (int i = 0; i < kSoftWarps; ++i) mbar_init(m_post + i, 1);
     mbar_init(mma_fin, NT);
     fence_mbar_init();
@@ -213,6 +302,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   int tch[NT] = {};  // a row tile's chunks of earlier tiles
   int maps_done = 0; // maps of earlier tiles: o_free's phases
   int tails = 0;     // earlier tiles with a tail chunk: v_zeroed's
+  int turns = 0;     // earlier tiles with chunks: q_full's
   int k_issued = 0, v_issued = 0;
   while (L < total) {
     const int lc = L < total_full ? L : L - total_full;
@@ -261,51 +351,39 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     const int row_tok = tile_row / gp, row_head = tile_row % gp;
     const bool row_valid = warp < kSoftWarps && row_tok < ntok && row_head < nh;
     const int row_pos = pos0 + row_tok;
-    if (warp < kSoftWarps) {
-#pragma unroll 1
-      for (int mp = kTurns ? wg : 0; mp < (kTurns ? wg + 1 : 2); ++mp) {
-        const uint4* src = row_valid ? reinterpret_cast<const uint4*>(
-                                           static_cast<const typename QE::T*>(p.q) +
-                                           ((long long)(row0 + row_tok) * p.num_q_heads + 2 * (h0 + row_head) + mp) * HEAD)
-                                     : nullptr;
-        uint8_t* dst = sQ + ((kTurns ? 0 : wg) * 2 + mp) * G::kQTile;
-        if constexpr (!kCvt) {
+    // map j's queries of this thread's row, to TMEM (one row tile) or to shared memory
+    const int last_ci = tch[0] + nch_t[0] - 1;  // map 1's last chunk
+    auto load_queries = [&](int mp) {
+      const uint4* src = row_valid ? reinterpret_cast<const uint4*>(
+                                         static_cast<const typename QE::T*>(p.q) +
+                                         ((long long)(row0 + row_tok) * p.num_q_heads + 2 * (h0 + row_head) + mp) * HEAD)
+                                   : nullptr;
+      uint32_t w[HEAD / 2];
+      const int shift = load_query_row<QDT, kCvt, HEAD>(src, w);
+      if constexpr (kCvt) s_shift[mp][tile_row] = static_cast<int8_t>(shift);
+      if constexpr (kTurns) {
+        // before map 2's are stored, map 1's products are done with theirs
+        if (mp == 1 && !mbar_wait_bounded(s_full + last_ci % SB, (last_ci / SB) & 1)) return false;
+        tc_fence_after();
+        const uint32_t at = tmem + G::kQCol + ((uint32_t)((warp & 3) * 32) << 16);
+        tmem_st32(at, w);
+        tmem_st32(at + 32, w + 32);
+        tmem_wait_st();
+      } else {
+        uint8_t* dst = sQ + (wg * 2 + mp) * G::kQTile;
 #pragma unroll
-          for (int c = 0; c < HEAD / 8; ++c) {
-            const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(row, c & 7)) = v;
-          }
-        } else {
-          float amax = 0.f;
-          for (int c = 0; c < HEAD / 8 && src; ++c) {
-            const uint4 v = src[c];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<QDT>(w[e]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          int ex = 0;
-          frexpf(amax, &ex);
-          const int shift = max(-100, min(100, 15 - ex));
-          s_shift[mp][tile_row] = static_cast<int8_t>(shift);
-#pragma unroll 4
-          for (int c = 0; c < HEAD / 8; ++c) {
-            const uint4 v = src ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<QDT>(w[e]);
-              h[e] = pack2<PA_F16>(ldexpf(f.x, shift), ldexpf(f.y, shift));
-            }
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(row, c & 7)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
-        }
+        for (int c = 0; c < HEAD / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * G::kQPiece + swz128(row, c & 7)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
       }
-      fence_proxy_async();
+      return true;
+    };
+    if (kTurns ? warp < 4 : warp < kSoftWarps) {
+      load_queries(0);
+      if constexpr (!kTurns) {
+        load_queries(1);
+        fence_proxy_async();
+      }
     }
     tc_fence_before();
     __syncthreads();  // the queries are in place; every role of the previous tile is done
@@ -430,7 +508,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         }
       }
     } else if (warp >= G::kMma && warp < G::kConvK) {
-      // ------------------------------------------------------------ MMA issuers, one warp a row tile
+      // ------------------------------------------------------------ MMA issuers, one thread a row tile
       // As soon as P(i) is written PV(i), then S(i + SB) into the buffer that PV(i) frees: a thread's
       // MMAs run in the order of their issue.
       const int t = NT == 1 ? 0 : warp - G::kMma;
@@ -439,86 +517,70 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
       const uint32_t fmt = ODT == PA_BF16 ? 1u : 0u;
       const uint32_t id_s = umma_idesc(kRows, kChunk, fmt, 0);
       const uint32_t id_o = umma_idesc(kRows, G::kWide, fmt, 1);
-      const uint64_t qd0 = umma_desc(smem_u32(sQ) + t * 2 * G::kQTile, 16, 1024);
       const uint64_t kd0 = umma_desc(smem_u32(sK), 16, 1024);
       const uint64_t vd0 = umma_desc(smem_u32(sV), BS * 128, 1024);
       const uint32_t tT = tmem + t * G::kTileCols;
       uint64_t* my_s_full = s_full + t * SB;
       uint64_t* my_p_full = p_full + t * SB;
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-      };
-      // the row tile's j-th chunk (of both maps): S(j) behind its keys; false where a wait gave up
-      auto issue_s = [&](int j) {
-        const int mp = j >= my_nch, gi = gch + (mp ? nch + j - my_nch : j);
-        if (!wait_all(k_full + gi % KST, (gi / KST) & 1)) return false;
-        tc_fence_after();
-        const uint64_t qd = qd0 + (uint64_t)(mp * G::kQTile >> 4);
-        const uint64_t kd = kd0 + (uint64_t)((gi % KST) * G::kKBytes >> 4);
-        const int buf = (tc + j) % SB;
-        if (elect_one()) {
+      if (elect_one()) {
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = mbar_wait_bounded(bar, parity); };
+        // chunks of a ring that this row tile does not read are released once they have landed
+        auto skip = [&](uint64_t* full, uint64_t* empty, int stages, int gi) {
+          if (wait(full + gi % stages, (gi / stages) & 1)) mbar_arrive(empty + gi % stages);
+        };
+        for (int mp = 0; ok && mp < 2; ++mp) {
+          const int g0 = gch + mp * nch, c0 = tc + mp * my_nch;
+          // chunk i's S behind its keys
+          auto issue_s = [&](int i) {
+            const int gi = g0 + i, buf = (c0 + i) % SB;
+            if (!wait(k_full + gi % KST, (gi / KST) & 1)) return;
+            tc_fence_after();
+            const uint64_t kd = kd0 + (uint64_t)((gi % KST) * G::kKBytes >> 4);
+            const uint64_t qd = umma_desc(smem_u32(sQ) + (t * 2 + mp) * G::kQTile, 16, 1024);
 #pragma unroll
-          for (int ks = 0; ks < HEAD / 16; ++ks) {
-            const uint32_t qo = ((ks >> 2) * G::kQPiece + (ks & 3) * 32) >> 4;
-            const uint32_t ko = ((ks >> 2) * G::kPiece + (ks & 3) * 32) >> 4;
-            umma(tT + buf * 64, qd + qo, kd + ko, id_s, ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < HEAD / 16; ++ks) {
+              const uint32_t ko = ((ks >> 2) * G::kPiece + (ks & 3) * 32) >> 4;
+              if constexpr (kTurns)
+                umma_tmem_a(tT + buf * 64, tmem + G::kQCol + ks * 8, kd + ko, id_s, ks > 0 ? 1u : 0u);
+              else
+                umma(tT + buf * 64, qd + (((ks >> 2) * G::kQPiece + (ks & 3) * 32) >> 4), kd + ko, id_s, ks > 0 ? 1u : 0u);
+            }
+            umma_commit(my_s_full + buf);
+            umma_commit(k_empty + gi % KST);
+            mbar_arrive(my_s_full + buf);  // passes on what k_full brought: the chunk's s_valid
+          };
+          if (kTurns && mp == 1 && my_nch > 0 && !wait(q_full, turns & 1)) break;
+          for (int i = 0; ok && i < SB && i < my_nch; ++i) issue_s(i);
+          for (int i = 0; ok && i < my_nch; ++i) {
+            const int gi = g0 + i, ci = c0 + i, buf = ci % SB;
+            // the last chunk's V is read only after the row tile that zeroes its end has done so
+            if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile && !wait(v_zeroed + mp, tails & 1)) break;
+            if (!wait(v_full + gi % VST, (gi / VST) & 1)) break;
+            // a map's first product overwrites O, which the map before it must have been read from
+            if (i == 0 && maps_done + mp > 0 && !wait(o_free + t, (maps_done + mp - 1) & 1)) break;
+            if (!wait(my_p_full + buf, (ci / SB) & 1)) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)((gi % VST) * G::kVBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < kChunk / 16; ++ks)
+              umma_tmem_a(tT + G::kOCol, tT + buf * 64 + ks * 8, vd + (uint64_t)(v_row_off<HEAD, BS>(16 * ks, 0) >> 4),
+                          id_o, (i > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(o_done + t * SB + buf);
+            umma_commit(v_empty + gi % VST);
+            if (i + SB < my_nch) issue_s(i + SB);
           }
-          umma_commit(my_s_full + buf);
-          umma_commit(k_empty + gi % KST);
-          mbar_arrive(my_s_full + buf);  // passes on what k_full brought: the chunk's s_valid
+          for (int i = my_nch; NT > 1 && ok && i < nch; ++i) {
+            skip(k_full, k_empty, KST, g0 + i);
+            if (ok) skip(v_full, v_empty, VST, g0 + i);
+          }
         }
-        __syncwarp();
-        return true;
-      };
-      // chunks of the rings that this row tile does not read are released once they have landed
-      auto skip = [&](uint64_t* full, uint64_t* empty, int stages, int gi) {
-        if (!wait_all(full + gi % stages, (gi / stages) & 1)) return false;
-        if (elect_one()) mbar_arrive(empty + gi % stages);
-        __syncwarp();
-        return true;
-      };
-      bool ok = true;
-      // S runs SB chunks ahead; keys behind a map's last chunk are skipped on the way
-      auto advance = [&](int j) {
-        ok = ok && issue_s(j);
-        if (NT > 1 && (j == my_nch - 1 || j == 2 * my_nch - 1))
-          for (int i = my_nch; ok && i < nch; ++i)
-            ok = skip(k_full, k_empty, KST, gch + (j >= my_nch ? nch : 0) + i);
-      };
-      if (NT > 1 && my_nch == 0)
-        for (int i = 0; ok && i < 2 * nch; ++i)
-          ok = skip(k_full, k_empty, KST, gch + i) && skip(v_full, v_empty, VST, gch + i);
-      for (int j = 0; ok && j < SB && j < 2 * my_nch; ++j) advance(j);
-      for (int j = 0; ok && j < 2 * my_nch; ++j) {
-        const int mp = j >= my_nch, i = mp ? j - my_nch : j;
-        const int gi = gch + mp * nch + i, ci = tc + j, buf = ci % SB;
-        // the last chunk's V is read only after the row tile that zeroes its end has written P
-        if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile &&
-            !(ok = wait_all(v_zeroed + mp, tails & 1)))
-          break;
-        if (!(ok = wait_all(my_p_full + buf, (ci / SB) & 1))) break;
-        if (!(ok = wait_all(v_full + gi % VST, (gi / VST) & 1))) break;
-        // a map's first product overwrites O, which the map before it must have been read from
-        if (i == 0 && (maps_done + mp) > 0 && !(ok = wait_all(o_free + t, (maps_done + mp - 1) & 1))) break;
-        tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)((gi % VST) * G::kVBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < kChunk / 16; ++ks)
-            umma_tmem_a(tT + G::kOCol, tT + buf * 64 + ks * 8, vd + (uint64_t)(v_row_off<HEAD, BS>(16 * ks, 0) >> 4),
-                        id_o, (i > 0 || ks > 0) ? 1u : 0u);
-          umma_commit(o_done + t * SB + buf);
-          umma_commit(v_empty + gi % VST);
+        if (!ok) {
+          flag_error(p.err, PA_ERRFLAG_TIMEOUT);
+          s_abort = 1;
         }
-        __syncwarp();
-        if (NT > 1 && i == my_nch - 1)
-          for (int q = my_nch; ok && q < nch; ++q) ok = skip(v_full, v_empty, VST, gch + mp * nch + q);
-        if (ok && j + SB < 2 * my_nch) advance(j + SB);
       }
-      if (!ok) {
-        if (lane == 0) flag_error(p.err, PA_ERRFLAG_TIMEOUT);
-        s_abort = 1;
-      }
+      __syncwarp();
     } else if (warp < kSoftWarps) {
       // ------------------------------------------------------------ softmax: a row a thread
       const int t = kTurns ? 0 : wg;
@@ -539,11 +601,11 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
       const int head = h0 + row_head;
       const long long pi = (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req + z;
       const int col0 = kTurns ? wg * G::kCols : 0;
+      uint8_t* turn = smem + G::kTurnOff + warp * 4096;
       bool fail = false;
 #pragma unroll 1
       for (int mp = 0; !fail && mp < 2; ++mp) {
-        const float c = kCvt ? ldexpf(p.scale * kLog2e * p.k_scale[(kvh + mp) * p.scale_stride], -s_shift[mp][tile_row])
-                             : p.scale * kLog2e;
+        const float unit = kCvt ? p.scale * kLog2e * p.k_scale[(kvh + mp) * p.scale_stride] : p.scale * kLog2e;
         float m = -INFINITY, l = 0.f;  // m: the row's maximum when this thread last saw it
 #pragma unroll 1
         for (int i = 0; i < my_nch; ++i) {
@@ -561,6 +623,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           tmem_ld32(tS + lane_base, sr);
           tmem_ld32(tS + 32 + lane_base, sr + 32);
           const int valid = s_valid[gi % kValidRing];
+          const float c = kCvt ? ldexpf(unit, -s_shift[mp][tile_row]) : unit;
           tmem_wait_ld();
           float sc[kChunk];
 #pragma unroll
@@ -658,8 +721,14 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(my_p_full + buf);
         }
-        // ---- the map's end: O is complete, the row's maximum and sum are joined
         const int cl = tc + (mp + 1) * my_nch - 1;  // the map's last chunk
+        // map 2's queries: by the warpgroup that is done with map 1's chunks first
+        if (kTurns && !fail && mp == 0 && my_nch > 0 && (cl & 1) != wg) {
+          fail = !__all_sync(0xffffffffu, load_queries(1));
+          tc_fence_before();
+          if (!fail) mbar_arrive(q_full);
+        }
+        // ---- the map's end: O is complete, the row's maximum and sum are joined
         if (!fail && my_nch > 0) {
           bool got = mbar_wait_bounded(my_o_done + cl % SB, (cl / SB) & 1);
           if (kTurns && (cl & 1) != wg) got = got && mbar_wait_bounded(m_post + (warp ^ 4), (cl >> 1) & 1);
@@ -689,6 +758,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         typename QE::T* out = static_cast<typename QE::T*>(p.out) +
                               ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
         const bool norm = mp == 1 && args.p.norm_weight != nullptr;
+        const bool keep = mp == 0 || !direct;  // fp32, to the workspace
 #pragma unroll 1
         for (int cb = 0; cb < G::kCols; cb += 32) {
           const float vs = kCvt ? p.v_scale[(kvh + (col0 + cb) / HEAD) * p.scale_stride] : 1.f;
@@ -704,15 +774,11 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
-          if (mp == 1 && direct && write) {
+          if (mp == 1 && __any_sync(0xffffffffu, write && direct)) {
+            float a1[32];
+            rows_from_memory(turn, ws - G::kWide + cb, write && direct, a1);  // map 1's
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 a = *reinterpret_cast<const float4*>(ws - G::kWide + cb + 4 * q);  // map 1's
-              v[4 * q] += a.x;
-              v[4 * q + 1] += a.y;
-              v[4 * q + 2] += a.z;
-              v[4 * q + 3] += a.w;
-            }
+            for (int j = 0; j < 32; ++j) v[j] += a1[j];
           }
           if (norm) {
 #pragma unroll
@@ -722,14 +788,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             }
             tmem_st32(tO + cb + lane_base, o);  // kept for the second look
           }
-          if (!write) continue;
-          if (mp == 0 || !direct) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(ws + cb + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          } else if (!norm) {
-            store_row<QDT>(out + cb, v);
-          }
+          if (__any_sync(0xffffffffu, write && keep)) rows_to_memory(turn, ws + cb, write && keep, v);
+          if (mp == 1 && !norm) rows_to_output<QDT>(turn, out + cb, write && direct, v);
         }
         if (write && !direct && (!kTurns || wg == 0)) p.ws_ml[at] = make_float2(m, l);
         if (norm) {
@@ -745,7 +805,6 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             uint32_t o[32];
             tmem_ld32(tO + cb + lane_base, o);
             tmem_wait_ld();
-            if (!write || !direct) continue;
             float v[32];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -753,7 +812,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(o[4 * q + e]) * (rn * w[e]);
             }
-            store_row<QDT>(out + cb, v);
+            rows_to_output<QDT>(turn, out + cb, write && direct, v);
           }
         }
         tc_fence_before();
@@ -768,6 +827,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     gch += 2 * nch;
     maps_done += 2;
     tails += tail_chunk;
+    turns += nch > 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) tch[t] += 2 * nch_t[t];
     if (tid == 0) s_next = atomicAdd(p.work_claim, 1);

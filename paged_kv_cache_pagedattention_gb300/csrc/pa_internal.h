@@ -241,7 +241,9 @@ struct DiffParams {
 
 cudaError_t launch_diff_generic(const DiffParams& p, int q_dtype, int kv_dtype, int grid_z, int only_multi_token,
                                 cudaStream_t stream);
-cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, cudaStream_t stream);
+// The partial states of single-token rows (`single`), or of the rows of multi-token requests, of at
+// most `partitions` partitions.
+cudaError_t launch_diff_merge(const DiffParams& p, int q_dtype, int single, int partitions, cudaStream_t stream);
 
 // Single-token rows on tensor cores; the maps' boxes are diff_decode_unit tokens of one head.
 bool diff_decode_supported(int q_dtype, int kv_dtype, int head_size, int block_size);
