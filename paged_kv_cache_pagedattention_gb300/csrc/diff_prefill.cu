@@ -101,9 +101,19 @@ __device__ __forceinline__ void widen_row(const uint8_t* srow, uint8_t* drow, in
 }
 
 // A warp's 32 rows x 32 columns between "a row a thread" and memory, where rows are far apart: turned
-// through 4 KB of shared memory, so that memory is touched in whole lines.  `at` is the thread's row
-// in memory (its first column), `live` whether it is touched.
-__device__ __forceinline__ void rows_to_memory(uint8_t* turn, float* at, bool live, const float (&v)[32]) {
+// through 4 KB of shared memory, so that memory is touched in whole lines.  In memory order lane l
+// touches rows 4 k + l / 8 (fp32; 16 bytes each) or 8 k + l / 4 (16-bit output), whose addresses it
+// takes once a map from the lanes that own the rows: nullptr where a row is not touched.
+template <int N, typename T>
+__device__ __forceinline__ void row_addresses(T* mine, bool live, T* (&at)[N]) {
+  const int lane = threadIdx.x & 31;
+  const unsigned long long x = reinterpret_cast<unsigned long long>(live ? mine : nullptr);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    at[k] = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, x, N == 8 ? 4 * k + (lane >> 3) : 8 * k + (lane >> 2)));
+}
+
+__device__ __forceinline__ void rows_to_memory(uint8_t* turn, float* const (&at)[8], int col, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   float4* t = reinterpret_cast<float4*>(turn);
   __syncwarp();
@@ -111,44 +121,48 @@ __device__ __forceinline__ void rows_to_memory(uint8_t* turn, float* at, bool li
   for (int q = 0; q < 8; ++q)
     t[lane * 8 + (q ^ (lane & 7))] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = 4 * k + (lane >> 3), q = lane & 7;
-    float* dst = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
-    if (dst) reinterpret_cast<float4*>(dst)[q] = t[row * 8 + (q ^ (row & 7))];
-  }
-}
-
-__device__ __forceinline__ void rows_from_memory(uint8_t* turn, const float* at, bool live, float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-  float4* t = reinterpret_cast<float4*>(turn);
   float4 x[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int row = 4 * k + (lane >> 3);
-    const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
-    x[k] = src ? reinterpret_cast<const float4*>(src)[lane & 7] : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[k] = t[row * 8 + ((lane & 7) ^ (row & 7))];
   }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (at[k]) reinterpret_cast<float4*>(at[k] + col)[lane & 7] = x[k];
+}
+
+// The loads and the turning apart, so that the next columns' loads are on their way meanwhile.
+__device__ __forceinline__ void load_rows(const float* const (&at)[8], int col, float4 (&x)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    x[k] = at[k] ? reinterpret_cast<const float4*>(at[k] + col)[lane & 7] : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+__device__ __forceinline__ void turn_rows(uint8_t* turn, const float4 (&x)[8], float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  float4* t = reinterpret_cast<float4*>(turn);
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int row = 4 * k + (lane >> 3), q = lane & 7;
-    t[row * 8 + (q ^ (row & 7))] = x[k];
+    const int row = 4 * k + (lane >> 3);
+    t[row * 8 + ((lane & 7) ^ (row & 7))] = x[k];
   }
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const float4 y = t[lane * 8 + (q ^ (lane & 7))];
-    v[4 * q] = y.x;
-    v[4 * q + 1] = y.y;
-    v[4 * q + 2] = y.z;
-    v[4 * q + 3] = y.w;
+    v[4 * q] += y.x;
+    v[4 * q + 1] += y.y;
+    v[4 * q + 2] += y.z;
+    v[4 * q + 3] += y.w;
   }
 }
 
-// The same, rounded to 16-bit output elements.
 template <int QDT>
-__device__ __forceinline__ void rows_to_output(uint8_t* turn, typename Elem<QDT>::T* at, bool live, const float (&v)[32]) {
+__device__ __forceinline__ void rows_to_output(uint8_t* turn, typename Elem<QDT>::T* const (&at)[4], int col,
+                                               const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   uint4* t = reinterpret_cast<uint4*>(turn);
   __syncwarp();
@@ -158,12 +172,15 @@ __device__ __forceinline__ void rows_to_output(uint8_t* turn, typename Elem<QDT>
         make_uint4(pack2<QDT>(v[8 * q], v[8 * q + 1]), pack2<QDT>(v[8 * q + 2], v[8 * q + 3]),
                    pack2<QDT>(v[8 * q + 4], v[8 * q + 5]), pack2<QDT>(v[8 * q + 6], v[8 * q + 7]));
   __syncwarp();
+  uint4 x[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int row = 8 * k + (lane >> 2), q = lane & 3;
-    uint4* dst = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? at : nullptr), row));
-    if (dst) dst[q] = t[row * 4 + (q ^ ((row >> 1) & 3))];
+    const int row = 8 * k + (lane >> 2);
+    x[k] = t[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (at[k]) reinterpret_cast<uint4*>(at[k] + col)[lane & 3] = x[k];
 }
 
 // A query row as 16-bit words: as it is, or for FP8 caches times 2^shift, so that f16 holds it.
@@ -532,10 +549,9 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         for (int mp = 0; ok && mp < 2; ++mp) {
           const int g0 = gch + mp * nch, c0 = tc + mp * my_nch;
           // chunk i's S behind its keys
+          auto wait_k = [&](int i) { return wait(k_full + (g0 + i) % KST, ((g0 + i) / KST) & 1); };
           auto issue_s = [&](int i) {
             const int gi = g0 + i, buf = (c0 + i) % SB;
-            if (!wait(k_full + gi % KST, (gi / KST) & 1)) return;
-            tc_fence_after();
             const uint64_t kd = kd0 + (uint64_t)((gi % KST) * G::kKBytes >> 4);
             const uint64_t qd = umma_desc(smem_u32(sQ) + (t * 2 + mp) * G::kQTile, 16, 1024);
 #pragma unroll
@@ -551,15 +567,25 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             mbar_arrive(my_s_full + buf);  // passes on what k_full brought: the chunk's s_valid
           };
           if (kTurns && mp == 1 && my_nch > 0 && !wait(q_full, turns & 1)) break;
-          for (int i = 0; ok && i < SB && i < my_nch; ++i) issue_s(i);
-          for (int i = 0; ok && i < my_nch; ++i) {
-            const int gi = g0 + i, ci = c0 + i, buf = ci % SB;
+          for (int i = 0; i < SB && i < my_nch && wait_k(i); ++i) {
+            tc_fence_after();
+            issue_s(i);
+          }
+          // The tensor core's queue is short: a wait hides behind the long products of PV(i), not behind
+          // the short ones of S.  So the next chunk's waits come between the two; the one for P(i + 1)
+          // too where S runs far enough ahead of it (one row tile: 962 -> 860 cycles a chunk).
+          auto ready = [&](int i) {
+            const int gi = g0 + i;
             // the last chunk's V is read only after the row tile that zeroes its end has done so
-            if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile && !wait(v_zeroed + mp, tails & 1)) break;
-            if (!wait(v_full + gi % VST, (gi / VST) & 1)) break;
-            // a map's first product overwrites O, which the map before it must have been read from
-            if (i == 0 && maps_done + mp > 0 && !wait(o_free + t, (maps_done + mp - 1) & 1)) break;
-            if (!wait(my_p_full + buf, (ci / SB) & 1)) break;
+            if (NT > 1 && tail_chunk && i == nch - 1 && t != zero_tile && !wait(v_zeroed + mp, tails & 1)) return false;
+            return wait(v_full + gi % VST, (gi / VST) & 1);
+          };
+          auto wait_p = [&](int i) { return wait(my_p_full + (c0 + i) % SB, ((c0 + i) / SB) & 1); };
+          // a map's first product overwrites O, which the map before it must have been read from
+          if (ok && my_nch > 0 && maps_done + mp > 0) wait(o_free + t, (maps_done + mp - 1) & 1);
+          ok = ok && (my_nch == 0 || (ready(0) && wait_p(0)));
+          for (int i = 0; ok && i < my_nch; ++i) {
+            const int gi = g0 + i, buf = (c0 + i) % SB;
             tc_fence_after();
             const uint64_t vd = vd0 + (uint64_t)((gi % VST) * G::kVBytes >> 4);
 #pragma unroll
@@ -568,7 +594,13 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
                           id_o, (i > 0 || ks > 0) ? 1u : 0u);
             umma_commit(o_done + t * SB + buf);
             umma_commit(v_empty + gi % VST);
+            const bool more = i + 1 < my_nch;
+            if (more && !ready(i + 1)) break;
+            if (i + SB < my_nch && !wait_k(i + SB)) break;
+            if (kTurns && more && !wait_p(i + 1)) break;
+            tc_fence_after();
             if (i + SB < my_nch) issue_s(i + SB);
+            if (!kTurns && more && !wait_p(i + 1)) break;
           }
           for (int i = my_nch; NT > 1 && ok && i < nch; ++i) {
             skip(k_full, k_empty, KST, g0 + i);
@@ -758,7 +790,17 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         typename QE::T* out = static_cast<typename QE::T*>(p.out) +
                               ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
         const bool norm = mp == 1 && args.p.norm_weight != nullptr;
-        const bool keep = mp == 0 || !direct;  // fp32, to the workspace
+        // fp32 rows to the workspace; map 1's of rows that end here from there
+        float* to[8];
+        const float* from[8];
+        const bool any_to = __any_sync(0xffffffffu, write && (mp == 0 || !direct));
+        const bool any_from = mp == 1 && __any_sync(0xffffffffu, write && direct);
+        row_addresses(ws, write && (mp == 0 || !direct), to);
+        row_addresses(static_cast<const float*>(ws - G::kWide), mp == 1 && write && direct, from);
+        typename QE::T* out_at[4];
+        row_addresses(out, write && direct, out_at);
+        float4 next[8];
+        if (any_from) load_rows(from, 0, next);
 #pragma unroll 1
         for (int cb = 0; cb < G::kCols; cb += 32) {
           const float vs = kCvt ? p.v_scale[(kvh + (col0 + cb) / HEAD) * p.scale_stride] : 1.f;
@@ -774,11 +816,9 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
-          if (mp == 1 && __any_sync(0xffffffffu, write && direct)) {
-            float a1[32];
-            rows_from_memory(turn, ws - G::kWide + cb, write && direct, a1);  // map 1's
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += a1[j];
+          if (any_from) {
+            turn_rows(turn, next, v);
+            if (cb + 32 < G::kCols) load_rows(from, cb + 32, next);
           }
           if (norm) {
 #pragma unroll
@@ -788,8 +828,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             }
             tmem_st32(tO + cb + lane_base, o);  // kept for the second look
           }
-          if (__any_sync(0xffffffffu, write && keep)) rows_to_memory(turn, ws + cb, write && keep, v);
-          if (mp == 1 && !norm) rows_to_output<QDT>(turn, out + cb, write && direct, v);
+          if (any_to) rows_to_memory(turn, to, cb, v);
+          if (any_from && !norm) rows_to_output<QDT>(turn, out_at, cb, v);
         }
         if (write && !direct && (!kTurns || wg == 0)) p.ws_ml[at] = make_float2(m, l);
         if (norm) {
@@ -812,7 +852,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(o[4 * q + e]) * (rn * w[e]);
             }
-            rows_to_output<QDT>(turn, out + cb, write && direct, v);
+            if (any_from) rows_to_output<QDT>(turn, out_at, cb, v);
           }
         }
         tc_fence_before();
