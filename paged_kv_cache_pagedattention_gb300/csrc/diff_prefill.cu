@@ -52,7 +52,7 @@ struct DiffTc {
   static constexpr int kKBytes = kPieces * kPiece;           // keys of a chunk
   static constexpr int kVBytes = 2 * kKBytes;                // values of a chunk
   static constexpr int kKStages = F8 ? 3 : HEAD == 128 ? 4 : 5;
-  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 3 : 5;
+  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 4 : 5;
   static constexpr int kQPiece = kRows * 128;
   static constexpr int kQTile = kPieces * kQPiece;           // of one map
   static constexpr int kKOff = kTurns ? 0 : kTiles * 2 * kQTile;
@@ -63,9 +63,9 @@ struct DiffTc {
   static constexpr int kStgTensor = kBlocks * kStgBlock;
   static constexpr int kStgKOff = kVOff + kVStages * kVBytes;
   static constexpr int kStgVOff = kStgKOff + kStg * kStgTensor;
-  static constexpr int kTurnOff = kStgVOff + kStg * 2 * kStgTensor;  // 4 KB a softmax warp
-  static constexpr int kBarOff = kTurnOff + kSoftWarps * 4096;
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 3 + kSoftWarps + 1 + 4 * kStg;
+  static constexpr int kTurnOff = kStgVOff + kStg * 2 * kStgTensor;  // 2 KB a softmax warp
+  static constexpr int kBarOff = kTurnOff + kSoftWarps * 2048;
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 3 + 1 + 4 * kStg;
   static constexpr int kSmem = 1024 + kBarOff + 8 * kNumBars + 16;
   static constexpr int kProducers = F8 ? 1 : 2;              // FP8: 16 warps leave 128 registers a thread
   static constexpr int kProducer = kSoftWarps, kMma = kProducer + kProducers, kConvK = kMma + kTiles, kConvV = kConvK + 2;
@@ -100,84 +100,87 @@ __device__ __forceinline__ void widen_row(const uint8_t* srow, uint8_t* drow, in
   }
 }
 
-// A warp's 32 rows x 32 columns between "a row a thread" and memory, where rows are far apart: turned
-// through 4 KB of shared memory, so that memory is touched in whole lines.  In memory order lane l
-// touches rows 4 k + l / 8 (fp32; 16 bytes each) or 8 k + l / 4 (16-bit output), whose addresses it
-// takes once a map from the lanes that own the rows: nullptr where a row is not touched.
-template <int N, typename T>
-__device__ __forceinline__ void row_addresses(T* mine, bool live, T* (&at)[N]) {
+// A warp's 32 rows between "a row a thread" and memory, where rows are far apart: turned through 2 KB
+// of shared memory (16 bytes of a row's 64 at a time, swizzled by row pairs), so that memory is touched
+// in whole sectors.  In memory order lane l touches rows 8 k + l / 4, whose addresses it takes once a
+// map from the lanes that own them: nullptr where a row is not touched.
+__device__ __forceinline__ int turn_at(int row, int q) { return row * 4 + (q ^ ((row >> 1) & 3)); }
+
+template <typename T>
+__device__ __forceinline__ void row_addresses(T* mine, bool live, T* (&at)[4]) {
   const int lane = threadIdx.x & 31;
   const unsigned long long x = reinterpret_cast<unsigned long long>(live ? mine : nullptr);
 #pragma unroll
-  for (int k = 0; k < N; ++k)
-    at[k] = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, x, N == 8 ? 4 * k + (lane >> 3) : 8 * k + (lane >> 2)));
+  for (int k = 0; k < 4; ++k)
+    at[k] = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, x, 8 * k + (lane >> 2)));
 }
 
-__device__ __forceinline__ void rows_to_memory(uint8_t* turn, float* const (&at)[8], int col, const float (&v)[32]) {
+// 64 bytes a row: 16 floats, or 32 elements of 16 bits.
+__device__ __forceinline__ void turn_out(uint4* t, const uint4 (&mine)[4], uint4 (&x)[4]) {
   const int lane = threadIdx.x & 31;
-  float4* t = reinterpret_cast<float4*>(turn);
   __syncwarp();
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    t[lane * 8 + (q ^ (lane & 7))] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  for (int q = 0; q < 4; ++q) t[turn_at(lane, q)] = mine[q];
   __syncwarp();
-  float4 x[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = 4 * k + (lane >> 3);
-    x[k] = t[row * 8 + ((lane & 7) ^ (row & 7))];
+  for (int k = 0; k < 4; ++k) x[k] = t[turn_at(8 * k + (lane >> 2), lane & 3)];
+}
+
+__device__ __forceinline__ void rows_to_memory(uint4* turn, float* const (&at)[4], int col, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 mine[4], x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* f = v + 16 * h + 4 * q;
+      mine[q] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    turn_out(turn, mine, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k]) reinterpret_cast<uint4*>(at[k] + col + 16 * h)[lane & 3] = x[k];
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (at[k]) reinterpret_cast<float4*>(at[k] + col)[lane & 7] = x[k];
 }
 
 // The loads and the turning apart, so that the next columns' loads are on their way meanwhile.
-__device__ __forceinline__ void load_rows(const float* const (&at)[8], int col, float4 (&x)[8]) {
+__device__ __forceinline__ void load_rows(const float* const (&at)[4], int col, uint4 (&x)[8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    x[k] = at[k] ? reinterpret_cast<const float4*>(at[k] + col)[lane & 7] : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[k] = at[k & 3] ? reinterpret_cast<const uint4*>(at[k & 3] + col + 16 * (k >> 2))[lane & 3] : make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void turn_rows(uint8_t* turn, const float4 (&x)[8], float (&v)[32]) {
+__device__ __forceinline__ void add_rows(uint4* t, const uint4 (&x)[8], float (&v)[32]) {
   const int lane = threadIdx.x & 31;
-  float4* t = reinterpret_cast<float4*>(turn);
-  __syncwarp();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = 4 * k + (lane >> 3);
-    t[row * 8 + ((lane & 7) ^ (row & 7))] = x[k];
-  }
-  __syncwarp();
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float4 y = t[lane * 8 + (q ^ (lane & 7))];
-    v[4 * q] += y.x;
-    v[4 * q + 1] += y.y;
-    v[4 * q + 2] += y.z;
-    v[4 * q + 3] += y.w;
+    for (int k = 0; k < 4; ++k) t[turn_at(8 * k + (lane >> 2), lane & 3)] = x[4 * h + k];
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 y = t[turn_at(lane, q)];
+      float* f = v + 16 * h + 4 * q;
+      f[0] += __uint_as_float(y.x);
+      f[1] += __uint_as_float(y.y);
+      f[2] += __uint_as_float(y.z);
+      f[3] += __uint_as_float(y.w);
+    }
   }
 }
 
 template <int QDT>
-__device__ __forceinline__ void rows_to_output(uint8_t* turn, typename Elem<QDT>::T* const (&at)[4], int col,
+__device__ __forceinline__ void rows_to_output(uint4* turn, typename Elem<QDT>::T* const (&at)[4], int col,
                                                const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
-  uint4* t = reinterpret_cast<uint4*>(turn);
-  __syncwarp();
+  uint4 mine[4], x[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    t[lane * 4 + (q ^ ((lane >> 1) & 3))] =
-        make_uint4(pack2<QDT>(v[8 * q], v[8 * q + 1]), pack2<QDT>(v[8 * q + 2], v[8 * q + 3]),
-                   pack2<QDT>(v[8 * q + 4], v[8 * q + 5]), pack2<QDT>(v[8 * q + 6], v[8 * q + 7]));
-  __syncwarp();
-  uint4 x[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = 8 * k + (lane >> 2);
-    x[k] = t[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
-  }
+    mine[q] = make_uint4(pack2<QDT>(v[8 * q], v[8 * q + 1]), pack2<QDT>(v[8 * q + 2], v[8 * q + 3]),
+                         pack2<QDT>(v[8 * q + 4], v[8 * q + 5]), pack2<QDT>(v[8 * q + 6], v[8 * q + 7]));
+  turn_out(turn, mine, x);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     if (at[k]) reinterpret_cast<uint4*>(at[k] + col)[lane & 3] = x[k];
@@ -210,6 +213,29 @@ __device__ __forceinline__ int load_query_row(const uint4* src, uint32_t (&w)[HE
     w[i] = pack2<PA_F16>(ldexpf(f.x, shift), ldexpf(f.y, shift));
   }
   return shift;
+}
+
+// A row's maximum handed from one warpgroup to the other: posted behind chunk `count` - 1, awaited
+// (all lanes of the warp, with a limit) until that chunk's is there.
+__device__ __forceinline__ void post(unsigned long long* at, int count, float m) {
+  asm volatile("st.volatile.shared.b64 [%0], %1;" ::"r"(smem_u32(at)),
+               "l"((unsigned long long)count << 32 | __float_as_uint(m))
+               : "memory");
+}
+
+__device__ __forceinline__ bool await_post(unsigned long long* at, int count, float& m) {
+  uint64_t since = 0;
+  for (int spins = 0;; ++spins) {
+    unsigned long long w;
+    asm volatile("ld.volatile.shared.b64 %0, [%1];" : "=l"(w) : "r"(smem_u32(at)) : "memory");
+    m = __uint_as_float(static_cast<unsigned>(w));
+    if (__all_sync(0xffffffffu, static_cast<int>(w >> 32) == count || count == 0)) return true;
+    if (spins >= 64 && spins % 64 == 0) {
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, now - since > 2000000000ull)) return false;
+    }
+  }
 }
 
 // All 256 softmax threads.
@@ -250,8 +276,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   uint64_t* o_free = o_done + NT * SB;      // a map's O has been read
   uint64_t* v_zeroed = o_free + NT;         // map j's last values have their end zeroed (two row tiles)
   uint64_t* q_full = v_zeroed + 2;          // map 2's queries are in TMEM (one row tile)
-  uint64_t* m_post = q_full + 1;            // softmax warp w has posted its rows' maxima
-  uint64_t* mma_fin = m_post + kSoftWarps;
+  uint64_t* mma_fin = q_full + 1;
   uint64_t* stgk_full = mma_fin + 1;
   uint64_t* stgk_empty = stgk_full + SG;
   uint64_t* stgv_full = stgk_empty + SG;
@@ -262,7 +287,10 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   __shared__ int s_next, s_abort;
   __shared__ int s_valid[kValidRing];       // bit b: block b of the chunk can be read
   __shared__ int s_fail[2];                 // a softmax warp gave up in map j
-  __shared__ float s_m[2][kRows], s_l[2][2][kRows], s_sq[2][kRows];
+  __shared__ float s_l[2][2][kRows], s_sq[2][kRows];
+  // a row's maximum behind a chunk, with the chunk's number behind it in the upper half: one word, so that
+  // it is read as soon as it is there
+  __shared__ unsigned long long s_post[2][kRows];
   __shared__ int8_t s_shift[2][NT * kRows];  // FP8 caches: map j's row times 2^shift fits f16
 
   if (tid == 0) {
@@ -291,11 +319,11 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     mbar_init(v_zeroed, kRows);
     mbar_init(v_zeroed + 1, kRows);
     mbar_init(q_full, kRows);
-    for (int i = 0; i < kSoftWarps; ++i) mbar_init(m_post + i, 1);
     mbar_init(mma_fin, NT);
     fence_mbar_init();
     s_abort = s_fail[0] = s_fail[1] = 0;
   }
+  if (tid < 2 * kRows) s_post[tid / kRows][tid % kRows] = 0;
   if (warp == G::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(512)
@@ -324,7 +352,10 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   while (L < total) {
     const int lc = L < total_full ? L : L - total_full;
     const int nc = L < total_full ? nfull : nwork - nfull;
-    const int x = (L < total_full ? 0 : nfull) + lc % nc, y = lc / nc;
+    // The list's last tiles run from a request's first rows to its last, whose keys are the most: they
+    // are claimed from the end on, all KV groups of a tile together, so that the short ones fill the
+    // tail (8,192 tokens: 723 -> 650 us).  Whole partitions are alike, and stay in their order.
+    const int at = lc / ny, y = lc % ny, x = L < total_full ? at : nfull + nc - 1 - at;
     const int4 item = p.work[x];
     const int r = item.x, row0 = item.y, z = item.z;
     const int g = y / num_groups, hg = y % num_groups, kvh = 2 * g;
@@ -633,7 +664,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
       const int head = h0 + row_head;
       const long long pi = (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req + z;
       const int col0 = kTurns ? wg * G::kCols : 0;
-      uint8_t* turn = smem + G::kTurnOff + warp * 4096;
+      uint4* turn = reinterpret_cast<uint4*>(smem + G::kTurnOff + warp * 2048);
+      const float lam = write && direct ? diff_lambda(args.p, qs + t0 + row_tok, head) : 0.f;
       bool fail = false;
 #pragma unroll 1
       for (int mp = 0; !fail && mp < 2; ++mp) {
@@ -682,19 +714,17 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           const float mx = max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7])) * c;
           float m_prev = m;  // the row's maximum before this chunk
           if constexpr (kTurns) {
-            // the other warpgroup's warp of the same rows posted it with the chunk before
-            if (ci > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(m_post + (warp ^ 4), ((ci - 1) >> 1) & 1))) {
+            // the other warpgroup posted it with the chunk before
+            if (!await_post(&s_post[wg ^ 1][row], ci, m_prev)) {
               fail = true;
               break;
             }
-            m_prev = i > 0 ? s_m[wg ^ 1][row] : -INFINITY;
+            if (i == 0) m_prev = -INFINITY;
           }
           const bool need = mx > m_prev + kRescaleSlack;
           const float nm = need ? fmaxf(m_prev, mx) : m_prev;
           if constexpr (kTurns) {
-            s_m[wg][row] = nm;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(m_post + warp);
+            post(&s_post[wg][row], ci + 1, nm);
           }
           if (nm != m) {
             l *= ex2_approx(m - nm);  // 0 while this thread's sum is
@@ -760,16 +790,33 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           tc_fence_before();
           if (!fail) mbar_arrive(q_full);
         }
-        // ---- the map's end: O is complete, the row's maximum and sum are joined
+        // ---- the map's end.  Where the rows go, and map 1's result for those that end here, are fetched
+        // while the last products run: fp32 rows go to the workspace, map 1's of rows that end here come
+        // from there
+        const long long at = pi * p.num_q_heads + 2 * head + mp;
+        float* ws = p.ws_acc + at * G::kWide + col0;
+        typename QE::T* out = static_cast<typename QE::T*>(p.out) +
+                              ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
+        const bool norm = mp == 1 && args.p.norm_weight != nullptr;
+        float* to[4];
+        const float* from[4];
+        typename QE::T* out_at[4];
+        const bool any_to = __any_sync(0xffffffffu, write && (mp == 0 || !direct));
+        const bool any_from = mp == 1 && __any_sync(0xffffffffu, write && direct);
+        row_addresses(ws, write && (mp == 0 || !direct), to);
+        row_addresses(static_cast<const float*>(ws - G::kWide), mp == 1 && write && direct, from);
+        row_addresses(out, write && direct, out_at);
+        uint4 next[8];
+        if (any_from) load_rows(from, 0, next);
+        // O is complete, the row's maximum and sum are joined
         if (!fail && my_nch > 0) {
-          bool got = mbar_wait_bounded(my_o_done + cl % SB, (cl / SB) & 1);
-          if (kTurns && (cl & 1) != wg) got = got && mbar_wait_bounded(m_post + (warp ^ 4), (cl >> 1) & 1);
-          fail = !__all_sync(0xffffffffu, got);
+          fail = !__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + cl % SB, (cl / SB) & 1));
           tc_fence_after();
         }
         if constexpr (kTurns) {
           if (!fail && my_nch > 0) {
-            const float last = s_m[cl & 1][row];
+            float last = m;
+            fail = !await_post(&s_post[cl & 1][row], cl + 1, last);
             if (last != m) {
               l *= ex2_approx(m - last);
               m = last;
@@ -782,25 +829,9 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           l = s_l[mp][0][row] + s_l[mp][1][row];
         }
         if (fail) break;
-        const long long at = pi * p.num_q_heads + 2 * head + mp;
-        float* ws = p.ws_acc + at * G::kWide + col0;
         float weight = diff_weight(l);
-        if (mp == 1 && write && direct) weight *= -diff_lambda(args.p, qs + t0 + row_tok, head);
+        if (mp == 1) weight *= -lam;
         float sq = 0.f;
-        typename QE::T* out = static_cast<typename QE::T*>(p.out) +
-                              ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
-        const bool norm = mp == 1 && args.p.norm_weight != nullptr;
-        // fp32 rows to the workspace; map 1's of rows that end here from there
-        float* to[8];
-        const float* from[8];
-        const bool any_to = __any_sync(0xffffffffu, write && (mp == 0 || !direct));
-        const bool any_from = mp == 1 && __any_sync(0xffffffffu, write && direct);
-        row_addresses(ws, write && (mp == 0 || !direct), to);
-        row_addresses(static_cast<const float*>(ws - G::kWide), mp == 1 && write && direct, from);
-        typename QE::T* out_at[4];
-        row_addresses(out, write && direct, out_at);
-        float4 next[8];
-        if (any_from) load_rows(from, 0, next);
 #pragma unroll 1
         for (int cb = 0; cb < G::kCols; cb += 32) {
           const float vs = kCvt ? p.v_scale[(kvh + (col0 + cb) / HEAD) * p.scale_stride] : 1.f;
@@ -817,7 +848,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
           if (any_from) {
-            turn_rows(turn, next, v);
+            add_rows(turn, next, v);
             if (cb + 32 < G::kCols) load_rows(from, cb + 32, next);
           }
           if (norm) {
