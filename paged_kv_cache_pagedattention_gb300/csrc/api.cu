@@ -1502,7 +1502,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
     if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
     if (fast_prefill &&
         (!encode_cache_map(&pk, k_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, true) ||
-         !encode_cache_map(&pv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size)))
+         !encode_cache_map(&pv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, false,
+                           2 * block_size)))
       return PA_ERR_CUDA;
     std::unique_lock<std::mutex> lock(g_side_mutex, std::defer_lock);
     SideStream* side = nullptr;

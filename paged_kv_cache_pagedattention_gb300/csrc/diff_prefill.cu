@@ -13,8 +13,9 @@
 // At the end of map 1 its rows A_1 = O / l go to their place in the workspace (fp32); at the end of
 // map 2 the same threads take A_1 - lambda A_2, its norm, and write the result.  Rows whose keys lie
 // in several partitions leave both maps' partial states instead.
-// Warps: eight for the softmax, two TMA producers (K; V), one issuer of MMAs a row tile; for FP8
-// caches one producer and six that widen codes to f16.
+// Warps: eight for the softmax, TMA producers (one for each 128-byte piece of the keys, whose copies
+// are small where blocks are: one thread takes some 100 cycles a copy; one for the values), one
+// issuer of MMAs a row tile; for FP8 caches one producer and six that widen codes to f16.
 //
 // What bounds it is the softmax: a warp needs some 1,600 cycles from S(i) to P(i) by itself, the
 // products of a chunk 768.  With one row tile, two warps of each scheduler therefore take its
@@ -57,7 +58,7 @@ struct DiffTc {
   static constexpr int kQTile = kPieces * kQPiece;           // of one map
   static constexpr int kKOff = kTurns ? 0 : kTiles * 2 * kQTile;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
-  // FP8: codes land in staging rings, K [block][token][head_size bytes], V [half][block][token][..]
+  // FP8: codes land in staging rings, K [block][token][head_size bytes], V [block][half][token][..]
   static constexpr int kStg = F8 ? 3 : 0;
   static constexpr int kStgBlock = BS * HEAD;
   static constexpr int kStgTensor = kBlocks * kStgBlock;
@@ -67,7 +68,7 @@ struct DiffTc {
   static constexpr int kBarOff = kTurnOff + kSoftWarps * 2048;
   static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 3 * kSBufs * kTiles + kTiles + 3 + 1 + 4 * kStg;
   static constexpr int kSmem = 1024 + kBarOff + 8 * kNumBars + 16;
-  static constexpr int kProducers = F8 ? 1 : 2;              // FP8: 16 warps leave 128 registers a thread
+  static constexpr int kProducers = F8 ? 1 : kPieces + 1;    // FP8: 16 warps leave 128 registers a thread
   static constexpr int kProducer = kSoftWarps, kMma = kProducer + kProducers, kConvK = kMma + kTiles, kConvV = kConvK + 2;
   static constexpr int kThreads = (F8 ? kConvV + 4 : kConvK) * 32;
   static_assert(kBlocks * BS == kChunk, "block size must divide the chunk");
@@ -77,7 +78,15 @@ struct DiffTc {
   static_assert(kSBufs + kKStages + kStg < kValidRing, "a chunk's word outlives its stages");
 };
 
-// Byte offset, inside a chunk's V, of key `key`'s row in piece `pc` (the pieces of both halves).
+// A block's value tiles of both halves are one copy (the copies' number bounds small blocks: with two
+// of them a block of 16 tokens a chunk took 960 cycles, in blocks of 32 800), which lands as [128-byte
+// piece][half][token]: so piece pc of a chunk's V is piece pc / 2 of half pc % 2, and that is the order
+// of O's columns, 64 to a piece.
+__device__ __forceinline__ int value_column(int head, int c) {
+  return head == 128 ? ((c >> 6) & 1) * 128 + (c >> 7) * 64 + (c & 63) : c;
+}
+
+// Byte offset, inside a chunk's V, of key `key`'s row in piece `pc`.
 template <int HEAD, int BS>
 __device__ __forceinline__ uint32_t v_row_off(int key, int pc) {
   return (uint32_t)((key / BS) * (HEAD / 32) * BS * 128 + pc * BS * 128 + (key % BS) * 128);
@@ -238,6 +247,22 @@ __device__ __forceinline__ bool await_post(unsigned long long* at, int count, fl
   }
 }
 
+// Whether three barriers have passed their phases, without waiting.
+__device__ __forceinline__ bool mbar_test3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred x, y, z;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 x, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 y, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 z, [%5], %6;\n\t"
+      "and.pred x, x, y;\n\tand.pred x, x, z;\n\t"
+      "selp.u32 %0, 1, 0, x;\n\t}"
+      : "=r"(all)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc)
+      : "memory");
+  return all != 0;
+}
+
 // All 256 softmax threads.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -297,7 +322,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     tma_prefetch_desc(&args.tk);
     tma_prefetch_desc(&args.tv);
     for (int i = 0; i < KST; ++i) {
-      mbar_init(k_full + i, kCvt ? 64 : 1);
+      mbar_init(k_full + i, kCvt ? 64 : G::kPieces);
       mbar_init(k_empty + i, NT);
     }
     for (int i = 0; i < VST; ++i) {
@@ -440,7 +465,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
 
     if (warp >= G::kProducer && warp < G::kMma) {
       // ------------------------------------------------------------ TMA producers
-      const bool does_k = warp == G::kProducer, does_v = kCvt || warp != G::kProducer;
+      const int piece = warp - G::kProducer;  // of the keys
+      const bool does_v = kCvt || warp == G::kMma - 1, does_k = kCvt || !does_v;
       const int kb_end = (k1 + BS - 1) / BS;
       auto load_window = [&](int w) {
         const int kb = kb_first + 32 * w + lane;
@@ -472,7 +498,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             const int e = __shfl_sync(0xffffffffu, win, (i * NB + b) & 31);
             const bool in_range = kb_first + i * NB + b < kb_end;
             const bool ok_b = e >= 0 && e < p.num_blocks;
-            if (in_range && !ok_b && lane == 0 && does_k) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
+            if (in_range && !ok_b && lane == 0 && piece == 0) flag_error(p.err, PA_ERRFLAG_BLOCK_TABLE);
             phys[b] = in_range && ok_b ? e : p.num_blocks;
             valid |= (ok_b || !in_range) << b;
           }
@@ -481,18 +507,16 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             uint64_t* full = (kCvt ? stgk_full : k_full) + gi % RS;
             if (!(ok = free_stage(kCvt ? stgk_empty : k_empty, RS, gi))) break;
             if (elect_one()) {
-              s_valid[gi % kValidRing] = valid;
-              mbar_arrive_expect_tx(full, kCvt ? G::kStgTensor : G::kKBytes);
+              if (piece == 0) s_valid[gi % kValidRing] = valid;
+              mbar_arrive_expect_tx(full, kCvt ? G::kStgTensor : G::kPiece);
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
                 if constexpr (kCvt) {
                   tma_load_4d(sStgK + gi % RS * G::kStgTensor + b * G::kStgBlock, &args.tk, 0, (kvh + mp) * BS, 0, phys[b],
                               full);
                 } else {
-#pragma unroll
-                  for (int pc = 0; pc < G::kPieces; ++pc)
-                    tma_load_4d(sK + gi % RS * G::kKBytes + pc * G::kPiece + b * BS * 128, &args.tk, 0, (kvh + mp) * BS, pc,
-                                phys[b], full);
+                  tma_load_4d(sK + gi % RS * G::kKBytes + piece * G::kPiece + b * BS * 128, &args.tk, 0, (kvh + mp) * BS,
+                              piece, phys[b], full);
                 }
               }
             }
@@ -507,12 +531,9 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
               mbar_arrive_expect_tx(full, kCvt ? 2 * G::kStgTensor : G::kVBytes);
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint8_t* d = kCvt ? sStgV + (gi % RS * 2 + h) * G::kStgTensor + b * G::kStgBlock
-                                    : sV + gi % RS * G::kVBytes + v_row_off<HEAD, BS>(b * BS, h * G::kPieces);
-                  tma_load_4d(d, &args.tv, 0, (kvh + h) * BS, 0, phys[b], full);
-                }
+                uint8_t* d = kCvt ? sStgV + gi % RS * 2 * G::kStgTensor + b * 2 * G::kStgBlock
+                                  : sV + gi % RS * G::kVBytes + v_row_off<HEAD, BS>(b * BS, 0);
+                tma_load_4d(d, &args.tv, 0, kvh * BS, 0, phys[b], full);
               }
             }
             __syncwarp();
@@ -545,8 +566,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             break;
           }
           if (is_v)
-            widen_row<KVDT>(sStgV + (ss * 2 + half) * G::kStgTensor + blk * G::kStgBlock + tok * 128,
-                            sV + s * G::kVBytes + v_row_off<HEAD, BS>(key, half * G::kPieces), BS * 128, key & 7);
+            widen_row<KVDT>(sStgV + ss * 2 * G::kStgTensor + (blk * 2 + half) * G::kStgBlock + tok * 128,
+                            sV + s * G::kVBytes + v_row_off<HEAD, BS>(key, half), 2 * BS * 128, key & 7);
           else
             widen_row<KVDT>(sStgK + ss * G::kStgTensor + blk * G::kStgBlock + tok * 128, sK + s * G::kKBytes + key * 128,
                             G::kPiece, key & 7);
@@ -626,9 +647,21 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             umma_commit(o_done + t * SB + buf);
             umma_commit(v_empty + gi % VST);
             const bool more = i + 1 < my_nch;
-            if (more && !ready(i + 1)) break;
-            if (i + SB < my_nch && !wait_k(i + SB)) break;
-            if (kTurns && more && !wait_p(i + 1)) break;
+            if constexpr (kTurns) {
+              // all three looked at together: one trip to shared memory where they are there
+              if (i + SB < my_nch) {
+                const int gv = gi + 1, gk = gi + SB, cp = c0 + i + 1;
+                if (!mbar_test3(v_full + gv % VST, (gv / VST) & 1, k_full + gk % KST, (gk / KST) & 1,
+                                my_p_full + cp % SB, (cp / SB) & 1) &&
+                    !(ready(i + 1) && wait_k(i + SB) && wait_p(i + 1)))
+                  break;
+              } else if (more && !(ready(i + 1) && wait_p(i + 1))) {
+                break;
+              }
+            } else {
+              if (more && !ready(i + 1)) break;
+              if (i + SB < my_nch && !wait_k(i + SB)) break;
+            }
             tc_fence_after();
             if (i + SB < my_nch) issue_s(i + SB);
             if (!kTurns && more && !wait_p(i + 1)) break;
@@ -794,9 +827,9 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         // while the last products run: fp32 rows go to the workspace, map 1's of rows that end here come
         // from there
         const long long at = pi * p.num_q_heads + 2 * head + mp;
-        float* ws = p.ws_acc + at * G::kWide + col0;
+        float* ws = p.ws_acc + at * G::kWide;
         typename QE::T* out = static_cast<typename QE::T*>(p.out) +
-                              ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide + col0;
+                              ((long long)(qs + t0 + row_tok) * (p.num_q_heads / 2) + head) * G::kWide;
         const bool norm = mp == 1 && args.p.norm_weight != nullptr;
         float* to[4];
         const float* from[4];
@@ -807,7 +840,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         row_addresses(static_cast<const float*>(ws - G::kWide), mp == 1 && write && direct, from);
         row_addresses(out, write && direct, out_at);
         uint4 next[8];
-        if (any_from) load_rows(from, 0, next);
+        if (any_from) load_rows(from, value_column(HEAD, col0), next);
         // O is complete, the row's maximum and sum are joined
         if (!fail && my_nch > 0) {
           fail = !__all_sync(0xffffffffu, mbar_wait_bounded(my_o_done + cl % SB, (cl / SB) & 1));
@@ -834,7 +867,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
         float sq = 0.f;
 #pragma unroll 1
         for (int cb = 0; cb < G::kCols; cb += 32) {
-          const float vs = kCvt ? p.v_scale[(kvh + (col0 + cb) / HEAD) * p.scale_stride] : 1.f;
+          const int col = value_column(HEAD, col0 + cb);
+          const float vs = kCvt ? p.v_scale[(kvh + col / HEAD) * p.scale_stride] : 1.f;
           const float f = direct ? vs * weight : vs;
           uint32_t o[32];
           if (my_nch > 0) {
@@ -849,7 +883,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
           if (any_from) {
             add_rows(turn, next, v);
-            if (cb + 32 < G::kCols) load_rows(from, cb + 32, next);
+            if (cb + 32 < G::kCols) load_rows(from, value_column(HEAD, col0 + cb + 32), next);
           }
           if (norm) {
 #pragma unroll
@@ -859,8 +893,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             }
             tmem_st32(tO + cb + lane_base, o);  // kept for the second look
           }
-          if (any_to) rows_to_memory(turn, to, cb, v);
-          if (any_from && !norm) rows_to_output<QDT>(turn, out_at, cb, v);
+          if (any_to) rows_to_memory(turn, to, col, v);
+          if (any_from && !norm) rows_to_output<QDT>(turn, out_at, col, v);
         }
         if (write && !direct && (!kTurns || wg == 0)) p.ws_ml[at] = make_float2(m, l);
         if (norm) {
@@ -873,17 +907,18 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           tmem_wait_st();
 #pragma unroll 1
           for (int cb = 0; cb < G::kCols; cb += 32) {
+            const int col = value_column(HEAD, col0 + cb);
             uint32_t o[32];
             tmem_ld32(tO + cb + lane_base, o);
             tmem_wait_ld();
             float v[32];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const float* w = args.p.norm_weight + col0 + cb + 4 * q;
+              const float* w = args.p.norm_weight + col + 4 * q;
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(o[4 * q + e]) * (rn * w[e]);
             }
-            if (any_from) rows_to_output<QDT>(turn, out_at, cb, v);
+            if (any_from) rows_to_output<QDT>(turn, out_at, col, v);
           }
         }
         tc_fence_before();

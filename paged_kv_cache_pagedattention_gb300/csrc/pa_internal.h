@@ -251,7 +251,8 @@ int diff_decode_unit(int kv_dtype, int head_size, int block_size);
 cudaError_t launch_diff_decode(const DiffParams& p, int q_dtype, int kv_dtype, int grid_z, const CUtensorMap* tmap_k,
                                const CUtensorMap* tmap_v, cudaStream_t stream);
 
-// Multi-token rows on tcgen05 tiles, as launch_prefill_tc.  Work items hold diff_prefill_tile_tokens query tokens.
+// Multi-token rows on tcgen05 tiles, as launch_prefill_tc; tmap_k has one-piece boxes, tmap_v both
+// halves' tiles of a block.  Work items hold diff_prefill_tile_tokens query tokens.
 bool diff_prefill_supported(int q_dtype, int kv_dtype, int head_size, int block_size);
 int diff_prefill_tile_tokens(int group, int head_size);
 cudaError_t launch_diff_prefill(const DiffParams& p, int q_dtype, int kv_dtype, int num_items, int max_ctas,
