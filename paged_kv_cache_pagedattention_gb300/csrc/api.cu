@@ -522,6 +522,7 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
   if (!lambda || lambda_row_stride < 0 || lambda_head_stride < 0) return PA_ERR_INVALID_ARG;
   if (norm_weight && (!(norm_eps > 0.f) || !(norm_eps < INFINITY))) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(lambda, 4) || !aligned(norm_weight, 4)) return PA_ERR_INVALID_ARG;
+  if (num_q_heads / 2 > 65535 || (long long)rows * (num_q_heads / 2) > INT32_MAX) return PA_ERR_UNSUPPORTED;  // grids
   const int64_t most = INT64_MAX / 8;
   if (lambda_row_stride > most / rows || lambda_head_stride > most / num_q_heads) return PA_ERR_UNSUPPORTED;
   // a row's output over what another one still reads
@@ -534,6 +535,11 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
     return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
+
+// The generic kernel's partitions: its CTAs share a partition among eight warps, so short contexts
+// take one (4 fp32 sequences of 17 to 200 tokens: one launch instead of two).  No more of them than
+// the layout has room for.
+int generic_diff_partition(int part, int bs) { return std::max(part, round_up(256, std::max(part, bs))); }
 
 // Chunks of new tokens: partitions so long that the row tiles' states are few, but where there are
 // fewer tiles than SMs the context is split until there are some two items an SM (a chunk of 37
@@ -1270,7 +1276,7 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
   cudaError_t e;
   {
     TraceScope t(3, s);
-    e = pa::launch_varlen_plan(p, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
+    e = pa::launch_varlen_plan(p, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, false, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
   const bool fast_decode = pa::decode_mma_supported(q_dtype, kv_dtype, head_size, block_size, p.group);
@@ -1384,14 +1390,16 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.a.num_rows = num_seqs;
   p.a.max_query_len = 1;
-  p.a.part = p.a.part_pf = p.a.part_shared = L.part;
-  p.a.max_partitions = static_cast<int>(L.parts);
+  const bool fast = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
+  const int part = fast || partition_size > 0 ? L.part : generic_diff_partition(L.part, block_size);
+  p.a.part = p.a.part_pf = p.a.part_shared = part;
+  p.a.max_partitions = static_cast<int>(ceil_div(max_seq_len, part));
   p.a.ws_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.a.ws_acc = reinterpret_cast<float*>(ws + L.acc_off);
-  const int grid_z = window_partitions(L.parts, window, 1, block_size, L.part);
+  const int grid_z = window_partitions(p.a.max_partitions, window, 1, block_size, part);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size)) {
+  if (fast) {
     CUtensorMap tk, tv;
     if (!diff_decode_maps(&tk, &tv, p.a, kv_dtype)) return PA_ERR_CUDA;
     TraceScope t(15, s);
@@ -1461,14 +1469,17 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
   a.query_start_loc = query_start_loc;
   a.num_rows = total_q_tokens;
   a.max_query_len = max_query_len;
-  a.part = L.part;
-  a.part_pf = L.part_pf;
-  a.part_shared = L.part;
-  a.max_partitions = static_cast<int>(L.parts);
+  // One request of several tokens: no single-token rows.
+  const bool multi = max_query_len > 1, single = num_seqs > 1 || total_q_tokens == 1;
+  const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
+  const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
+  a.part = fast_decode || partition_size > 0 ? L.part : generic_diff_partition(L.part, block_size);
+  a.part_pf = fast_prefill || partition_size > 0 ? L.part_pf : generic_diff_partition(L.part_pf, block_size);
+  a.part_shared = a.part;
+  a.max_partitions = static_cast<int>(ceil_div(max_seq_len, a.part));
   a.causal = causal ? 1 : 0;
-  const int grid_dec = window_partitions(L.parts, window, 1, block_size, L.part);
-  const int grid_all = window_partitions(L.parts, window, max_query_len, block_size, L.part);
-  const int grid_pf = window_partitions(L.parts_pf, window, max_query_len, block_size, L.part_pf);
+  const int grid_dec = window_partitions(a.max_partitions, window, 1, block_size, a.part);
+  const int grid_pf = window_partitions(ceil_div(max_seq_len, a.part_pf), window, max_query_len, block_size, a.part_pf);
   int32_t* work_count = reinterpret_cast<int32_t*>(ws);
   a.plan_ok = reinterpret_cast<int32_t*>(ws + 4);
   a.work_claim = reinterpret_cast<int32_t*>(ws + 8);
@@ -1484,22 +1495,18 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
   cudaError_t e;
   {
     TraceScope t(3, s);
-    e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, s);
+    e = pa::launch_varlen_plan(a, part_off, work, work_count, static_cast<int>(L.max_work), tile_tokens, true, s);
   }
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  // One request of several tokens: no single-token rows.
-  const bool multi = max_query_len > 1, single = num_seqs > 1 || total_q_tokens == 1;
-  const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
-  const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
   if (!fast_decode) {
     TraceScope t(15, s);
-    e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_all, grid_pf), -1, s);
+    e = pa::launch_diff_generic(p, q_dtype, kv_dtype, std::max(grid_dec, grid_pf), -1, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
   } else {
     // Single-token rows (bound by memory) beside the tiles (bound by the tensor cores), as in
     // pa_varlen_attn: the tiles hold two thirds of the SMs first, and all of them once the rows end.
     CUtensorMap tk, tv, pk, pv;
-    if (!diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
+    if (single && !diff_decode_maps(&tk, &tv, a, kv_dtype)) return PA_ERR_CUDA;
     if (fast_prefill &&
         (!encode_cache_map(&pk, k_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, true) ||
          !encode_cache_map(&pv, v_cache, kv_dtype, num_blocks, num_kv_heads, block_size, head_size, false,

@@ -11,6 +11,7 @@
 // local maxima brought to the global maximum before adding); [LINEAGE]
 // "PagedAttention" (K/V read through the block table).
 #include "kv_rows.cuh"
+#include "launch.cuh"
 #include "pa_common.cuh"
 
 namespace pa {
@@ -455,9 +456,24 @@ __device__ RequestPlan plan_request(const AttnParams& p, int r, int tile_tokens)
 // whole partition (work_full of them), then each row tile's last, shorter one, so
 // that the persistent tile grids claim the long tiles first and the short ones fill
 // the tail.
-__global__ void __launch_bounds__(1024)
-    varlen_plan_kernel(const AttnParams p, int32_t* part_off, int4* work, int32_t* work_count,
-                       int32_t* plan_ok, int max_work, int tile_tokens) {
+struct PlanArgs {
+  AttnParams p;
+  int32_t* part_off;
+  int4* work;
+  int32_t* work_count;
+  int32_t* plan_ok;
+  int max_work, tile_tokens;
+};
+
+__global__ void __launch_bounds__(1024) varlen_plan_kernel(const PlanArgs args) {
+  const AttnParams& p = args.p;
+  int32_t* part_off = args.part_off;
+  int4* work = args.work;
+  int32_t *work_count = args.work_count, *plan_ok = args.plan_ok;
+  const int max_work = args.max_work, tile_tokens = args.tile_tokens;
+  // (both without effect but where this kernel, or the one behind it, is launched by launch_early)
+  next_may_start();
+  previous_done();
   __shared__ int warp_tot[3][32];
   __shared__ int carry[3];
   __shared__ int bad, full_total, num_listed;
@@ -612,10 +628,18 @@ cudaError_t launch_merge(const AttnParams& p, int q_dtype, cudaStream_t stream) 
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work,
-                               int32_t* work_count, int max_work, int tile_tokens, cudaStream_t stream) {
-  varlen_plan_kernel<<<1, 1024, 0, stream>>>(p, part_off, work, work_count,
-                                             const_cast<int32_t*>(p.plan_ok), max_work, tile_tokens);
+cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work, int32_t* work_count, int max_work,
+                               int tile_tokens, bool early, cudaStream_t stream) {
+  PlanArgs args;
+  args.p = p;
+  args.part_off = part_off;
+  args.work = work;
+  args.work_count = work_count;
+  args.plan_ok = const_cast<int32_t*>(p.plan_ok);
+  args.max_work = max_work;
+  args.tile_tokens = tile_tokens;
+  if (early) return launch_early<PlanArgs>(varlen_plan_kernel, dim3(1), 1024, 0, 1, args, stream);
+  varlen_plan_kernel<<<1, 1024, 0, stream>>>(args);
   return cudaGetLastError();
 }
 

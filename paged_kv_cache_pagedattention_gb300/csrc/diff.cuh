@@ -13,9 +13,6 @@
 
 namespace pa {
 
-constexpr int kDiffMaxHead = 256;
-constexpr int kDiffPairs = 2 * kDiffMaxHead / 64;  // pairs of output elements a lane holds, at most
-
 __device__ __forceinline__ float diff_lambda(const DiffParams& p, long long row, int head) {
   return p.lambda[row * p.lambda_row_stride + head * p.lambda_head_stride];
 }

@@ -1,5 +1,5 @@
 // Differential attention without matrix instructions, and the joining of partial states:
-//  * diff_generic_kernel -- one warp per (query row, head, partition), fp32 throughout: fp32 caches,
+//  * diff_generic_kernel -- one CTA per (query row, head, partition), fp32 throughout: fp32 caches,
 //    NVFP4 caches and every shape that the tensor-core kernels do not take;
 //  * diff_merge_kernel -- a row's partial states of both maps -> their difference, norm and output.
 #include "diff.cuh"
@@ -11,78 +11,145 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kGenericWarps = 8;
 
-// 32 keys at a time: lane j scores key j under both maps, then every lane adds the 32 value rows,
-// elements 64 k + 2 lane and the next of each, into both maps' sums: a value row is read once.
-template <int QDT, int KVDT>
-__global__ void __launch_bounds__(128) diff_generic_kernel(const DiffParams p, int only_multi_token) {
+struct DiffGenericArgs {
+  DiffParams p;
+  int only_multi_token;  // -1: every row; 0, 1: of single-token requests, of the others
+};
+
+// Element pairs of cached rows.
+template <int KVDT>
+__device__ __forceinline__ float2 kv_pair(const KvRow& r, int e) {
+  if constexpr (KVDT == PA_F32) {
+    return *reinterpret_cast<const float2*>(r.row + 4 * e);
+  } else if constexpr (KVDT == PA_F16 || KVDT == PA_BF16) {
+    return unpack2<KVDT>(*reinterpret_cast<const uint32_t*>(r.row + 2 * e));
+  } else {
+    return make_float2(kv_elem<KVDT>(r, e), kv_elem<KVDT>(r, e + 1));
+  }
+}
+
+// One CTA a (query row, head, partition); its eight warps deal the keys out in groups of kKeys.  Of a
+// group, eight lanes share a key's dot products, four keys at once; then lane i adds elements
+// 64 k + 2 i and the next of the value rows, which were fetched before the scores were known, to both
+// maps' sums.  The warps' states meet in shared memory, so that a context of one partition (256 tokens
+// at least) takes one launch.
+//
+// Latency is what bounds the calls that come here (4 fp32 sequences of 17 to 200 tokens: table, rows,
+// two sums over the warp): loads are in flight together, 64 registers of values a lane.
+template <int QDT, int KVDT, int N>
+__global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const DiffGenericArgs args) {
   using QE = Elem<QDT>;
+  constexpr int kKeys = 32 / N;
+  const DiffParams& p = args.p;
   const AttnParams& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = a.num_q_heads / 2, d = a.head_size, width = 2 * d;
-  const int head = blockIdx.y * 4 + warp;
-  const int row = blockIdx.x, z = blockIdx.z;
-  if (head >= heads || plan_rejected(a)) return;
+  const int head = blockIdx.y, row = blockIdx.x, z = blockIdx.z;
+  previous_done();
+  if (plan_rejected(a)) return;
   const RowInfo ri = row_info(a, row);
-  float2 acc[2][kDiffPairs];
-#pragma unroll
-  for (int k = 0; k < kDiffPairs; ++k) acc[0][k] = acc[1][k] = make_float2(0.f, 0.f);
   if (!ri.ok) {
     if (z == 0) {
       typename QE::T* out = static_cast<typename QE::T*>(a.out) + ((long long)row * heads + head) * width;
-      for (int i = lane; i < width; i += 32) out[i] = QE::from_float(0.f);
-      if (lane == 0 && a.query_start_loc == nullptr) flag_error(a.err, PA_ERRFLAG_SEQ_LEN);
+      for (int i = threadIdx.x; i < width; i += 32 * kGenericWarps) out[i] = QE::from_float(0.f);
+      if (threadIdx.x == 0 && a.query_start_loc == nullptr) flag_error(a.err, PA_ERRFLAG_SEQ_LEN);
     }
     return;
   }
-  if (a.query_start_loc != nullptr && only_multi_token >= 0 && (ri.q_len > 1) != (only_multi_token != 0)) return;
+  if (a.query_start_loc != nullptr && args.only_multi_token >= 0 && (ri.q_len > 1) != (args.only_multi_token != 0)) return;
   if (z >= ri.parts_row) return;
 
   const int kvh = head / a.group * 2;
-  const int t0 = ri.origin + z * ri.part, t1 = min(t0 + ri.part, ri.kv_len);
-  float c[2], vscale[2];
+  const int t0 = max(ri.origin + z * ri.part, ri.lo), t1 = min(ri.origin + (z + 1) * ri.part, ri.kv_len);
+  __shared__ float sq[2][64 * N];
+  __shared__ float red[kGenericWarps][2][64 * N];
+  __shared__ float2 red_ml[kGenericWarps][2];
+  const typename QE::T* qrow = static_cast<const typename QE::T*>(a.q) + ((long long)row * a.num_q_heads + 2 * head) * d;
+  for (int i = threadIdx.x; i < width; i += 32 * kGenericWarps) sq[i >= d][i >= d ? i - d : i] = QE::load(qrow + i);
+  __syncthreads();
+  float c[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    c[j] = a.scale * kLog2e;
-    vscale[j] = 1.f;
-    if (is_scaled<KVDT>()) {
-      c[j] *= a.k_scale[(kvh + j) * a.scale_stride];
-      vscale[j] = a.v_scale[(kvh + j) * a.scale_stride];
-    }
-  }
-  __shared__ float sq[4][2][kDiffMaxHead];
-  const typename QE::T* qrow =
-      static_cast<const typename QE::T*>(a.q) + ((long long)row * a.num_q_heads + 2 * head) * d;
-  for (int i = lane; i < width; i += 32) sq[warp][i / d][i % d] = QE::load(qrow + i);
-  __syncwarp();
+  for (int j = 0; j < 2; ++j)
+    c[j] = a.scale * kLog2e * (is_scaled<KVDT>() ? a.k_scale[(kvh + j) * a.scale_stride] : 1.f);
 
   const int32_t* table = a.block_tables + (long long)ri.request * a.max_blocks_per_seq;
+  const bool even = d % 2 == 0, quads = KVDT == PA_F32 && d % 4 == 0;
+  const int sub = lane & 7;  // this lane's place among the eight of a key
+  float2 acc[2][N];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  for (int tb = max(t0, ri.lo); tb < t1; tb += 32) {
-    const int tt = tb + lane, off = tt % a.block_size;
-    long long tile = -1;
+#pragma unroll
+  for (int k = 0; k < N; ++k) acc[0][k] = acc[1][k] = make_float2(0.f, 0.f);
+  for (int tb = t0 + warp * kKeys; tb < t1; tb += kGenericWarps * kKeys) {
+    // lane i of the first kKeys holds where key tb + i lies
+    const int mine = tb + lane;
+    long long my_tile = -1;
+    int my_off = 0;
+    if (lane < kKeys && mine < t1) {
+      const int phys = table[mine / a.block_size];
+      my_off = mine % a.block_size;
+      if (phys < 0 || phys >= a.num_blocks) flag_error(a.err, PA_ERRFLAG_BLOCK_TABLE);
+      else my_tile = (long long)phys * a.num_kv_heads + kvh;
+    }
+    // scores: s[j] of key tb + lane ends up in lane (of the first kKeys)
     float s[2] = {-INFINITY, -INFINITY};
-    if (tt < t1) {
-      const int phys = table[tt / a.block_size];
-      if (phys < 0 || phys >= a.num_blocks) {
-        flag_error(a.err, PA_ERRFLAG_BLOCK_TABLE);
-      } else {
-        tile = (long long)phys * a.num_kv_heads + kvh;
+#pragma unroll
+    for (int k0 = 0; k0 < kKeys; k0 += 4) {
+      const int key = k0 + (lane >> 3);
+      const long long tile = __shfl_sync(0xffffffffu, my_tile, key);
+      const int off = __shfl_sync(0xffffffffu, my_off, key);
+      float dot[2] = {0.f, 0.f};
+      if (tile >= 0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const KvRow kr = kv_row<KVDT>(a.k_cache, tile + j, a.block_size, d, off);
-          const float* q = sq[warp][j];
-          float dot[4] = {0.f, 0.f, 0.f, 0.f};
-          int dd = 0;
-          for (; dd + 32 <= d; dd += 32) {
-            float kv[32];
+          if (quads) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) kv[e] = kv_elem<KVDT>(kr, dd + e);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) dot[e & 3] = fmaf(q[dd + e], kv[e], dot[e & 3]);
+            for (int e = 0; e < 64 * N / 2; e += 32) {
+              if (e + 4 * sub < d) {
+                const float4 x = *reinterpret_cast<const float4*>(kr.row + 4 * (e + 4 * sub));
+                const float4 y = *reinterpret_cast<const float4*>(&sq[j][e + 4 * sub]);
+                dot[j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, dot[j]))));
+              }
+            }
+          } else if (even) {
+#pragma unroll 4
+            for (int e = 2 * sub; e < d; e += 16) {
+              const float2 x = kv_pair<KVDT>(kr, e);
+              dot[j] = fmaf(x.x, sq[j][e], fmaf(x.y, sq[j][e + 1], dot[j]));
+            }
+          } else {
+            for (int e = sub; e < d; e += 8) dot[j] = fmaf(kv_elem<KVDT>(kr, e), sq[j][e], dot[j]);
           }
-          for (; dd < d; ++dd) dot[0] = fmaf(q[dd], kv_elem<KVDT>(kr, dd), dot[0]);
-          s[j] = ((dot[0] + dot[1]) + (dot[2] + dot[3])) * c[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x = warp_sum_xor(dot[j], 1, 4);
+        const float got = __shfl_sync(0xffffffffu, x, (lane & 3) * 8);  // of key k0 + lane % 4
+        if ((lane & ~3) == k0 && my_tile >= 0) s[j] = got * c[j];
+      }
+    }
+    // the values, before the weights are known
+    float2 v[kKeys][N];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const long long tile = __shfl_sync(0xffffffffu, my_tile, i);
+      const int off = __shfl_sync(0xffffffffu, my_off, i);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int e = 64 * k + 2 * lane;
+        v[i][k] = make_float2(0.f, 0.f);
+        if (tile >= 0 && e < width) {
+          if (even) {
+            v[i][k] = kv_pair<KVDT>(kv_row<KVDT>(a.v_cache, tile + (e >= d), a.block_size, d, off), e >= d ? e - d : e);
+          } else {  // a pair may lie in both halves
+            const KvRow r0 = kv_row<KVDT>(a.v_cache, tile, a.block_size, d, off);
+            const KvRow r1 = kv_row<KVDT>(a.v_cache, tile + 1, a.block_size, d, off);
+            v[i][k].x = e < d ? kv_elem<KVDT>(r0, e) : kv_elem<KVDT>(r1, e - d);
+            v[i][k].y = e + 1 < d ? kv_elem<KVDT>(r0, e + 1) : kv_elem<KVDT>(r1, e + 1 - d);
+          }
         }
       }
     }
@@ -96,51 +163,64 @@ __global__ void __launch_bounds__(128) diff_generic_kernel(const DiffParams p, i
       l[j] = l[j] * alpha + warp_sum_xor(w[j], 1, 16);
       m[j] = top;
 #pragma unroll
-      for (int k = 0; k < kDiffPairs; ++k) {
+      for (int k = 0; k < N; ++k) {
         acc[j][k].x *= alpha;
         acc[j][k].y *= alpha;
       }
     }
-    const int n = min(32, t1 - tb);
-    const long long place = tile < 0 ? -1 : tile * a.block_size + off;  // of the first half's row
-    for (int i = 0; i < n; ++i) {
-      const float w0 = __shfl_sync(0xffffffffu, w[0], i), w1 = __shfl_sync(0xffffffffu, w[1], i);
-      const long long at = __shfl_sync(0xffffffffu, place, i);
-      if (at < 0) continue;  // an unreadable block, flagged above
-      const long long vt = at / a.block_size;
-      const int vo = static_cast<int>(at - vt * a.block_size);
-      const KvRow r0 = kv_row<KVDT>(a.v_cache, vt, a.block_size, d, vo);
-      const KvRow r1 = kv_row<KVDT>(a.v_cache, vt + 1, a.block_size, d, vo);
 #pragma unroll
-      for (int k = 0; k < kDiffPairs; ++k) {
-        const int e = 64 * k + 2 * lane;
-        if (e < width) {  // d is no multiple of 2 everywhere: each element by itself
-          const float x = e < d ? kv_elem<KVDT>(r0, e) : kv_elem<KVDT>(r1, e - d);
-          const float y = e + 1 < d ? kv_elem<KVDT>(r0, e + 1) : kv_elem<KVDT>(r1, e + 1 - d);
-          acc[0][k].x = fmaf(w0, x, acc[0][k].x);
-          acc[0][k].y = fmaf(w0, y, acc[0][k].y);
-          acc[1][k].x = fmaf(w1, x, acc[1][k].x);
-          acc[1][k].y = fmaf(w1, y, acc[1][k].y);
+    for (int i = 0; i < kKeys; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float f = __shfl_sync(0xffffffffu, w[j], i);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          acc[j][k].x = fmaf(f, v[i][k].x, acc[j][k].x);
+          acc[j][k].y = fmaf(f, v[i][k].y, acc[j][k].y);
         }
       }
     }
   }
-  if constexpr (is_scaled<KVDT>()) {
+  // ---- the warps' states; the first warp joins them
 #pragma unroll
-    for (int k = 0; k < kDiffPairs; ++k) {
-      const int e = 64 * k + 2 * lane;
-      const float x = vscale[e >= d], y = vscale[e + 1 >= d];
+  for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[j][k].x *= x;
-        acc[j][k].y *= y;
+    for (int k = 0; k < N; ++k) *reinterpret_cast<float2*>(&red[warp][j][64 * k + 2 * lane]) = acc[j][k];
+    if (lane == 0) red_ml[warp][j] = make_float2(m[j], l[j]);
+  }
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+    for (int v = 0; v < kGenericWarps; ++v) combine_ml(m[j], l[j], red_ml[v][j].x, red_ml[v][j].y);
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[j][k] = make_float2(0.f, 0.f);
+    for (int v = 0; v < kGenericWarps; ++v) {
+      const float2 ml = red_ml[v][j];
+      const float f = ml.y > 0.f ? exp2f(ml.x - m[j]) : 0.f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float2 x = *reinterpret_cast<const float2*>(&red[v][j][64 * k + 2 * lane]);
+        acc[j][k].x = fmaf(x.x, f, acc[j][k].x);
+        acc[j][k].y = fmaf(x.y, f, acc[j][k].y);
+      }
+    }
+    if constexpr (is_scaled<KVDT>()) {
+      const float vs[2] = {a.v_scale[kvh * a.scale_stride], a.v_scale[(kvh + 1) * a.scale_stride]};
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int e = 64 * k + 2 * lane;
+        acc[j][k].x *= vs[e >= d];
+        acc[j][k].y *= vs[e + 1 >= d];
       }
     }
   }
   if (ri.parts_row == 1) {
     const float w0 = diff_weight(l[0]), w1 = diff_weight(l[1]) * diff_lambda(p, row, head);
 #pragma unroll
-    for (int k = 0; k < kDiffPairs; ++k) {
+    for (int k = 0; k < N; ++k) {
       acc[0][k].x = acc[0][k].x * w0 - acc[1][k].x * w1;
       acc[0][k].y = acc[0][k].y * w0 - acc[1][k].y * w1;
     }
@@ -151,7 +231,7 @@ __global__ void __launch_bounds__(128) diff_generic_kernel(const DiffParams p, i
     for (int j = 0; j < 2; ++j) {
       float* wa = a.ws_acc + (pi * a.num_q_heads + 2 * head + j) * width;
 #pragma unroll
-      for (int k = 0; k < kDiffPairs; ++k) {
+      for (int k = 0; k < N; ++k) {
         const int e = 64 * k + 2 * lane;
         if (e < width) *reinterpret_cast<float2*>(wa + e) = acc[j][k];
       }
@@ -260,9 +340,14 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
 
 template <int QDT, int KVDT>
 cudaError_t launch_generic_t(const DiffParams& p, int grid_z, int only_multi, cudaStream_t s) {
-  const dim3 grid(p.a.num_rows, (p.a.num_q_heads / 2 + 3) / 4, grid_z);
-  diff_generic_kernel<QDT, KVDT><<<grid, 128, 0, s>>>(p, only_multi);
-  return cudaGetLastError();
+  DiffGenericArgs args;
+  args.p = p;
+  args.only_multi_token = only_multi;
+  const dim3 grid(p.a.num_rows, p.a.num_q_heads / 2, grid_z);
+  const int threads = 32 * kGenericWarps;
+  if (p.a.head_size <= 64) return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 2>, grid, threads, 0, 1, args, s);
+  if (p.a.head_size <= 128) return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 4>, grid, threads, 0, 1, args, s);
+  return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 8>, grid, threads, 0, 1, args, s);
 }
 
 // Single-token rows may have many partitions: eight warps a head then.  Rows of chunks have few, and there are many of them.

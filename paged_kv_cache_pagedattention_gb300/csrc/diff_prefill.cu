@@ -944,6 +944,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     if (s_abort) break;
   }
 
+  next_may_start();
   // ---- every MMA completes and every copy lands before TMEM is released and the CTA leaves
   if (warp >= G::kMma && warp < G::kConvK) {
     if (elect_one()) umma_commit(mma_fin);

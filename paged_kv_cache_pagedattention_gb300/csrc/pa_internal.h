@@ -211,8 +211,9 @@ cudaError_t launch_reshape_and_cache(const ScatterParams& p, int src_dtype, int 
 cudaError_t launch_attn_generic(const AttnParams& p, int q_dtype, int kv_dtype, int grid_z,
                                 int only_multi_token, cudaStream_t stream);
 cudaError_t launch_merge(const AttnParams& p, int q_dtype, cudaStream_t stream);
-cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work,
-                               int32_t* work_count, int max_work, int tile_tokens, cudaStream_t stream);
+// early: as launch_early launches.
+cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* work, int32_t* work_count, int max_work,
+                               int tile_tokens, bool early, cudaStream_t stream);
 
 bool decode_mma_supported(int q_dtype, int kv_dtype, int head_size, int block_size, int group);
 cudaError_t launch_decode_mma(const AttnParams& p, int q_dtype, int kv_dtype, int grid_z,
