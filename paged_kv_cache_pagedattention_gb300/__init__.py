@@ -695,52 +695,69 @@ def pa_diff_varlen_workspace_size(num_seqs, total_q_tokens, max_query_len, num_q
                                               head_size, max_seq_len, block_size, partition_size)
 
 
-def _diff_args(where, out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight, k_scale,
-               v_scale):
-    """Checks of a differential call's tensors; (rows, num_q_heads, geometry, lambda's strides, device)."""
-    if q.dim() != 3:
-        raise ValueError(f"{where}: q must be [rows][num_q_heads][head_size]")
+def _diff_bad(where, out, q, block_tables, seq_lens, lambda_, norm_weight, k_scale, v_scale, hkv):
+    """Refuse a differential call: what _diff_args found wrong, named."""
     t, hq, d = q.shape
-    nb, hkv, bs, head = cache_geometry(k_cache, v_cache, d)
-    if head != d or hq % 2 or hkv % 2 or out.shape != (t, hq // 2, 2 * d) or out.dtype is not q.dtype:
+    if hq % 2 or hkv % 2 or out.shape != (t, hq // 2, 2 * d) or out.dtype is not q.dtype:
         raise ValueError(f"{where}: q must be [rows][num_q_heads][head_size] and out [rows][num_q_heads/2]"
                          "[2*head_size] of one dtype, with even numbers of heads and the caches' head size")
-    b, dev = seq_lens.numel(), q.get_device()
     if seq_lens.dtype is not _int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
-        _bad(seq_lens, (b,), "seq_lens")
-    if block_tables.dtype is not _int32 or block_tables.dim() != 2 or block_tables.shape[0] != b or \
-            not block_tables.is_contiguous():
+        _bad(seq_lens, (seq_lens.numel(),), "seq_lens")
+    if block_tables.dtype is not _int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != seq_lens.numel() or not block_tables.is_contiguous():
         raise ValueError(f"{where}: block_tables must be a contiguous int32 tensor [num_seqs][max_blocks_per_seq]")
-    if lambda_.dtype is not _float32 or lambda_.dim() > 2:
+    if lambda_.dtype is not _float32:
         raise ValueError(f"{where}: lambda must be float32: a number, [heads] or [rows][heads]")
-    shape, strides = (1, 1) + lambda_.shape, (0, 0) + lambda_.stride()
-    if shape[-1] not in (1, hq // 2) or shape[-2] not in (1, t):
+    if norm_weight is not None and (norm_weight.dtype is not _float32 or norm_weight.shape != (2 * d,) or
+                                    not norm_weight.is_contiguous()):
+        raise ValueError(f"{where}: norm_weight must be a contiguous float32 tensor [2*head_size]")
+    raise ValueError(f"{where}: q, out, the caches and the workspace must be contiguous, and all tensors on one "
+                     "CUDA device")
+
+
+def _diff_args(where, out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight, k_scale,
+               v_scale):
+    """Checks of a differential call's tensors; (rows, num_q_heads, sequences, geometry, lambda's
+    strides, device)."""
+    shape, dev = q.shape, q.get_device()
+    if len(shape) != 3:
+        raise ValueError(f"{where}: q must be [rows][num_q_heads][head_size]")
+    t, hq, d = shape
+    nb, hkv, bs, head = cache_geometry(k_cache, v_cache, d)
+    lens, tables, lam = seq_lens.shape, block_tables.shape, lambda_.shape
+    if head != d or hq % 2 or hkv % 2 or out.shape != (t, hq // 2, 2 * d) or out.dtype is not q.dtype or \
+            len(lens) != 1 or len(tables) != 2 or tables[0] != lens[0] or seq_lens.dtype is not _int32 or \
+            block_tables.dtype is not _int32 or lambda_.dtype is not _float32 or \
+            not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and
+                 seq_lens.is_contiguous() and block_tables.is_contiguous() and workspace.is_contiguous()) or \
+            not (out.get_device() == k_cache.get_device() == v_cache.get_device() == block_tables.get_device() ==
+                 seq_lens.get_device() == lambda_.get_device() == workspace.get_device() == dev) or \
+            (norm_weight is not None and (norm_weight.dtype is not _float32 or norm_weight.shape != (2 * d,) or
+                                          not norm_weight.is_contiguous() or norm_weight.get_device() != dev)):
+        _diff_bad(where, out, q, block_tables, seq_lens, lambda_, norm_weight, k_scale, v_scale, hkv)
+    row_stride = head_stride = 0
+    n = len(lam)
+    if n == 1 or n == 2:
+        heads = lam[n - 1]
+        if heads != 1:
+            head_stride = lambda_.stride(n - 1)
+        if n == 2 and lam[0] != 1:
+            row_stride = lambda_.stride(0)
+        if (heads != 1 and heads != hq // 2) or (n == 2 and lam[0] != 1 and lam[0] != t):
+            raise ValueError(f"{where}: lambda must be a number, [heads] or [rows][heads]")
+    elif n:
         raise ValueError(f"{where}: lambda must be a number, [heads] or [rows][heads]")
-    row_stride = strides[-2] if shape[-2] > 1 else 0
-    head_stride = strides[-1] if shape[-1] > 1 else 0
-    others = [out, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace]
-    if norm_weight is not None:
-        if norm_weight.dtype is not _float32 or norm_weight.shape != (2 * d,) or not norm_weight.is_contiguous():
-            raise ValueError(f"{where}: norm_weight must be a contiguous float32 tensor [2*head_size]")
-        others.append(norm_weight)
-    for scale in (k_scale, v_scale):
-        if scale is not None:
-            if scale.dtype is not _float32 or scale.numel() not in (1, hkv) or not scale.is_contiguous():
-                raise ValueError(f"{where}: scales: float32, one per tensor or one per KV head")
-            others.append(scale)
-    if k_scale is not None and (v_scale is None or v_scale.numel() != k_scale.numel()):
-        raise ValueError(f"{where}: scales: float32, both one per tensor or both one per KV head")
-    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and
-            workspace.is_contiguous()):
-        raise ValueError(f"{where}: q, out, the caches and the workspace must be contiguous")
-    for x in others:
-        if x.get_device() != dev:
-            raise ValueError(f"{where}: all tensors must be on one CUDA device")
-    return t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
+    code = kv_code(k_cache, k_scale)
+    k_ptr = v_ptr = None
+    if code >= PA_FP8_E4M3 and (k_scale is not None or v_scale is not None):
+        if k_scale is None or v_scale is None or k_scale.dtype is not _float32 or v_scale.dtype is not _float32 or \
+                v_scale.numel() != k_scale.numel() or k_scale.numel() not in (1, hkv) or \
+                not (k_scale.is_contiguous() and v_scale.is_contiguous()) or \
+                not k_scale.get_device() == v_scale.get_device() == dev:
+            raise ValueError(f"{where}: scales: float32, both one per tensor or both one per KV head, on the caches' "
+                             "device")
+        k_ptr, v_ptr = k_scale.data_ptr(), v_scale.data_ptr()
+    return t, hq, lens[0], nb, hkv, bs, d, row_stride, head_stride, dev, code, k_ptr, v_ptr
 
 
 def pa_diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, scale, lambda_, workspace,
@@ -750,7 +767,7 @@ def pa_diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len
     lambda softmax(q[2h+1] K_2) V of q [B][Hq][d] on caches whose KV heads 2g, 2g+1 hold group g's
     two keys and its value's halves.  lambda_ float32: a number, [Hq/2] or [B][Hq/2] (any strides);
     norm_weight float32 [2d]: root-mean-square norm of every head.  See pa.h."""
-    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev = _diff_args(
+    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev, code, k_ptr, v_ptr = _diff_args(
         "pa_diff_decode", out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight, k_scale,
         v_scale)
     if t != b:
@@ -761,8 +778,8 @@ def pa_diff_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len
     st = _lib.pa_diff_decode(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), b, max_seq_len, hq, hkv, d, bs, scale, lambda_.data_ptr(),
-        row_stride, head_stride, _opt(norm_weight), norm_eps, window, dtype_code(q), kv_code(k_cache, k_scale),
-        _opt(k_scale), _opt(v_scale), partition_size, workspace.data_ptr(), workspace.nbytes,
+        row_stride, head_stride, None if norm_weight is None else norm_weight.data_ptr(), norm_eps, window,
+        dtype_code(q), code, k_ptr, v_ptr, partition_size, workspace.data_ptr(), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_diff_decode"))
     if st != PA_OK:
         raise PAError(st, "pa_diff_decode")
@@ -773,7 +790,7 @@ def pa_diff_varlen_attn(out, q, k_cache, v_cache, block_tables, query_start_loc,
                         v_scale=None, partition_size=0, stream=None, window=0) -> None:
     """Differential attention of a flattened varlen batch (pa_diff_decode's heads, lambda and norm;
     q [T][Hq][d], query_start_loc int32 [B+1]).  See pa.h."""
-    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev = _diff_args(
+    t, hq, b, nb, hkv, bs, d, row_stride, head_stride, dev, code, k_ptr, v_ptr = _diff_args(
         "pa_diff_varlen_attn", out, q, k_cache, v_cache, block_tables, seq_lens, lambda_, workspace, norm_weight,
         k_scale, v_scale)
     if query_start_loc.dtype is not _int32 or query_start_loc.shape != (b + 1,) or \
@@ -786,9 +803,9 @@ def pa_diff_varlen_attn(out, q, k_cache, v_cache, block_tables, query_start_loc,
     st = _lib.pa_diff_varlen_attn(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, block_tables.data_ptr(),
         block_tables.shape[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), b, t, max_query_len, max_seq_len, hq,
-        hkv, d, bs, scale, lambda_.data_ptr(), row_stride, head_stride, _opt(norm_weight), norm_eps, window,
-        1 if causal else 0, dtype_code(q), kv_code(k_cache, k_scale), _opt(k_scale), _opt(v_scale), partition_size,
-        workspace.data_ptr(), workspace.nbytes,
+        hkv, d, bs, scale, lambda_.data_ptr(), row_stride, head_stride,
+        None if norm_weight is None else norm_weight.data_ptr(), norm_eps, window, 1 if causal else 0, dtype_code(q),
+        code, k_ptr, v_ptr, partition_size, workspace.data_ptr(), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream_on(stream, dev, "pa_diff_varlen_attn"))
     if st != PA_OK:
         raise PAError(st, "pa_diff_varlen_attn")

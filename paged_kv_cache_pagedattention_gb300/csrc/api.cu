@@ -168,9 +168,9 @@ struct VarlenLayout {
 };
 
 VarlenLayout varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
-                           int requested, int tile_tokens, int part_pf = 0) {
+                           int requested, int tile_tokens, int part = 0, int part_pf = 0) {
   VarlenLayout L;
-  L.part = resolve_partition(requested, num_seqs, hkv, max_seq_len, bs);
+  L.part = resolve_partition(requested > 0 ? requested : part, num_seqs, hkv, max_seq_len, bs);
   L.part_pf = requested > 0 ? L.part : part_pf > 0 ? part_pf : prefill_partition(L.part);
   L.parts = ceil_div(max_seq_len, L.part);
   L.parts_pf = ceil_div(max_seq_len, L.part_pf);
@@ -536,6 +536,32 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
   return PA_OK;
 }
 
+// Single-token rows, `span` keys each at most: partitions for two waves of the decode kernel's CTAs
+// (three an SM) where the rows are few, and their lengths likely alike, else four, which even out
+// ragged rows (3 rows of 131,072 tokens, 12 units: 230 us with 1,024-token partitions, 3.4 waves, 220
+// with two waves; 64 rows of 512 to 4,096, 256 units: 103 us with four waves, 112 with two; 256 rows of
+// a 4,096-token window, 1,024 units: 352 with two partitions of which one is a block, 330 with two).
+int diff_partition(int num_seqs, int hq, int hkv, int span, int bs) {
+  const long long slots = 3LL * sm_count();
+  const long long units = std::max(1LL, (long long)num_seqs * (std::max(2, hkv) / 2) * ceil_div(std::max(1, hq / hkv), 8));
+  const long long parts = units <= slots / 8 ? 2 * slots / units : ceil_div(4 * slots, units);
+  return round_up(static_cast<int>(std::clamp(ceil_div(span, parts), 64LL, 1LL << 20)), bs);
+}
+
+DecodeLayout diff_decode_layout(int num_seqs, int hq, int hkv, int d, int max_seq_len, int bs, int requested) {
+  return decode_layout(num_seqs, hq, 2 * d, max_seq_len, bs, hkv / 2,
+                       requested > 0 ? requested : diff_partition(num_seqs, hq, hkv, max_seq_len, bs));
+}
+
+// The partition of a call whose layout has `part`: a window's keys are cut as finely as a whole
+// context's, into no more partitions than the layout has room for.
+int window_partition(int part, long long parts, int num_seqs, int hq, int hkv, int max_seq_len, int window, int bs) {
+  if (window <= 0) return part;
+  const int span = static_cast<int>(std::min<long long>(max_seq_len, (long long)window + bs - 1));
+  const int least = round_up(static_cast<int>(std::min(ceil_div(span, parts), 1LL << 20)), bs);
+  return std::min(part, std::max(diff_partition(num_seqs, hq, hkv, span, bs), least));
+}
+
 // The generic kernel's partitions: its CTAs share a partition among eight warps, so short contexts
 // take one (4 fp32 sequences of 17 to 200 tokens: one launch instead of two).  No more of them than
 // the layout has room for.
@@ -550,8 +576,9 @@ VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int hq, int hkv, int 
   const long long tiles = ceil_div(total_q, tile_tokens) * (std::max(2, hkv) / 2) * std::max(1LL, ceil_div(hq / hkv, 8));
   const long long parts = std::max(1LL, ceil_div(2 * sm_count(), tiles));
   const int least = round_up(64, bs);
-  const int part = std::min(round_up(16384, least), round_up(std::max(least, static_cast<int>(ceil_div(max_seq_len, parts))), least));
-  return varlen_layout(num_seqs, total_q, hq, hkv / 2, 2 * d, max_seq_len, bs, requested, tile_tokens, part);
+  const int part = round_up(static_cast<int>(std::min(16384LL, ceil_div(max_seq_len, parts))), least);
+  return varlen_layout(num_seqs, total_q, hq, hkv / 2, 2 * d, max_seq_len, bs, requested, tile_tokens,
+                       diff_partition(num_seqs, hq, hkv, max_seq_len, bs), part);
 }
 
 bool diff_decode_maps(CUtensorMap* tk, CUtensorMap* tv, const AttnParams& a, int kv_dtype) {
@@ -1354,7 +1381,8 @@ size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int3
                                      int32_t head_size, int32_t max_seq_len, int32_t block_size,
                                      int32_t partition_size) {
   if (num_seqs < 1 || num_q_heads < 1 || head_size < 1 || max_seq_len < 1 || block_size < 1) return 256;
-  return decode_layout(num_seqs, num_q_heads, 2 * head_size, max_seq_len, block_size, num_kv_heads / 2, partition_size)
+  return diff_decode_layout(num_seqs, num_q_heads, std::max(1, num_kv_heads), head_size, max_seq_len, block_size,
+                            partition_size)
       .total;
 }
 
@@ -1378,8 +1406,8 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
                          block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
-  const DecodeLayout L = decode_layout(num_seqs, num_q_heads, 2 * head_size, max_seq_len, block_size,
-                                       num_kv_heads / 2, partition_size);
+  const DecodeLayout L =
+      diff_decode_layout(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size, partition_size);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
   if (overlap(out, (size_t)num_seqs * num_q_heads * head_size * dtype_bytes(q_dtype), workspace, L.total))
     return PA_ERR_INVALID_ARG;
@@ -1391,12 +1419,14 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
   p.a.num_rows = num_seqs;
   p.a.max_query_len = 1;
   const bool fast = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
-  const int part = fast || partition_size > 0 ? L.part : generic_diff_partition(L.part, block_size);
+  const int part = partition_size > 0 ? L.part
+                   : fast ? window_partition(L.part, L.parts, num_seqs, num_q_heads, num_kv_heads, max_seq_len, window, block_size)
+                          : generic_diff_partition(L.part, block_size);
   p.a.part = p.a.part_pf = p.a.part_shared = part;
-  p.a.max_partitions = static_cast<int>(ceil_div(max_seq_len, part));
+  const int grid_z = window_partitions(ceil_div(max_seq_len, part), window, 1, block_size, part);
+  p.a.max_partitions = grid_z;
   p.a.ws_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.a.ws_acc = reinterpret_cast<float*>(ws + L.acc_off);
-  const int grid_z = window_partitions(p.a.max_partitions, window, 1, block_size, part);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (fast) {
@@ -1473,7 +1503,9 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
   const bool multi = max_query_len > 1, single = num_seqs > 1 || total_q_tokens == 1;
   const bool fast_decode = pa::diff_decode_supported(q_dtype, kv_dtype, head_size, block_size);
   const bool fast_prefill = multi && pa::diff_prefill_supported(q_dtype, kv_dtype, head_size, block_size);
-  a.part = fast_decode || partition_size > 0 ? L.part : generic_diff_partition(L.part, block_size);
+  a.part = partition_size > 0 ? L.part
+           : fast_decode ? window_partition(L.part, L.parts, num_seqs, num_q_heads, num_kv_heads, max_seq_len, window, block_size)
+                         : generic_diff_partition(L.part, block_size);
   a.part_pf = fast_prefill || partition_size > 0 ? L.part_pf : generic_diff_partition(L.part_pf, block_size);
   a.part_shared = a.part;
   a.max_partitions = static_cast<int>(ceil_div(max_seq_len, a.part));

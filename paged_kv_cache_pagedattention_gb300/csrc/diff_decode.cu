@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32) diff_decode_kernel(const __grid_c
       }
       diff_finish<QDT>(p, row, h, W, o[0]);
     } else {
+      if (n + kWarps >= nh) next_may_start();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const long long at = pi * a.num_q_heads + 2 * h + j;
