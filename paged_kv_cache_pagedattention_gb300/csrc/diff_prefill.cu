@@ -73,7 +73,7 @@ struct DiffTc {
   static constexpr int kThreads = (F8 ? kConvV + 4 : kConvK) * 32;
   static_assert(kBlocks * BS == kChunk, "block size must divide the chunk");
   static_assert(kTiles * kTileCols == 512, "TMEM columns");
-  static_assert(kSmem + 5 * 1024 <= 227 * 1024, "shared memory, with the static arrays");
+  static_assert(kSmem + 7 * 1024 <= 227 * 1024, "shared memory, with the static arrays");
   static_assert(!F8 || HEAD == 128, "FP8 rows are one 128-byte piece");
   static_assert(kSBufs + kKStages + kStg < kValidRing, "a chunk's word outlives its stages");
 };
@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
   __shared__ int s_valid[kValidRing];       // bit b: block b of the chunk can be read
   __shared__ int s_fail[2];                 // a softmax warp gave up in map j
   __shared__ float s_l[2][2][kRows], s_sq[2][kRows];
+  __shared__ float4 s_norm[G::kWide / 4];
   // a row's maximum behind a chunk, with the chunk's number behind it in the upper half: one word, so that
   // it is read as soon as it is there
   __shared__ unsigned long long s_post[2][kRows];
@@ -356,6 +357,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   previous_done();
+  if (args.p.norm_weight)
+    for (int i = tid; i < G::kWide; i += G::kThreads) reinterpret_cast<float*>(s_norm)[i] = args.p.norm_weight[i];
   const int num_groups = (p.group + 7) / 8;
   const int ny = p.num_kv_heads / 2 * num_groups;
   const bool rejected = plan_rejected(p);
@@ -885,7 +888,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             add_rows(turn, next, v);
             if (cb + 32 < G::kCols) load_rows(from, value_column(HEAD, col0 + cb + 32), next);
           }
-          if (norm) {
+          if (norm && any_from) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               sq = fmaf(v[j], v[j], sq);
@@ -906,7 +909,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           const float rn = rsqrtf(sq / G::kWide + args.p.norm_eps);
           tmem_wait_st();
 #pragma unroll 1
-          for (int cb = 0; cb < G::kCols; cb += 32) {
+          for (int cb = 0; any_from && cb < G::kCols; cb += 32) {
             const int col = value_column(HEAD, col0 + cb);
             uint32_t o[32];
             tmem_ld32(tO + cb + lane_base, o);
@@ -914,11 +917,13 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
             float v[32];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const float* w = args.p.norm_weight + col + 4 * q;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(o[4 * q + e]) * (rn * w[e]);
+              const float4 w = s_norm[col / 4 + q];
+              v[4 * q] = __uint_as_float(o[4 * q]) * (rn * w.x);
+              v[4 * q + 1] = __uint_as_float(o[4 * q + 1]) * (rn * w.y);
+              v[4 * q + 2] = __uint_as_float(o[4 * q + 2]) * (rn * w.z);
+              v[4 * q + 3] = __uint_as_float(o[4 * q + 3]) * (rn * w.w);
             }
-            if (any_from) rows_to_output<QDT>(turn, out_at, col, v);
+            rows_to_output<QDT>(turn, out_at, col, v);
           }
         }
         tc_fence_before();
