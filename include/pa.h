@@ -727,10 +727,14 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
  *   window         sliding window, as pa_decode_windowed and pa_varlen_attn_windowed (0: none)
  *   the rest, partitions, masks and errors as pa_decode and pa_varlen_attn.  out and q are 16-byte
  *   aligned; out must not overlap what is read (PA_ERR_INVALID_ARG).
- * Maps, difference and norm are fp32, rounded once (the tensor-core kernels round the maps' weights
- * to 16 bits for their product with V, as pa_decode does).  A map that attends nothing (all of a
- * row's entries out of range) is 0.  bf16 and f16 with head_size 64 or 128, and FP8 caches with
- * head_size 128, run on the tensor cores where block_size is 16, 32 or 64; the rest in fp32.
+ * Maps, difference and norm are fp32, rounded once (chunks on the tensor cores: the maps' weights
+ * are rounded to 16 bits for their product with V, as in pa_varlen_attn; single-token rows: to two
+ * 16-bit numbers, or for a bf16 output on an FP8 cache to one f16).  A map that attends nothing (all
+ * of a row's entries out of range) is 0.  Slots behind a sequence's tokens may hold anything; a
+ * sequence's own cached values are finite.  bf16 and f16 with head_size 64 or 128, and FP8 caches
+ * with head_size 128, run on the tensor cores where block_size is a multiple of 16 (chunks: 16, 32
+ * or 64); the rest, NVFP4 caches among it, in fp32 without them.  max_seq_len and partition_size up
+ * to 2^30, num_q_heads up to 131070.
  */
 size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t head_size, int32_t max_seq_len, int32_t block_size,
@@ -744,7 +748,8 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
                          const float* v_scale, int32_t partition_size, void* workspace, size_t workspace_bytes,
                          pa_stream_t stream);
 
-/* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together. */
+/* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together, at once
+ * on two streams (num_seqs > 1; as there, the first such call on a device comes before any capture). */
 size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                      int32_t max_seq_len, int32_t block_size, int32_t partition_size);

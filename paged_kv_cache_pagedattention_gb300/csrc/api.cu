@@ -513,8 +513,9 @@ bool rows_overlap(const void* a, int64_t a_width, const void* b, int64_t b_width
 
 // What the differential calls check beyond check_attention_args; `rows` of q and out.
 pa_status check_diff_args(const void* out, const void* q, const void* k_cache, const void* v_cache,
-                          int32_t num_blocks, int32_t rows, int32_t num_q_heads, int32_t num_kv_heads,
-                          int32_t head_size, int32_t block_size, float scale, const float* lambda,
+                          int32_t num_blocks, int32_t rows, int32_t max_seq_len, int32_t partition_size,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t block_size, float scale,
+                          const float* lambda,
                           int64_t lambda_row_stride, int64_t lambda_head_stride, const float* norm_weight,
                           float norm_eps, pa_dtype q_dtype, pa_dtype kv_dtype) {
   if (!(scale > 0.f) || !(scale < INFINITY)) return PA_ERR_INVALID_ARG;
@@ -522,6 +523,7 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
   if (!lambda || lambda_row_stride < 0 || lambda_head_stride < 0) return PA_ERR_INVALID_ARG;
   if (norm_weight && (!(norm_eps > 0.f) || !(norm_eps < INFINITY))) return PA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(lambda, 4) || !aligned(norm_weight, 4)) return PA_ERR_INVALID_ARG;
+  if (max_seq_len > kMostPages || partition_size > kMostPages) return PA_ERR_UNSUPPORTED;  // keys by 32-bit places
   if (num_q_heads / 2 > 65535 || (long long)rows * (num_q_heads / 2) > INT32_MAX) return PA_ERR_UNSUPPORTED;  // grids
   const int64_t most = INT64_MAX / 8;
   if (lambda_row_stride > most / rows || lambda_head_stride > most / num_q_heads) return PA_ERR_UNSUPPORTED;
@@ -569,7 +571,9 @@ int generic_diff_partition(int part, int bs) { return std::max(part, round_up(25
 
 // Chunks of new tokens: partitions so long that the row tiles' states are few, but where there are
 // fewer tiles than SMs the context is split until there are some two items an SM (a chunk of 37
-// tokens on 1,000: 47 us with one partition, 23 with 17).
+// tokens on 1,000, the call: 47 us with one partition, 33 with 17).  16,384 tokens at most: a mixed
+// step of chunks on up to 64K takes 1,589 us with them, 1,633 with 8,192 (more states), 1,729 with
+// 32,768 (the last items run alone).
 VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
                                 int requested) {
   const int tile_tokens = pa::diff_prefill_tile_tokens(hq / hkv, d);
@@ -1402,8 +1406,8 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
                                       seq_lens, max_seq_len, num_q_heads, num_kv_heads, head_size, block_size,
                                       q_dtype, kv_dtype, k_scale, v_scale, partition_size, workspace);
   if (st == PA_OK)
-    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, num_seqs, num_q_heads, num_kv_heads, head_size,
-                         block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
+    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, num_seqs, max_seq_len, partition_size, num_q_heads,
+                         num_kv_heads, head_size, block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
   const DecodeLayout L =
@@ -1478,8 +1482,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
                                       seq_lens, max_seq_len, num_q_heads, num_kv_heads, head_size, block_size,
                                       q_dtype, kv_dtype, k_scale, v_scale, partition_size, workspace);
   if (st == PA_OK)
-    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, total_q_tokens, num_q_heads, num_kv_heads, head_size,
-                         block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
+    st = check_diff_args(out, q, k_cache, v_cache, num_blocks, total_q_tokens, max_seq_len, partition_size, num_q_heads,
+                         num_kv_heads, head_size, block_size, scale, lambda, lambda_row_stride, lambda_head_stride, norm_weight, norm_eps,
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
   const int tile_tokens = pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size);

@@ -17,6 +17,12 @@ __device__ __forceinline__ float diff_lambda(const DiffParams& p, long long row,
   return p.lambda[row * p.lambda_row_stride + head * p.lambda_head_stride];
 }
 
+// A row whose keys and partial states have their places: row_info's checks, and no more tokens in its
+// request than the call was told of (the plan has flagged such a request and keeps no room for it).
+__device__ __forceinline__ bool diff_row_ok(const AttnParams& a, const RowInfo& ri) {
+  return ri.ok && ri.q_len <= a.max_query_len;
+}
+
 // A map's weight in the difference, with its sum divided out; 0 where the map attends nothing.
 __device__ __forceinline__ float diff_weight(float l) { return l > 0.f ? 1.f / l : 0.f; }
 

@@ -37,6 +37,10 @@ struct Geom {
   static constexpr int kTile = TOK * kRow;      // one head's unit of K or V
   static constexpr int kStage = 4 * kTile;      // K_1, K_2, V_1, V_2
   static constexpr int kStages = 2;
+  // Weights meet V as two 16-bit numbers, the second what the first leaves out, so that they are good to
+  // 2^-16 (bf16) or 2^-21 of themselves: memory bounds these rows, the second product is free.  The f16
+  // weights of an FP8 cache are far finer than a bf16 output already.
+  static constexpr bool kSplit = !(kFp8 && QDT == PA_BF16);
   static constexpr int kMTiles = TOK / 16, kSteps = HEAD / 16;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kRedRow = 2 * HEAD + 8;  // a state's row, off the banks of its neighbours
@@ -186,7 +190,7 @@ __device__ __forceinline__ void attend_unit(const uint8_t* stage, int rem, int l
   }
 
   // online softmax, fp32; the maximum is raised only past a slack (see kRescaleSlack)
-  uint32_t pb[NT][G::kMTiles][2];
+  uint32_t pb[NT][G::kMTiles][2], pr[NT][G::kMTiles][2];  // weights, and what they leave out
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float top[2] = {-INFINITY, -INFINITY};
@@ -217,16 +221,21 @@ __device__ __forceinline__ void attend_unit(const uint8_t* stage, int rem, int l
     const float u0 = w.m[t][0] == -INFINITY ? 0.f : w.m[t][0], u1 = w.m[t][1] == -INFINITY ? 0.f : w.m[t][1];
 #pragma unroll
     for (int mt = 0; mt < G::kMTiles; ++mt) {
-      const uint32_t x = pack2<MDT>(ex2_approx(fmaf(sc[t][mt][0], c[t][0], -u0)),
-                                    ex2_approx(fmaf(sc[t][mt][1], c[t][1], -u1)));
-      const uint32_t y = pack2<MDT>(ex2_approx(fmaf(sc[t][mt][2], c[t][0], -u0)),
-                                    ex2_approx(fmaf(sc[t][mt][3], c[t][1], -u1)));
-      // the sums are of the rounded weights that meet V
+      const float e0 = ex2_approx(fmaf(sc[t][mt][0], c[t][0], -u0)), e1 = ex2_approx(fmaf(sc[t][mt][1], c[t][1], -u1));
+      const float e2 = ex2_approx(fmaf(sc[t][mt][2], c[t][0], -u0)), e3 = ex2_approx(fmaf(sc[t][mt][3], c[t][1], -u1));
+      const uint32_t x = pack2<MDT>(e0, e1), y = pack2<MDT>(e2, e3);
       const float2 fx = unpack2<MDT>(x), fy = unpack2<MDT>(y);
-      w.l[t][0] += fx.x + fy.x;
-      w.l[t][1] += fx.y + fy.y;
       pb[t][mt][0] = movmatrix_trans(x);
       pb[t][mt][1] = movmatrix_trans(y);
+      if constexpr (G::kSplit) {
+        w.l[t][0] += e0 + e2;
+        w.l[t][1] += e1 + e3;
+        pr[t][mt][0] = movmatrix_trans(pack2<MDT>(e0 - fx.x, e1 - fx.y));
+        pr[t][mt][1] = movmatrix_trans(pack2<MDT>(e2 - fy.x, e3 - fy.y));
+      } else {  // the sums are of the rounded weights that meet V
+        w.l[t][0] += fx.x + fy.x;
+        w.l[t][1] += fx.y + fy.y;
+      }
     }
   }
 
@@ -254,8 +263,11 @@ __device__ __forceinline__ void attend_unit(const uint8_t* stage, int rem, int l
             a3 &= m89;
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t) {
             mma_16816<MDT>(w.acc[t][half * G::kSteps + dt], a0, a1, a2, a3, pb[t][kt][0], pb[t][kt][1]);
+            if constexpr (G::kSplit)
+              mma_16816<MDT>(w.acc[t][half * G::kSteps + dt], a0, a1, a2, a3, pr[t][kt][0], pr[t][kt][1]);
+          }
         }
       } else {
         // dims 16 (lane >> 2) .. + 15 of those tokens
@@ -286,6 +298,12 @@ __device__ __forceinline__ void attend_unit(const uint8_t* stage, int rem, int l
                               pb[t][kt][1]);
             mma_16816<PA_F16>(w.acc[t][half * G::kSteps + 2 * k + 1], c01[2], c01[3], c89[2], c89[3], pb[t][kt][0],
                               pb[t][kt][1]);
+            if constexpr (G::kSplit) {
+              mma_16816<PA_F16>(w.acc[t][half * G::kSteps + 2 * k], c01[0], c01[1], c89[0], c89[1], pr[t][kt][0],
+                                pr[t][kt][1]);
+              mma_16816<PA_F16>(w.acc[t][half * G::kSteps + 2 * k + 1], c01[2], c01[3], c89[2], c89[3], pr[t][kt][0],
+                                pr[t][kt][1]);
+            }
           }
         }
       }

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
   previous_done();
   if (plan_rejected(a)) return;
   const RowInfo ri = row_info(a, row);
-  if (!ri.ok) {
+  if (!diff_row_ok(a, ri)) {
     if (z == 0) {
       typename QE::T* out = static_cast<typename QE::T*>(a.out) + ((long long)row * heads + head) * width;
       for (int i = threadIdx.x; i < width; i += 32 * kGenericWarps) out[i] = QE::from_float(0.f);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
     row = q0;
   }
   const RowInfo ri = row_info(a, row);
-  if (!ri.ok || (ri.q_len > 1) == (args.single != 0)) return;
+  if (!diff_row_ok(a, ri) || (ri.q_len > 1) == (args.single != 0)) return;
   const int np = ri.parts_row;
   if (np <= 1) return;  // written by the attention kernel
   const long long base = row_partial_base(a, ri, row);

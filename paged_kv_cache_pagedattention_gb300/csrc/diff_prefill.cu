@@ -17,10 +17,22 @@
 // are small where blocks are: one thread takes some 100 cycles a copy; one for the values), one
 // issuer of MMAs a row tile; for FP8 caches one producer and six that widen codes to f16.
 //
-// What bounds it is the softmax: a warp needs some 1,600 cycles from S(i) to P(i) by itself, the
-// products of a chunk 768.  With one row tile, two warps of each scheduler therefore take its
-// chunks in turn (four S buffers), and hand the running maximum of a row from one to the other
-// through shared memory; with two row tiles each has its own four warps (two S buffers each).
+// The products of a chunk take 768 cycles, a softmax warp some 1,100 from S(i) to P(i).  With one row
+// tile, two warps of each scheduler therefore take its chunks in turn (three S buffers), and hand the
+// running maximum of a row from one to the other through shared memory; with two row tiles each has
+// its own four warps (two S buffers each), and the softmax is what bounds it.  With one row tile the
+// queries lie in tensor memory: from shared memory a product of S takes 49 cycles instead of 33 (its
+// rows are read 64 columns at a time), and what the ring's copies write there comes on top (1,293
+// cycles a chunk, 906 now in blocks of 16 tokens, 835 of 64).
+//
+// Measured (GB300, 32/8 heads of 128 bf16): 8,192 tokens 643 us, 1,280 TFLOP/s, at the card's power
+// limit (1,370 W, 1,957 MHz); of a tile's time 17 to 24% are the two ends of its maps, where the
+// tensor core waits: 128 KB of sums through 32 bytes a cycle.  An FP8 cache 880 TFLOP/s (widening),
+// head_size 64 950 TFLOP/s (softmax).
+//
+// P is rounded to 16 bits, as in every tile of this kind: an output is then off by 2.6 10^-3 of its
+// size where its own bf16 rounding is 1.7 10^-3 (f16: 3.2 10^-4 and 2.1 10^-4).  A second product with
+// what P leaves out, as single-token rows have it, would take a chunk from 768 to 1,280 cycles.
 #include <algorithm>
 
 #include "diff.cuh"
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     const int nc = L < total_full ? nfull : nwork - nfull;
     // The list's last tiles run from a request's first rows to its last, whose keys are the most: they
     // are claimed from the end on, all KV groups of a tile together, so that the short ones fill the
-    // tail (8,192 tokens: 723 -> 650 us).  Whole partitions are alike, and stay in their order.
+    // tail.  Whole partitions are alike, and stay in their order.
     const int at = lc / ny, y = lc % ny, x = L < total_full ? at : nfull + nc - 1 - at;
     const int4 item = p.work[x];
     const int r = item.x, row0 = item.y, z = item.z;
@@ -628,7 +640,7 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
           }
           // The tensor core's queue is short: a wait hides behind the long products of PV(i), not behind
           // the short ones of S.  So the next chunk's waits come between the two; the one for P(i + 1)
-          // too where S runs far enough ahead of it (one row tile: 962 -> 860 cycles a chunk).
+          // too where S runs far enough ahead of it (one row tile).
           auto ready = [&](int i) {
             const int gi = g0 + i;
             // the last chunk's V is read only after the row tile that zeroes its end has done so

@@ -2,7 +2,7 @@
 output may be from the oracle's.
 
 Tolerances count roundings.  u is half a step of the type that the maps' weights are rounded to for
-their product with V (2^-8 bf16, 2^-11 f16; 0 where they stay fp32).  For a row with n keys,
+their product with V (2^-8 bf16, 2^-11 f16; 0 where they stay fp32; single-token rows keep more).  For a row with n keys,
 A = A_1 + |lambda| A_2 (A_j: map j's weighted sum of |value|) and R the largest sum of scale |q_i k_i|:
 a score of d fp32 products and sums is off by (d + 4) 2^-24 R, its exponential by as much and 2^-21
 relative (argument and exponential), each sum over keys by n 2^-24 at most; numerator and denominator

@@ -119,7 +119,7 @@ def test_refusals(pa, fn):
     for kw in (dict(out=F + (1 << 20)), dict(out=F + (1 << 20) - 16), dict(out=F + (2 << 20) + 4096), dict(out=F + (3 << 20)),
                dict(out=F + (9 << 20)), dict(norm=F + 16), dict(out=F + (16 << 20) + 256)):
         assert fn(pa, **kw) == bad, kw
-    for kw in (dict(d=264), dict(qd=3), dict(kd=1), dict(kd=99), dict(kd=7, d=24, ks=F, vs=F), dict(ls=1 << 61),
+    for kw in (dict(longest=(1 << 30) + 1), dict(part=(1 << 30) + 16), dict(hq=131072, hkv=2), dict(d=264), dict(qd=3), dict(kd=1), dict(kd=99), dict(kd=7, d=24, ks=F, vs=F), dict(ls=1 << 61),
                dict(lh=1 << 61)):
         assert fn(pa, **kw) == no, kw
     assert fn(pa, ws=F + (16 << 20) + 16) == small

@@ -226,6 +226,68 @@ def test_bad_tables_and_lengths(pa, kv, qd, bs):
     assert bool((c.out == 9.0).all())
 
 
+@pytest.mark.parametrize("kv,d", [("f32", 64), ("bf16", 128), ("bf16", 96)])
+def test_a_request_longer_than_told(pa, kv, d):
+    """More new tokens than max_query_len: flagged, and the other requests' rows are what they are without it."""
+    c = Diff([90, 500, 300, 7], [40, 20, 1, 1], 8, 4, d, 16, kv, seed=21)
+    c.to_device()
+    c.b.__class__.max_query_len, keep = property(lambda b: 30), c.b.__class__.max_query_len
+    try:
+        c.call(pa, True, 64)
+    finally:
+        c.b.__class__.max_query_len = keep
+    assert pa.pa_get_error_flags(clear=True) == pa.PA_ERRFLAG_QUERY
+    rows = set(range(40, 62))
+    c.check(rows=rows)
+    assert bool((c.out[:40] == 9.0).all()) or not bool(c.out[:40].any())     # left, or zero
+
+
+def test_two_streams_at_once(pa):
+    """Mixed batches on two streams, each call with a workspace of its own and the side stream between
+    them, give what they give one after the other."""
+    cs = [Diff([700, 90, 33, 400], [200, 1, 33, 1], 16, 4, 128, 16, kv, per_token=True, seed=22 + i)
+          for i, kv in enumerate(("bf16", "f16", "bf16"))]
+    for c in cs:
+        c.to_device()
+        c.ws = c.workspace(pa, True)
+    want = [c.call(pa, True, ws=c.ws).clone() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for c in cs:
+        c.out.fill_(9.0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cs, streams):
+            c.call(pa, True, ws=c.ws, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cs, want):
+        assert torch.equal(c.out, w)
+    assert pa.pa_get_error_flags(clear=True) == 0
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_batches_of_any_shape(pa, seed):
+    """Shapes, lengths, windows and options drawn at random, both calls."""
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([64, 128]))
+    kv = str(rng.choice(["bf16", "f16", "fp8_e4m3", "fp8_e5m2"] if d == 128 else ["bf16", "f16"]))
+    qd = str(rng.choice(["bf16", "f16"])) if kv[:3] == "fp8" else None
+    hkv = 2 * int(rng.integers(1, 5))
+    hq = hkv * int(rng.integers(1, 10))
+    n = int(rng.integers(1, 9))
+    new = [int(rng.choice([0, 1, 1, 2, 17, 63, 64, 65, 128, 200])) for _ in range(n)]
+    if not sum(new):
+        new[0] = 1
+    lens = [max(1, q + int(rng.choice([0, 0, 1, 15, 16, 100, 700]))) for q in new]
+    c = Diff(lens, new, hq, hkv, d, int(rng.choice([16, 32, 64])), kv, qd, int(rng.choice([0, 0, 0, 1, 16, 77])),
+             bool(rng.integers(2)), bool(rng.integers(2)), seed)
+    poison(c)
+    c.to_device()
+    c.call(pa, True, int(rng.choice([0, 0, 64, 128])))
+    assert pa.pa_get_error_flags(clear=True) == 0
+    c.check()
+
+
 @pytest.mark.parametrize("varlen", [False, True])
 def test_streams_graphs_and_workspaces(pa, varlen):
     """Another stream; a workspace full of NaN; two graphs that share it, replayed in turn, each on
