@@ -27,7 +27,7 @@
 //
 // Measured (GB300, 32/8 heads of 128 bf16): 8,192 tokens 643 us, 1,280 TFLOP/s, at the card's power
 // limit (1,370 W, 1,957 MHz); of a tile's time 17 to 24% are the two ends of its maps, where the
-// tensor core waits: 128 KB of sums through 32 bytes a cycle.  An FP8 cache 880 TFLOP/s (widening),
+// tensor core waits: 128 KB of sums through 32 bytes a cycle.  An FP8 cache 950 TFLOP/s (widening),
 // head_size 64 950 TFLOP/s (softmax).
 //
 // P is rounded to 16 bits, as in every tile of this kind: an output is then off by 2.6 10^-3 of its
@@ -65,13 +65,13 @@ struct DiffTc {
   static constexpr int kKBytes = kPieces * kPiece;           // keys of a chunk
   static constexpr int kVBytes = 2 * kKBytes;                // values of a chunk
   static constexpr int kKStages = F8 ? 3 : HEAD == 128 ? 4 : 5;
-  static constexpr int kVStages = F8 ? 2 : HEAD == 128 ? 4 : 5;
+  static constexpr int kVStages = F8 ? 3 : HEAD == 128 ? 4 : 5;
   static constexpr int kQPiece = kRows * 128;
   static constexpr int kQTile = kPieces * kQPiece;           // of one map
   static constexpr int kKOff = kTurns ? 0 : kTiles * 2 * kQTile;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
   // FP8: codes land in staging rings, K [block][token][head_size bytes], V [block][half][token][..]
-  static constexpr int kStg = F8 ? 3 : 0;
+  static constexpr int kStg = F8 ? 2 : 0;
   static constexpr int kStgBlock = BS * HEAD;
   static constexpr int kStgTensor = kBlocks * kStgBlock;
   static constexpr int kStgKOff = kVOff + kVStages * kVBytes;
