@@ -638,8 +638,10 @@ cudaError_t launch_varlen_plan(const AttnParams& p, int32_t* part_off, int4* wor
   args.plan_ok = const_cast<int32_t*>(p.plan_ok);
   args.max_work = max_work;
   args.tile_tokens = tile_tokens;
-  if (early) return launch_early<PlanArgs>(varlen_plan_kernel, dim3(1), 1024, 0, 1, args, stream);
-  varlen_plan_kernel<<<1, 1024, 0, stream>>>(args);
+  // no more threads than requests: its barriers take longer the more warps meet there
+  const int threads = p.num_seqs >= 1024 ? 1024 : (p.num_seqs + 127) / 128 * 128;
+  if (early) return launch_early<PlanArgs>(varlen_plan_kernel, dim3(1), threads, 0, 1, args, stream);
+  varlen_plan_kernel<<<1, threads, 0, stream>>>(args);
   return cudaGetLastError();
 }
 

@@ -11,7 +11,9 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kGenericWarps = 8;
+// Warps of a generic CTA: 256 keys in one or two rounds of them (N pairs of output elements a lane).
+template <int N>
+constexpr int generic_warps() { return N <= 4 ? 16 : 8; }
 
 struct DiffGenericArgs {
   DiffParams p;
@@ -30,7 +32,7 @@ __device__ __forceinline__ float2 kv_pair(const KvRow& r, int e) {
   }
 }
 
-// One CTA a (query row, head, partition); its eight warps deal the keys out in groups of kKeys.  Of a
+// One CTA a (query row, head, partition); its warps deal the keys out in groups of kKeys.  Of a
 // group, eight lanes share a key's dot products, four keys at once; then lane i adds elements
 // 64 k + 2 i and the next of the value rows, which were fetched before the scores were known, to both
 // maps' sums.  The warps' states meet in shared memory, so that a context of one partition (256 tokens
@@ -41,9 +43,9 @@ __device__ __forceinline__ float2 kv_pair(const KvRow& r, int e) {
 // 11.9 us, where a warp a head that took the keys one after the other in partitions of 64, and a second
 // launch to join them, took 61.
 template <int QDT, int KVDT, int N>
-__global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const DiffGenericArgs args) {
+__global__ void __launch_bounds__(32 * generic_warps<N>()) diff_generic_kernel(const DiffGenericArgs args) {
   using QE = Elem<QDT>;
-  constexpr int kKeys = 32 / N;
+  constexpr int kKeys = 32 / N, kWarps = generic_warps<N>();
   const DiffParams& p = args.p;
   const AttnParams& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
   if (!diff_row_ok(a, ri)) {
     if (z == 0) {
       typename QE::T* out = static_cast<typename QE::T*>(a.out) + ((long long)row * heads + head) * width;
-      for (int i = threadIdx.x; i < width; i += 32 * kGenericWarps) out[i] = QE::from_float(0.f);
+      for (int i = threadIdx.x; i < width; i += 32 * kWarps) out[i] = QE::from_float(0.f);
       if (threadIdx.x == 0 && a.query_start_loc == nullptr) flag_error(a.err, PA_ERRFLAG_SEQ_LEN);
     }
     return;
@@ -66,11 +68,12 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
   const int kvh = head / a.group * 2;
   const int t0 = max(ri.origin + z * ri.part, ri.lo), t1 = min(ri.origin + (z + 1) * ri.part, ri.kv_len);
   __shared__ float sq[2][64 * N];
-  __shared__ float red[kGenericWarps][2][64 * N];
-  __shared__ float2 red_ml[kGenericWarps][2];
+  __shared__ float red[kWarps][2][64 * N];
+  __shared__ float2 red_ml[kWarps][2];
   const typename QE::T* qrow = static_cast<const typename QE::T*>(a.q) + ((long long)row * a.num_q_heads + 2 * head) * d;
-  for (int i = threadIdx.x; i < width; i += 32 * kGenericWarps) sq[i >= d][i >= d ? i - d : i] = QE::load(qrow + i);
+  for (int i = threadIdx.x; i < width; i += 32 * kWarps) sq[i >= d][i >= d ? i - d : i] = QE::load(qrow + i);
   __syncthreads();
+  const float lam = diff_lambda(p, row, head);  // on its way before it is needed
   float c[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < N; ++k) acc[0][k] = acc[1][k] = make_float2(0.f, 0.f);
-  for (int tb = t0 + warp * kKeys; tb < t1; tb += kGenericWarps * kKeys) {
+  for (int tb = t0 + warp * kKeys; tb < t1; tb += kWarps * kKeys) {
     // lane i of the first kKeys holds where key tb + i lies
     const int mine = tb + lane;
     long long my_tile = -1;
@@ -196,10 +199,10 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
   for (int j = 0; j < 2; ++j) {
     m[j] = -INFINITY;
     l[j] = 0.f;
-    for (int v = 0; v < kGenericWarps; ++v) combine_ml(m[j], l[j], red_ml[v][j].x, red_ml[v][j].y);
+    for (int v = 0; v < kWarps; ++v) combine_ml(m[j], l[j], red_ml[v][j].x, red_ml[v][j].y);
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[j][k] = make_float2(0.f, 0.f);
-    for (int v = 0; v < kGenericWarps; ++v) {
+    for (int v = 0; v < kWarps; ++v) {
       const float2 ml = red_ml[v][j];
       const float f = ml.y > 0.f ? exp2f(ml.x - m[j]) : 0.f;
 #pragma unroll
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(32 * kGenericWarps) diff_generic_kernel(const 
     }
   }
   if (ri.parts_row == 1) {
-    const float w0 = diff_weight(l[0]), w1 = diff_weight(l[1]) * diff_lambda(p, row, head);
+    const float w0 = diff_weight(l[0]), w1 = diff_weight(l[1]) * lam;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       acc[0][k].x = acc[0][k].x * w0 - acc[1][k].x * w1;
@@ -273,6 +276,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
   const long long base = row_partial_base(a, ri, row);
   const int hq = a.num_q_heads;
   const float2* ml = a.ws_ml + base * hq + 2 * head;
+  const float lam = diff_lambda(p, row, head);
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   for (int z = lane; z < np; z += 32) {
     const float4 v = *reinterpret_cast<const float4*>(ml + (long long)z * hq);
@@ -287,16 +291,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
     }
   }
   // weights of the difference: 1 / l1 and -lambda / l2
-  const float f0 = diff_weight(l[0]), f1 = -diff_weight(l[1]) * diff_lambda(p, row, head);
+  const float f0 = diff_weight(l[0]), f1 = -diff_weight(l[1]) * lam;
   float2 o[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) o[k] = make_float2(0.f, 0.f);
   const float* acc = a.ws_acc + (base * hq + 2 * head) * width;
-  for (int z0 = part; z0 < np; z0 += 2 * kWarps) {
-    float2 x[2][2][N];
-    float w[2][2];
+  constexpr int kAhead = N == 8 ? 2 : 4;  // partitions whose loads are on their way together
+  for (int z0 = part; z0 < np; z0 += kAhead * kWarps) {
+    float2 x[kAhead][2][N];
+    float w[kAhead][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       const int z = z0 + u * kWarps;
       const bool in = z < np;
       const float4 v = in ? *reinterpret_cast<const float4*>(ml + (long long)z * hq)
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
         }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -346,10 +351,11 @@ cudaError_t launch_generic_t(const DiffParams& p, int grid_z, int only_multi, cu
   args.p = p;
   args.only_multi_token = only_multi;
   const dim3 grid(p.a.num_rows, p.a.num_q_heads / 2, grid_z);
-  const int threads = 32 * kGenericWarps;
-  if (p.a.head_size <= 64) return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 2>, grid, threads, 0, 1, args, s);
-  if (p.a.head_size <= 128) return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 4>, grid, threads, 0, 1, args, s);
-  return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 8>, grid, threads, 0, 1, args, s);
+  if (p.a.head_size <= 64)
+    return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 2>, grid, 32 * generic_warps<2>(), 0, 1, args, s);
+  if (p.a.head_size <= 128)
+    return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 4>, grid, 32 * generic_warps<4>(), 0, 1, args, s);
+  return launch_early<DiffGenericArgs>(diff_generic_kernel<QDT, KVDT, 8>, grid, 32 * generic_warps<8>(), 0, 1, args, s);
 }
 
 // Single-token rows may have many partitions: eight warps a head then.  Rows of chunks have few, and
