@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import workloads
 from tests.diff_harness import Diff
 
@@ -226,6 +227,34 @@ def test_bad_tables_and_lengths(pa, kv, qd, bs):
     assert bool((c.out == 9.0).all())
 
 
+def growing(c):
+    """Keys whose magnitude grows along every sequence, from a fifth to ten times: the maxima rise chunk
+    after chunk by far more than the slack within which sums are not rescaled."""
+    b = c.b
+    factor = np.ones((b.num_blocks, b.block_size))
+    for r, n in enumerate(b.seq_lens):
+        pos = np.arange(int(n))
+        factor[b.block_tables[r, pos // b.block_size], pos % b.block_size] = 0.2 + 10 * pos / int(n)
+    k = oracle.decode_bits(b.k_cache, b.kv_dtype, b.k_scale) * factor[:, None, :, None]
+    b.k_cache = workloads._cast_bits(torch.from_numpy(k.astype(np.float32)), b.kv_dtype, b.k_scale)
+
+
+@pytest.mark.parametrize("kv,qd,hq,d,bs", [
+    ("bf16", None, 16, 128, 16), ("f16", None, 16, 128, 32), ("bf16", None, 40, 128, 64), ("f16", None, 16, 64, 16),
+    ("bf16", None, 8, 64, 64), ("fp8_e4m3", "bf16", 16, 128, 16), ("fp8_e5m2", "f16", 64, 128, 32), ("f32", None, 8, 64, 16)])
+@pytest.mark.parametrize("part", [0, 128])
+def test_maxima_that_rise(pa, kv, qd, hq, d, bs, part):
+    for new in ([1, 1, 1], [300, 1, 90], [129, 40, 600]):
+        c = Diff([900, 333, 600], new, hq, 4, d, bs, kv, qd, seed=31, cache_scale=0.25 if kv[:3] == "fp8" else None)
+        growing(c)
+        c.to_device()
+        for varlen in (True, False) if max(new) == 1 else (True,):
+            c.out.fill_(9.0)
+            c.call(pa, varlen, part)
+            c.check()
+    assert pa.pa_get_error_flags(clear=True) == 0
+
+
 @pytest.mark.parametrize("kv,d", [("f32", 64), ("bf16", 128), ("bf16", 96)])
 def test_a_request_longer_than_told(pa, kv, d):
     """More new tokens than max_query_len: flagged, and the other requests' rows are what they are without it."""
@@ -348,8 +377,6 @@ def test_cache_behind_2_to_32_elements(pa):
 
 def test_a_layer_step(pa):
     """Rotary write on several axes, then differential attention on what it wrote, in one graph."""
-    import oracle
-
     c = Diff([130, 40, 300], [1, 40, 60], 16, 4, 128, 16, "bf16", seed=15)
     b = c.b
     c.to_device()
