@@ -13,8 +13,8 @@
 //
 // Bound by memory: the bytes of K and V.  What counts is bytes on their way: units of 16 KB, two a warp,
 // two warps a CTA, three CTAs an SM (192 KB).  Measured on the card's 6.7 TB/s (copy): 64 rows of 512 to
-// 4,096 tokens, 32/8 heads of 128 bf16, 103 us, 5.8 TB/s with the joining of the partitions (5 us); 3
-// rows of 131,072, 64/8 heads f16, 223 us, 6.3 TB/s; 256 rows of a 4,096-token window on an e4m3 cache
+// 4,096 tokens, 32/8 heads of 128 bf16, 102 us, 5.9 TB/s with the joining of the partitions; 3 rows of
+// 98,304 to 131,072, 64/8 heads f16, 220 us, 6.4 TB/s; 256 rows of a 4,096-token window on an e4m3 cache
 // 328 us, 6.3 TB/s.  16% of the issue slots, so the second product of each weight (see kSplit) takes
 // nothing: 102.9 and 103.3 us without and with it.
 #include "diff.cuh"

@@ -40,8 +40,8 @@ __device__ __forceinline__ float2 kv_pair(const KvRow& r, int e) {
 //
 // Latency is what bounds the calls that come here (table, rows, two sums over the warp, the meeting):
 // loads are in flight together, 64 registers of values a lane.  4 fp32 sequences of 17 to 200 tokens:
-// 11.9 us, where a warp a head that took the keys one after the other in partitions of 64, and a second
-// launch to join them, took 61.
+// 8.9 us (11.9 with eight warps, two rounds of keys), where a warp a head that took the keys one after
+// the other in partitions of 64, and a second launch to join them, took 61.
 template <int QDT, int KVDT, int N>
 __global__ void __launch_bounds__(32 * generic_warps<N>()) diff_generic_kernel(const DiffGenericArgs args) {
   using QE = Elem<QDT>;
