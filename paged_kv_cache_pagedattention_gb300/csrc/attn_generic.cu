@@ -544,12 +544,28 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const PlanArgs args) 
     __syncthreads();
     // a warp writes a request's tiles, partition-major: the row tiles that read one partition are
     // listed (and so claimed) one after another, and read its K/V from L2 while it is there
-    for (int q = wid; q < num_listed; q += nw) {
+    // (several warps in turn where there are more of them than requests)
+    const int share = max(1, nw / max(1, num_listed));
+    for (int q = wid / share; q < num_listed; q += nw / share) {
       const int lr = listed[q].x;
       int kf = listed[q].y, kl = listed[q].z;
       const RequestPlan lp = plan_request(p, lr, tile_tokens);
       const int row0 = p.query_start_loc[lr], tiles = ceil_div_dev(lp.q_len, tile_tokens);
       const int np_max = tile_partitions(p, lp, (tiles - 1) * tile_tokens, tile_tokens);  // the most any row tile has
+      if (tiles <= 32) {  // one tile a lane; what the partitions below list is a sum over the tiles
+        const int t0 = lane * tile_tokens;
+        const int np = lane < tiles ? tile_partitions(p, lp, t0, tile_tokens) : 0;
+        for (int z = wid % share; z < np_max; z += share) {
+          const int kf_z = kf + __reduce_add_sync(0xffffffffu, min(max(np - 1, 0), z));
+          const int kl_z = kl + __popc(__ballot_sync(0xffffffffu, np > 0 && np <= z));
+          const unsigned whole = __ballot_sync(0xffffffffu, z + 1 < np), last = __ballot_sync(0xffffffffu, z + 1 == np);
+          const unsigned below = (1u << lane) - 1;
+          const int k = z + 1 < np ? kf_z + __popc(whole & below) : kl_z + __popc(last & below);
+          if (z < np && k < max_work) work[k] = make_int4(lr, row0 + t0, z, 0);
+        }
+        continue;
+      }
+      if (wid % share) continue;
       for (int z = 0; z < np_max; ++z) {
         for (int tb = 0; tb < tiles; tb += 32) {
           const int t0 = (tb + lane) * tile_tokens;

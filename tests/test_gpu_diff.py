@@ -271,6 +271,22 @@ def test_a_request_longer_than_told(pa, kv, d):
     assert bool((c.out[:40] == 9.0).all()) or not bool(c.out[:40].any())     # left, or zero
 
 
+@pytest.mark.parametrize("d,heads", [(128, 16), (64, 8)])
+@pytest.mark.parametrize("lens,new", [
+    ([900, 333], [130, 333]),                                   # two requests, two warps of the plan each
+    ([1500, 700, 640], [1300, 33, 2]),                          # more than 32 tiles beside a few
+    ([400, 64, 2100, 77, 1200], [399, 64, 40, 2, 1100]),        # more requests than warps
+])
+def test_tiles_of_split_requests(pa, lens, new, d, heads):
+    """Every tile over every partition is listed once, for few tiles and for many."""
+    c = Diff(lens, new, heads, 4, d, 16, "bf16", seed=sum(new))
+    poison(c)
+    c.to_device()
+    c.call(pa, True, 64)
+    assert pa.pa_get_error_flags(clear=True) == 0
+    c.check()
+
+
 def test_two_streams_at_once(pa):
     """Mixed batches on two streams, each call with a workspace of its own and the side stream between
     them, give what they give one after the other."""
