@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) diff_merge_ke
   const int part = kWarps == 1 ? 0 : warp;  // this warp's place among its head's
   previous_done();
   if (item >= (long long)(args.single ? a.num_seqs : a.num_rows) * heads || plan_rejected(a)) return;
+  if (a.query_start_loc && !a.plan_ok && (a.query_start_loc[0] != 0 || a.query_start_loc[1] != a.num_rows)) return;
   int row = static_cast<int>(item / heads);
   const int head = static_cast<int>(item % heads);
   if (args.single && a.query_start_loc) {

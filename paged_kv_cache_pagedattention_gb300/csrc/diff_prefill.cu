@@ -278,6 +278,15 @@ __device__ __forceinline__ bool mbar_test3(uint64_t* a, uint32_t pa, uint64_t* b
 // All 256 softmax threads.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// One request without a plan: whether its starts or lengths are out of range (flagged by one thread).
+__device__ __forceinline__ bool alone_rejected(const AttnParams& p, bool flags) {
+  const int q0 = p.query_start_loc[0], q_len = p.query_start_loc[1] - q0, seq_len = p.seq_lens[0];
+  const bool query = q0 != 0 || q_len != p.num_rows || q_len > p.max_query_len || q_len > seq_len;
+  const bool length = seq_len > p.max_seq_len || (long long)seq_len > (long long)p.max_blocks_per_seq * p.block_size;
+  if (flags && (query || length)) flag_error(p.err, query ? PA_ERRFLAG_QUERY : PA_ERRFLAG_SEQ_LEN);
+  return query || length;
+}
+
 struct DiffPrefillArgs {
   DiffParams p;
   CUtensorMap tk, tv;
@@ -373,11 +382,25 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     for (int i = tid; i < G::kWide; i += G::kThreads) reinterpret_cast<float*>(s_norm)[i] = args.p.norm_weight[i];
   const int num_groups = (p.group + 7) / 8;
   const int ny = p.num_kv_heads / 2 * num_groups;
-  const bool rejected = plan_rejected(p);
-  const int nwork = rejected ? 0 : *p.work_count;
-  const int nfull = rejected ? 0 : *p.work_full;
+  int gp = 1;
+  while (gp < min(p.group, 8)) gp <<= 1;
+  const int tile_tokens = kRows / gp;
+  // One request of few tiles has no plan: each CTA takes the item of its own number.
+  const bool alone = p.work == nullptr;
+  const bool rejected = alone ? alone_rejected(p, blockIdx.x == 0 && tid == 0) : plan_rejected(p);
+  int nwork = 0, nfull = 0, alone_parts = 1;
+  if (!rejected) {
+    if (alone) {
+      const int q_len = p.num_rows, origin = window_origin(p, p.seq_lens[0], q_len);
+      alone_parts = (p.seq_lens[0] - origin + p.part_pf - 1) / p.part_pf;
+      nwork = (q_len + NT * tile_tokens - 1) / (NT * tile_tokens) * alone_parts;
+    } else {
+      nwork = *p.work_count;
+      nfull = *p.work_full;
+    }
+  }
   const int total = nwork * ny, total_full = nfull * ny;
-  if (tid == 0) s_next = rejected ? 0 : atomicAdd(p.work_claim, 1);
+  if (tid == 0) s_next = alone ? blockIdx.x : rejected ? 0 : atomicAdd(p.work_claim, 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -396,14 +419,11 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     // are claimed from the end on, all KV groups of a tile together, so that the short ones fill the
     // tail.  Whole partitions are alike, and stay in their order.
     const int at = lc / ny, y = lc % ny, x = L < total_full ? at : nfull + nc - 1 - at;
-    const int4 item = p.work[x];
+    const int4 item = alone ? make_int4(0, x / alone_parts * NT * tile_tokens, x % alone_parts, 0) : p.work[x];
     const int r = item.x, row0 = item.y, z = item.z;
     const int g = y / num_groups, hg = y % num_groups, kvh = 2 * g;
     const int h0 = g * p.group + hg * 8;
     const int nh = min(8, p.group - hg * 8);
-    int gp = 1;
-    while (gp < min(p.group, 8)) gp <<= 1;
-    const int tile_tokens = kRows / gp;
     const int qs = p.query_start_loc[r];
     const int q_len = p.query_start_loc[r + 1] - qs;
     const int seq_len = p.seq_lens[r];
@@ -414,6 +434,10 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     const int origin = window_origin(p, seq_len, q_len);
     const int parts_req = (seq_len - origin + part - 1) / part;
     const int k0 = origin + z * part;
+    if (alone && p.causal && k0 >= pos0 + ntok) {  // behind the last key that this tile attends
+      L += gridDim.x;
+      continue;
+    }
     const int klo = p.window > 0 ? max(k0, max(0, pos0 - p.window + 1) / BS * BS) : k0;
     auto tile_chunks = [&](int t) {
       const int nt = min(ntok, (t + 1) * tile_tokens) - t * tile_tokens;
@@ -710,7 +734,8 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
       const bool write = row_valid && z < parts_row;
       const bool direct = parts_row == 1;
       const int head = h0 + row_head;
-      const long long pi = (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req + z;
+      const long long pi = (alone ? (long long)(t0 + row_tok) * p.max_partitions
+                                  : (long long)p.part_off[r] + (long long)(t0 + row_tok) * parts_req) + z;
       const int col0 = kTurns ? wg * G::kCols : 0;
       uint4* turn = reinterpret_cast<uint4*>(smem + G::kTurnOff + warp * 2048);
       const float lam = write && direct ? diff_lambda(args.p, qs + t0 + row_tok, head) : 0.f;
@@ -953,11 +978,11 @@ __global__ void __launch_bounds__(DiffTc<HEAD, BS, is_fp8<KVDT>()>::kThreads, 1)
     turns += nch > 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) tch[t] += 2 * nch_t[t];
-    if (tid == 0) s_next = atomicAdd(p.work_claim, 1);
+    if (tid == 0 && !alone) s_next = atomicAdd(p.work_claim, 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    L = s_next;
+    L = alone ? L + gridDim.x : s_next;
     if (s_abort) break;
   }
 

@@ -271,6 +271,38 @@ def test_a_request_longer_than_told(pa, kv, d):
     assert bool((c.out[:40] == 9.0).all()) or not bool(c.out[:40].any())     # left, or zero
 
 
+@pytest.mark.parametrize("n,new", [(2, 2), (37, 37), (1000, 37), (700, 300), (513, 513), (4000, 129)])
+@pytest.mark.parametrize("kv,qd,d", [("bf16", None, 128), ("f16", None, 64), ("fp8_e4m3", "bf16", 128)])
+@pytest.mark.parametrize("window,part,causal", [(0, 0, True), (0, 64, True), (100, 64, True), (0, 128, False)])
+def test_one_request_alone(pa, n, new, kv, qd, d, window, part, causal):
+    c = Diff([n], [new], 24, 4, d, 16, kv, qd, window, norm=part != 64, seed=n + window, causal=causal)
+    poison(c)
+    c.to_device()
+    c.call(pa, True, part)
+    assert pa.pa_get_error_flags(clear=True) == 0
+    c.check()
+
+
+def test_one_request_out_of_range(pa):
+    """Starts that do not run to the rows' number, a length out of range: nothing is written."""
+    c = Diff([300], [100], 8, 4, 128, 16, "bf16", seed=23)
+    c.to_device()
+    ws = torch.full_like(c.workspace(pa, True, 64), 0xff)
+    for starts, length, flag in (([0, 99], 300, pa.PA_ERRFLAG_QUERY), ([1, 101], 300, pa.PA_ERRFLAG_QUERY),
+                                 ([0, 100], 99, pa.PA_ERRFLAG_QUERY), ([0, 100], 0, pa.PA_ERRFLAG_QUERY),
+                                 ([0, 100], 301, pa.PA_ERRFLAG_SEQ_LEN), ([0, -5], 300, pa.PA_ERRFLAG_QUERY)):
+        c.db.qsl.copy_(torch.tensor(starts, dtype=torch.int32))
+        c.db.lens.fill_(length)
+        c.out.fill_(9.0)
+        c.call(pa, True, 64, ws)
+        assert pa.pa_get_error_flags(clear=True) == flag
+        assert bool((c.out == 9.0).all())
+    c.db.qsl.copy_(torch.tensor([0, 100], dtype=torch.int32))
+    c.db.lens.fill_(300)
+    c.call(pa, True, 64, ws)
+    c.check()
+
+
 @pytest.mark.parametrize("d,heads", [(128, 16), (64, 8)])
 @pytest.mark.parametrize("lens,new", [
     ([900, 333], [130, 333]),                                   # two requests, two warps of the plan each
