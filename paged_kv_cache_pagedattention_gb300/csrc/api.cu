@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -569,17 +570,46 @@ int window_partition(int part, long long parts, int num_seqs, int hq, int hkv, i
 // the layout has room for.
 int generic_diff_partition(int part, int bs) { return std::max(part, round_up(256, std::max(part, bs))); }
 
-// Chunks of new tokens: partitions so long that the row tiles' states are few, but where there are
-// fewer tiles than SMs the context is split until there are some two items an SM (a chunk of 37
-// tokens on 1,000, the call: 47 us with one partition, 33 with 17).  16,384 tokens at most: a mixed
-// step of chunks on up to 64K takes 1,589 us with them, 1,633 with 8,192 (more states), 1,729 with
-// 32,768 (the last items run alone).
-VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs,
-                                int requested) {
+// Chunks of new tokens: in how many partitions row tiles, fewer than the SMs, share a context.  A chunk's
+// time is that of its rounds of items over the SMs, `span / parts` keys and an item's start and end (as
+// long as some 400 keys) each, and that of writing and joining every partition's states (`state` keys a
+// partition, and the joining's launch).  37 tokens on 8,000 take 152 us with one partition, 24 with one
+// item an SM, 41 with two; 600 on 600 (76 tiles) 28 with one and 36 with two partitions.  Several
+// requests' contexts are taken to be half the longest on average, their items claimed as SMs come free
+// and the last half an item late: 400 tokens each behind 1,075 and 8,600 take 179 us with one partition,
+// 130 with three; 200 each behind 475 to 3,800, eight requests, 105 with one and 146 with two.
+long long diff_chunk_parts(long long tiles, long long span, long long rows, int hq, int d, bool ragged) {
+  const double sms = sm_count();
+  const int rows_a_tile = d == 128 ? 1 : 2;  // a tile of two row tiles takes twice the time a key
+  const double state = std::max(1e-3, (double)rows * hq * 2 * d / (rows_a_tile * 16384.0)), join = 256.0 / rows_a_tile;
+  auto cost = [&](long long parts) {
+    const double item = (double)span / parts + 400.0;
+    const double run = ragged ? std::max(item, tiles * (span / 2 + 200.0 * (parts + 1)) / sms + item / 2)
+                              : std::ceil(tiles * parts / sms) * item;
+    return run + (parts > 1 ? parts * state + join : 0.0);
+  };
+  long long best = 1;
+  for (int rounds = 1; rounds <= (ragged ? 4 : 2); ++rounds) {
+    const long long most = static_cast<long long>(rounds * sms / tiles);
+    const long long parts = std::min(most, static_cast<long long>(std::sqrt(rounds * (double)span / state)) + 1);
+    if (parts > 1 && cost(parts) < cost(best)) best = parts;
+  }
+  return best;
+}
+
+// 16,384 tokens a partition at most: a mixed step of chunks on up to 64K takes 1,589 us with them, 1,633
+// with 8,192 (more states), 1,729 with 32,768 (the last items run alone).
+VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int max_query_len, int hq, int hkv, int d, int max_seq_len,
+                                int bs, int requested) {
   const int tile_tokens = pa::diff_prefill_tile_tokens(hq / hkv, d);
-  const long long tiles = ceil_div(total_q, tile_tokens) * (std::max(2, hkv) / 2) * std::max(1LL, ceil_div(hq / hkv, 8));
-  const long long parts = std::max(1LL, ceil_div(2 * sm_count(), tiles));
+  // as few requests of several tokens as there may be, alike in length
+  const long long chunks = std::clamp<long long>(
+      ceil_div(std::max(0, total_q - num_seqs), std::max(1, max_query_len - 1)), 1, num_seqs);
+  const long long rows = std::max(chunks, total_q - (num_seqs - chunks));
+  const long long tiles = chunks * ceil_div(ceil_div(rows, chunks), tile_tokens) * (std::max(2, hkv) / 2) *
+                          std::max(1LL, ceil_div(hq / hkv, 8));
   const int least = round_up(64, bs);
+  const long long parts = diff_chunk_parts(tiles, max_seq_len, rows, hq, d, chunks > 1);
   const int part = round_up(static_cast<int>(std::min(16384LL, ceil_div(max_seq_len, parts))), least);
   return varlen_layout(num_seqs, total_q, hq, hkv / 2, 2 * d, max_seq_len, bs, requested, tile_tokens,
                        diff_partition(num_seqs, hq, hkv, max_seq_len, bs), part);
@@ -1453,12 +1483,11 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
 size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                      int32_t max_seq_len, int32_t block_size, int32_t partition_size) {
-  (void)max_query_len;
   if (num_seqs < 1 || total_q_tokens < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_size < 1 ||
       max_seq_len < 1 || block_size < 1)
     return 256;
-  return diff_varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size,
-                            partition_size)
+  return diff_varlen_layout(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads, head_size, max_seq_len,
+                            block_size, partition_size)
       .total;
 }
 
@@ -1487,8 +1516,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
                          q_dtype, kv_dtype);
   if (st != PA_OK) return st;
   const int tile_tokens = pa::diff_prefill_tile_tokens(num_q_heads / num_kv_heads, head_size);
-  const VarlenLayout L = diff_varlen_layout(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len,
-                                            block_size, partition_size);
+  const VarlenLayout L = diff_varlen_layout(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads, head_size,
+                                            max_seq_len, block_size, partition_size);
   if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
   if (overlap(out, (size_t)total_q_tokens * num_q_heads * head_size * dtype_bytes(q_dtype), workspace, L.total))
     return PA_ERR_INVALID_ARG;
