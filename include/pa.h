@@ -749,7 +749,9 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
                          pa_stream_t stream);
 
 /* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together, at once
- * on two streams (num_seqs > 1; as there, the first such call on a device comes before any capture). */
+ * on two streams (num_seqs > 1; as there, the first such call on a device comes before any capture).
+ * The workspace size follows every argument, max_query_len too: contexts of few new tokens are split
+ * more finely, so ask for each batch's own size; it is not a bound for smaller batches. */
 size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                      int32_t max_seq_len, int32_t block_size, int32_t partition_size);

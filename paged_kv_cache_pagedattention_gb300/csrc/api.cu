@@ -1560,8 +1560,8 @@ pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, con
   cudaError_t e;
   // One request whose items are at most one an SM needs no plan, each CTA takes its own: 37 tokens on
   // 1,000 take 20.3 us so, 25.1 with a plan.  More of them are claimed as CTAs come free: dealt out in
-  // turn, 37 tokens on 8,000 took 35.5 instead of 40.9 us, but 1,000 new tokens 51.0 instead of 39.1
-  // (a CTA's two items may both be long ones) and 8,192 674 instead of 614.
+  // turn, two an SM, 1,000 new tokens took 51.0 instead of 39.1 us (a CTA's two may both be long ones)
+  // and 8,192 674 instead of 614.
   const long long alone_items =
       ceil_div(total_q_tokens, tile_tokens) * grid_pf * (num_kv_heads / 2) * ceil_div(num_q_heads / num_kv_heads, 8);
   if (num_seqs == 1 && fast_prefill && !single && alone_items <= sm_count()) {
