@@ -449,6 +449,20 @@ __device__ RequestPlan plan_request(const AttnParams& p, int r, int tile_tokens)
   return rp;
 }
 
+// One thread writes its request's tiles, whole ones from kf on and last ones from kl on.
+__device__ void list_tiles(const AttnParams& p, const RequestPlan& rp, int r, int tile_tokens, int kf, int kl,
+                           int4* work, int max_work) {
+  const int row0 = p.query_start_loc[r];
+  for (int z = 0; z < rp.parts; ++z) {
+    for (int t0 = 0; t0 < rp.q_len; t0 += tile_tokens) {
+      const int np = tile_partitions(p, rp, t0, tile_tokens);
+      if (z >= np) continue;
+      const int k = z + 1 < np ? kf++ : kl++;
+      if (k < max_work) work[k] = make_int4(r, row0 + t0, z, 0);
+    }
+  }
+}
+
 // Single CTA.  For each request: validates its query range and computes
 //   part_off[r] = sum over earlier requests of q_len * ceil(seq_len / part_r),
 // the index of its first partial row, and lists its prefill tiles (requests with
@@ -464,6 +478,8 @@ struct PlanArgs {
   int32_t* plan_ok;
   int max_work, tile_tokens;
 };
+
+constexpr int kOwnTiles = 8;  // that a thread writes while a warp takes one turn
 
 __global__ void __launch_bounds__(1024) varlen_plan_kernel(const PlanArgs args) {
   const AttnParams& p = args.p;
@@ -536,15 +552,23 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const PlanArgs args) 
     int ex[3];
     for (int k = 0; k < 3; ++k) ex[k] = carry[k] + (wid ? warp_tot[k][wid - 1] : 0) + sc[k] - v[k];
     if (tid == 0) num_listed = 0;
-    __syncthreads();
+    const int tiles_here = rp.full_tiles + rp.last_tiles;
+    const int busy = __syncthreads_count(tiles_here > 0);
+    // A request's tiles are written partition-major: the row tiles that read one partition are listed
+    // (and so claimed) one after another, and read its K/V from L2 while it is there.  A thread writes its
+    // request's few tiles itself, some 0.1 us each; longer lists are left to the warps, who take them in
+    // turn, some 0.5 to 1 us each.  So a list is long by the turns that the warps would need for all.
+    // The plan of 2,000 requests of 3 tokens: 13 us, 74 where warps write every list; 256 of 4: 9 and 26;
+    // one of 8,192: 10 and 34 where its thread writes it.
     if (r < p.num_seqs) {
       part_off[r] = ex[0];
-      if (rp.full_tiles + rp.last_tiles) listed[atomicAdd(&num_listed, 1)] = make_int3(r, ex[1], full_total + ex[2]);
+      if (tiles_here > kOwnTiles * ceil_div_dev(busy, nw))
+        listed[atomicAdd(&num_listed, 1)] = make_int3(r, ex[1], full_total + ex[2]);
+      else if (tiles_here > 0)
+        list_tiles(p, rp, r, tile_tokens, ex[1], full_total + ex[2], work, max_work);
     }
     __syncthreads();
-    // a warp writes a request's tiles, partition-major: the row tiles that read one partition are
-    // listed (and so claimed) one after another, and read its K/V from L2 while it is there
-    // (several warps in turn where there are more of them than requests)
+    // a warp a list (several of them in turn where there are more than lists)
     const int share = max(1, nw / max(1, num_listed));
     for (int q = wid / share; q < num_listed; q += nw / share) {
       const int lr = listed[q].x;
