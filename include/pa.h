@@ -735,6 +735,9 @@ pa_status pa_varlen_attn_windowed(void* out, const void* q, const void* k_cache,
  * with head_size 128, run on the tensor cores where block_size is a multiple of 16 (chunks: 16, 32
  * or 64); the rest, NVFP4 caches among it, in fp32 without them.  max_seq_len and partition_size up
  * to 2^30, num_q_heads up to 131070.
+ * A workspace size serves every batch of at most as many sequences (and, for the flattened call, new
+ * tokens) and of contexts at most as long as it was asked for, of the same heads, head_size, block_size
+ * and partition_size: a caller sizes one workspace for the largest batch.
  */
 size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t head_size, int32_t max_seq_len, int32_t block_size,
@@ -750,8 +753,7 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
 
 /* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together, at once
  * on two streams (num_seqs > 1; as there, the first such call on a device comes before any capture).
- * The workspace size follows every argument, max_query_len too: contexts of few new tokens are split
- * more finely, so ask for each batch's own size; it is not a bound for smaller batches. */
+ * Contexts of few new tokens are split more finely than those of many; the size holds for either. */
 size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                      int32_t max_seq_len, int32_t block_size, int32_t partition_size);

@@ -539,6 +539,11 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
   return PA_OK;
 }
 
+// (KV group, head group) pairs that work on one row, or row tile.
+long long diff_units(int hq, int hkv) {
+  return std::max(2, hkv) / 2 * std::max(1LL, ceil_div(hq / std::max(1, hkv), 8));
+}
+
 // Single-token rows, `span` keys each at most: partitions for two waves of the decode kernel's CTAs
 // (three an SM) where the rows are few, and their lengths likely alike, else four, which even out
 // ragged rows (3 rows of 131,072 tokens, 12 units: 230 us with 1,024-token partitions, 3.4 waves, 220
@@ -546,9 +551,21 @@ pa_status check_diff_args(const void* out, const void* q, const void* k_cache, c
 // a 4,096-token window, 1,024 units: 352 with two partitions of which one is a block, 330 with two).
 int diff_partition(int num_seqs, int hq, int hkv, int span, int bs) {
   const long long slots = 3LL * sm_count();
-  const long long units = std::max(1LL, (long long)num_seqs * (std::max(2, hkv) / 2) * ceil_div(std::max(1, hq / hkv), 8));
+  const long long units = num_seqs * diff_units(hq, hkv);
   const long long parts = units <= slots / 8 ? 2 * slots / units : ceil_div(4 * slots, units);
   return round_up(static_cast<int>(std::clamp(ceil_div(span, parts), 64LL, 1LL << 20)), bs);
+}
+
+// Partial rows that single-token rows may need with the default partitions: of no batch of fewer sequences
+// or shorter contexts are they more, although its partitions may be finer (n rows are cut into 4 slots / U
+// and fewer than n more parts; no part is below 64 tokens but for the last).
+long long diff_decode_rows(int num_seqs, int hq, int hkv, int span, int bs) {
+  const long long cut = 4 * 3LL * sm_count() / diff_units(hq, hkv) + num_seqs;
+  return std::max(num_seqs * ceil_div(span, 1LL << 20), std::min(num_seqs * ceil_div(span, round_up(64, bs)), cut));
+}
+
+size_t diff_state_bytes(long long rows, int hq, int d) {
+  return align256((size_t)rows * hq * sizeof(float2)) + align256((size_t)rows * hq * 2 * d * sizeof(float));
 }
 
 DecodeLayout diff_decode_layout(int num_seqs, int hq, int hkv, int d, int max_seq_len, int bs, int requested) {
@@ -597,6 +614,15 @@ long long diff_chunk_parts(long long tiles, long long span, long long rows, int 
   return best;
 }
 
+// Partial rows to which chunks are cut at most: all SMs, four times over, with whole tiles.  Where single-token
+// rows are many beside few tokens of chunks, the states of every row would take gigabytes otherwise (1,000
+// decodes beside 4 tokens, 32/8 heads of 128 on 32,768: 76 partitions, 2.5 GB).
+long long diff_chunk_rows_most(int hq, int hkv, int d) {
+  return 4LL * sm_count() * pa::diff_prefill_tile_tokens(hq / hkv, d) / diff_units(hq, hkv);
+}
+
+constexpr long long kDiffChunkPart = 16384;
+
 // 16,384 tokens a partition at most: a mixed step of chunks on up to 64K takes 1,589 us with them, 1,633
 // with 8,192 (more states), 1,729 with 32,768 (the last items run alone).
 VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int max_query_len, int hq, int hkv, int d, int max_seq_len,
@@ -606,13 +632,26 @@ VarlenLayout diff_varlen_layout(int num_seqs, int total_q, int max_query_len, in
   const long long chunks = std::clamp<long long>(
       ceil_div(std::max(0, total_q - num_seqs), std::max(1, max_query_len - 1)), 1, num_seqs);
   const long long rows = std::max(chunks, total_q - (num_seqs - chunks));
-  const long long tiles = chunks * ceil_div(ceil_div(rows, chunks), tile_tokens) * (std::max(2, hkv) / 2) *
-                          std::max(1LL, ceil_div(hq / hkv, 8));
+  const long long tiles = chunks * ceil_div(ceil_div(rows, chunks), tile_tokens) * diff_units(hq, hkv);
   const int least = round_up(64, bs);
-  const long long parts = diff_chunk_parts(tiles, max_seq_len, rows, hq, d, chunks > 1);
-  const int part = round_up(static_cast<int>(std::min(16384LL, ceil_div(max_seq_len, parts))), least);
+  const long long parts = std::min(diff_chunk_parts(tiles, max_seq_len, rows, hq, d, chunks > 1),
+                                   std::max(1LL, diff_chunk_rows_most(hq, hkv, d) / total_q));
+  const int part = round_up(static_cast<int>(std::min(kDiffChunkPart, ceil_div(max_seq_len, parts))), least);
   return varlen_layout(num_seqs, total_q, hq, hkv / 2, 2 * d, max_seq_len, bs, requested, tile_tokens,
                        diff_partition(num_seqs, hq, hkv, max_seq_len, bs), part);
+}
+
+// What holds diff_varlen_layout of every batch of at most as many sequences and tokens and contexts as long:
+// each term is the most that it may be, and grows with every argument.
+size_t diff_varlen_bound(int num_seqs, int total_q, int hq, int hkv, int d, int max_seq_len, int bs) {
+  const long long coarse = ceil_div(max_seq_len, kDiffChunkPart);
+  const long long fine = std::min(ceil_div(max_seq_len, round_up(64, bs)),
+                                  std::max(1LL, 4LL * sm_count() / diff_units(hq, hkv)));
+  const long long chunk_rows = std::max(total_q * coarse, std::min(std::max<long long>(diff_chunk_rows_most(hq, hkv, d), total_q),
+                                                                   total_q * fine));
+  const long long work = chunk_rows / pa::diff_prefill_tile_tokens(hq / hkv, d) + (num_seqs + 1LL) * std::max(coarse, fine);
+  return 256 + align256((size_t)num_seqs * sizeof(int32_t)) + align256((size_t)work * sizeof(int4)) +
+         diff_state_bytes(diff_decode_rows(num_seqs, hq, hkv, max_seq_len, bs) + chunk_rows, hq, d);
 }
 
 bool diff_decode_maps(CUtensorMap* tk, CUtensorMap* tv, const AttnParams& a, int kv_dtype) {
@@ -1415,9 +1454,12 @@ size_t pa_diff_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int3
                                      int32_t head_size, int32_t max_seq_len, int32_t block_size,
                                      int32_t partition_size) {
   if (num_seqs < 1 || num_q_heads < 1 || head_size < 1 || max_seq_len < 1 || block_size < 1) return 256;
-  return diff_decode_layout(num_seqs, num_q_heads, std::max(1, num_kv_heads), head_size, max_seq_len, block_size,
-                            partition_size)
-      .total;
+  num_kv_heads = std::max(1, num_kv_heads);
+  if (partition_size > 0)
+    return diff_decode_layout(num_seqs, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size, partition_size)
+        .total;
+  return 256 + diff_state_bytes(diff_decode_rows(num_seqs, num_q_heads, num_kv_heads, max_seq_len, block_size),
+                                num_q_heads, head_size);
 }
 
 pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const void* v_cache, int32_t num_blocks,
@@ -1486,9 +1528,11 @@ size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, i
   if (num_seqs < 1 || total_q_tokens < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_size < 1 ||
       max_seq_len < 1 || block_size < 1)
     return 256;
-  return diff_varlen_layout(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads, head_size, max_seq_len,
-                            block_size, partition_size)
-      .total;
+  if (partition_size > 0)
+    return diff_varlen_layout(num_seqs, total_q_tokens, max_query_len, num_q_heads, num_kv_heads, head_size,
+                              max_seq_len, block_size, partition_size)
+        .total;
+  return diff_varlen_bound(num_seqs, total_q_tokens, num_q_heads, num_kv_heads, head_size, max_seq_len, block_size);
 }
 
 pa_status pa_diff_varlen_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
