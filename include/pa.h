@@ -753,7 +753,10 @@ pa_status pa_diff_decode(void* out, const void* q, const void* k_cache, const vo
 
 /* The flattened batch of pa_varlen_attn: chunks of new tokens and single-token rows together, at once
  * on two streams (num_seqs > 1; as there, the first such call on a device comes before any capture).
- * Contexts of few new tokens are split more finely than those of many; the size holds for either. */
+ * Contexts of few new tokens are split more finely than those of many; the size holds for either.
+ * A request whose length is out of range, or that is longer than its sequence or max_query_len, sets its
+ * flag; one of a single token gets an all-zero output row, the rows of one of several tokens are left as
+ * they were, as is the whole output where query_start_loc is out of order.  Other requests are unaffected. */
 size_t pa_diff_varlen_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t max_query_len,
                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                      int32_t max_seq_len, int32_t block_size, int32_t partition_size);

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32 * generic_warps<N>()) diff_generic_kernel(c
   if (plan_rejected(a)) return;
   const RowInfo ri = row_info(a, row);
   if (!diff_row_ok(a, ri)) {
-    if (z == 0) {
+    if (z == 0 && ri.q_len == 1) {  // as the tiles, which no such request of several tokens has
       typename QE::T* out = static_cast<typename QE::T*>(a.out) + ((long long)row * heads + head) * width;
       for (int i = threadIdx.x; i < width; i += 32 * kWarps) out[i] = QE::from_float(0.f);
       if (threadIdx.x == 0 && a.query_start_loc == nullptr) flag_error(a.err, PA_ERRFLAG_SEQ_LEN);
