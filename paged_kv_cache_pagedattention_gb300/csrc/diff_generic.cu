@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(32 * generic_warps<N>()) diff_generic_kernel(c
 
   const int kvh = head / a.group * 2;
   const int t0 = max(ri.origin + z * ri.part, ri.lo), t1 = min(ri.origin + (z + 1) * ri.part, ri.kv_len);
-  __shared__ float sq[2][64 * N];
-  __shared__ float red[kWarps][2][64 * N];
+  __shared__ __align__(16) float sq[2][64 * N];            // read four at a time
+  __shared__ __align__(16) float red[kWarps][2][64 * N];   // two
   __shared__ float2 red_ml[kWarps][2];
   const typename QE::T* qrow = static_cast<const typename QE::T*>(a.q) + ((long long)row * a.num_q_heads + 2 * head) * d;
   for (int i = threadIdx.x; i < width; i += 32 * kWarps) sq[i >= d][i >= d ? i - d : i] = QE::load(qrow + i);
