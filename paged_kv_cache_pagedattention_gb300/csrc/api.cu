@@ -549,6 +549,9 @@ long long diff_units(int hq, int hkv) {
 // ragged rows (3 rows of 131,072 tokens, 12 units: 230 us with 1,024-token partitions, 3.4 waves, 220
 // with two waves; 64 rows of 512 to 4,096, 256 units: 103 us with four waves, 112 with two; 256 rows of
 // a 4,096-token window, 1,024 units: 352 with two partitions of which one is a block, 330 with two).
+// 12 to 48 units of contexts alike (32/8 heads of 128): two waves 248 to 252, four 250 to 256; of contexts
+// from an eighth of the longest on, which the host cannot tell from them, 175 to 180 and 157 to 160.  64 to
+// 192 units, alike: 263 to 344 and 250 to 325; ragged: 167 to 225 and 154 to 200.
 int diff_partition(int num_seqs, int hq, int hkv, int span, int bs) {
   const long long slots = 3LL * sm_count();
   const long long units = num_seqs * diff_units(hq, hkv);
@@ -582,7 +585,7 @@ int window_partition(int part, long long parts, int num_seqs, int hq, int hkv, i
   return std::min(part, std::max(diff_partition(num_seqs, hq, hkv, span, bs), least));
 }
 
-// The generic kernel's partitions: its CTAs share a partition among eight warps, so short contexts
+// The generic kernel's partitions: its CTAs share a partition among eight or sixteen warps, so short contexts
 // take one (4 fp32 sequences of 17 to 200 tokens: one launch instead of two).  No more of them than
 // the layout has room for.
 int generic_diff_partition(int part, int bs) { return std::max(part, round_up(256, std::max(part, bs))); }

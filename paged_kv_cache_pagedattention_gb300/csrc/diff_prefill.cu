@@ -25,10 +25,12 @@
 // rows are read 64 columns at a time), and what the ring's copies write there comes on top (1,293
 // cycles a chunk, 906 now in blocks of 16 tokens, 835 of 64).
 //
-// Measured (GB300, 32/8 heads of 128 bf16): 8,192 tokens 643 us, 1,280 TFLOP/s, at the card's power
-// limit (1,370 W, 1,957 MHz); of a tile's time 17 to 24% are the two ends of its maps, where the
-// tensor core waits: 128 KB of sums through 32 bytes a cycle.  An FP8 cache 950 TFLOP/s (widening),
-// head_size 64 950 TFLOP/s (softmax).
+// Measured (GB300, 32/8 heads of 128 bf16): 8,192 tokens 605 to 625 us in a graph, 638 to 647 call by call,
+// 1,275 to 1,365 TFLOP/s, at the card's power limit (1,370 W, 1,957 MHz); of a tile's time 17 to 24% are the
+// two ends of its maps, where the tensor core waits: 128 KB of sums through 32 bytes a cycle.  2 x 1,024
+// tokens on 2K and 16K: 1,255 TFLOP/s, on an e4m3 cache 840 (tensor pipe 31%, issue slots 41%; a chunk's
+// values are widened for each map), with head_size 64 795 (tensor pipe 38%, issue slots 45%, exponentials
+// 25%: no unit's limit, so likely the softmax warps' chain of a chunk, which nothing overlaps).
 //
 // P is rounded to 16 bits, as in every tile of this kind: an output is then off by 2.6 10^-3 of its
 // size where its own bf16 rounding is 1.7 10^-3 (f16: 3.2 10^-4 and 2.1 10^-4).  A second product with
